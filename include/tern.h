@@ -396,6 +396,76 @@ int tern_layer_bwd_dw(const tern_proj_t *projs, int32_t n, int64_t T, int32_t ac
                       size_t workspace_bytes, void *stream);
 
 /*
+ * The gated linear recurrence of a time-mixing layer: what stands between the
+ * receptance / key / value projections and the output projection.  Per channel
+ * of [T, C] activations, over packed sequences,
+ *   w_t = sigmoid(K_t)    h_t = h_{t-1} + w_t (V_t - h_{t-1})    (the state)
+ *   Y_t = sigmoid(R_t) h_t
+ * The key is the write gate: w near 0 keeps the state, near 1 replaces it.
+ *
+ *   K, V, R   [T, C] of act_dtype (TERN_F32 or TERN_BF16) with one row stride
+ *             ld (elements): separate matrices, or column slices of the
+ *             Y_group that one grouped projection writes (tern_group_gather).
+ *   offsets   device int64 [n_seq + 1]: sequence s holds the tokens
+ *             offsets[s] <= t < offsets[s + 1].  Ascending, starting at 0 and
+ *             not above T; equal neighbours are sequences of no tokens.  NULL:
+ *             one sequence of all T tokens (n_seq 1).  Rows from
+ *             offsets[n_seq] on belong to no sequence: nothing is written to
+ *             them.  Offsets that break these rules give unspecified outputs,
+ *             but no access outside the buffers.
+ *   h0        fp32 [n_seq, C], the state each sequence starts from, or NULL
+ *             (zeros).
+ *   T, n_seq, C >= 0, C and every row stride multiples of 8, strides >= C;
+ *   every pointer 16-byte aligned (offsets: 8-byte).  Outputs may be column
+ *   slices of one matrix, but share no element with an input or another
+ *   output (TERN_ERR_ALIAS).
+ * All states, gradients and sums are fp32; Y, dK, dV and dR are rounded once
+ * (nearest even) to act_dtype.  The order of every sum is fixed: repeated
+ * calls are bitwise identical.  Values of one sequence (a NaN among them)
+ * never reach another.
+ *
+ * tern_recur_fwd -- Y [T, C] (row stride ldy).
+ *   hT      fp32 [n_seq, C], the state behind each sequence's last token (h0
+ *           for a sequence of no tokens), or NULL.
+ *   states  checkpoints for the backward, tern_recur_states_bytes(T, C) bytes
+ *           (the state before every TERN_RECUR_BLOCK-th row), or NULL.
+ *   workspace  at least tern_recur_workspace_bytes(T, C) bytes (NULL when that
+ *           is 0), for this call only.
+ *
+ * tern_recur_bwd -- from dY [T, C] (row stride lddy; dy_dtype TERN_F32, as the
+ *   dX of the output projection is, or act_dtype) and dhT (fp32 [n_seq, C],
+ *   the gradient of hT, or NULL: zeros), with g_t the gradient reaching h_t:
+ *   dK = g_t (V_t - h_{t-1}) w_t (1 - w_t),  dV = g_t w_t,
+ *   dR = dY_t h_t sigmoid'(R_t)              [T, C] of act_dtype, stride ldd
+ *   dh0  fp32 [n_seq, C], the gradient of h0 (dhT for a sequence of no
+ *           tokens), or NULL.
+ *   K, V, R, h0 and offsets as given to the forward, states as it wrote them.
+ *
+ * tern_recur_step -- one token of each of `rows` sequences, as a generation
+ *   loop runs it: h_out = h + sigmoid(K) (V - h), Y = sigmoid(R) h_out, on
+ *   K, V, R [rows, C] (stride ld), h and h_out fp32 [rows, C] (h_out may be h:
+ *   the state is then updated in place), Y [rows, C] (stride ldy).
+ *
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, ALIAS, HIP.  The bytes
+ * functions return 0 for invalid sizes.
+ */
+#define TERN_RECUR_BLOCK 16
+size_t tern_recur_states_bytes(int64_t T, int64_t C);
+size_t tern_recur_workspace_bytes(int64_t T, int64_t C);
+int tern_recur_fwd(const void *K, const void *V, const void *R, int64_t ld, int32_t act_dtype,
+                   const float *h0, const int64_t *offsets, int64_t n_seq, int64_t T, int64_t C,
+                   void *Y, int64_t ldy, float *hT, float *states, void *workspace,
+                   size_t workspace_bytes, void *stream);
+int tern_recur_bwd(const void *K, const void *V, const void *R, int64_t ld, int32_t act_dtype,
+                   const float *h0, const int64_t *offsets, int64_t n_seq, int64_t T, int64_t C,
+                   const float *states, const void *dY, int64_t lddy, int32_t dy_dtype,
+                   const float *dhT, void *dK, void *dV, void *dR, int64_t ldd, float *dh0,
+                   void *workspace, size_t workspace_bytes, void *stream);
+int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int32_t act_dtype,
+                    int64_t rows, int64_t C, const float *h, float *h_out, void *Y, int64_t ldy,
+                    void *stream);
+
+/*
  * Graphs of library calls.  The page's trainer launches every glue kernel and
  * GEMM of a step separately and notes that it is launch-bound; a caller can
  * instead record any sequence of the calls above (for example materialize,

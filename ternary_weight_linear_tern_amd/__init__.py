@@ -56,6 +56,13 @@ SIGNATURES = {
     "tern_layer_bwd_dx": (ctypes.c_int, [_vp, _i32, _i64, _i32, _vp]),
     "tern_layer_bwd_dw_workspace_bytes": (_sz, [_vp, _i32, _i64]),
     "tern_layer_bwd_dw": (ctypes.c_int, [_vp, _i32, _i64, _i32, _vp, _sz, _vp]),
+    "tern_recur_states_bytes": (_sz, [_i64, _i64]),
+    "tern_recur_workspace_bytes": (_sz, [_i64, _i64]),
+    "tern_recur_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
+                                      _vp, _sz, _vp]),
+    "tern_recur_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i32,
+                                      _vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "tern_recur_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
     "tern_graph_begin": (ctypes.c_int, [_vp]),
     "tern_graph_end": (ctypes.c_int, [_vp, ctypes.POINTER(_vp)]),
     "tern_graph_launch": (ctypes.c_int, [_vp, _vp]),
@@ -501,6 +508,136 @@ def tern_layer_bwd_dw(projs, workspace, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("tern_layer_bwd_dw", lib().tern_layer_bwd_dw(arr, len(projs), X0.shape[0], _act_code(X0),
                                                        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+RECUR_BLOCK = 16
+
+
+def tern_recur_states_bytes(T: int, C: int) -> int:
+    return int(lib().tern_recur_states_bytes(int(T), int(C)))
+
+
+def tern_recur_workspace_bytes(T: int, C: int) -> int:
+    return int(lib().tern_recur_workspace_bytes(int(T), int(C)))
+
+
+def _rows(fn: str, ts):
+    """Shared row stride (elements) of [rows, cols] tensors whose rows are
+    contiguous: whole matrices, or column slices of a wider one."""
+    for name, t in ts:
+        if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{fn}: the rows of {name} must be contiguous")
+    # the stride of a single row means nothing
+    lds = {t.stride(0) for _, t in ts if t.shape[0] > 1} or {ts[0][1].shape[1]}
+    if len(lds) > 1:
+        names = ", ".join(n for n, _ in ts)
+        raise ValueError(f"{fn}: {names} must share one row stride, got {sorted(lds)}")
+    return lds.pop()
+
+
+def _row_ptr(t):
+    return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() else None
+
+
+def _stream_of(t: torch.Tensor, stream):
+    """The stream handle for a call on t's device: the given stream, or the
+    current stream of that device."""
+    return _stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+
+
+def _recur_checks(fn, K, V, R, h0, offsets):
+    for name, t in (("K", K), ("V", V), ("R", R)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a tensor")
+    if K.dim() != 2:
+        raise ValueError(f"{fn}: K must be [T, C]")
+    T, C = K.shape
+    _need(fn, "K", K, (T, C), _ACT)
+    _need(fn, "V", V, (T, C), (K.dtype,))
+    _need(fn, "R", R, (T, C), (K.dtype,))
+    S = 1
+    if offsets is not None:
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError(f"{fn}: offsets must be a tensor [n_seq + 1]")
+        S = offsets.shape[0] - 1
+        _need(fn, "offsets", offsets, (S + 1,), (torch.int64,))
+    if h0 is not None:
+        _need(fn, "h0", h0, (S, C), _F32)
+    return T, C, S, _rows(fn, [("K", K), ("V", V), ("R", R)])
+
+
+def _bytes_of(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def tern_recur_fwd(K, V, R, Y, workspace, h0=None, offsets=None, hT=None, states=None, stream=None) -> None:
+    """Y = sigmoid(R) h with h_t = h_{t-1} + sigmoid(K_t) (V_t - h_{t-1}), over
+    the packed sequences `offsets` cuts [T, C] into (int64 [n_seq + 1] on the
+    device; None: one sequence).  K, V, R may be column slices of one matrix;
+    hT receives the final states, states the backward's checkpoints."""
+    fn = "tern_recur_fwd"
+    T, C, S, ld = _recur_checks(fn, K, V, R, h0, offsets)
+    _need(fn, "Y", Y, (T, C), (K.dtype,))
+    if hT is not None:
+        _need(fn, "hT", hT, (S, C), _F32)
+    if states is not None:
+        _need_bytes(fn, "states", states, tern_recur_states_bytes(T, C))
+    _need_device(fn, K, V, R, Y, workspace, h0, offsets, hT, states)
+    with torch.cuda.device(K.device):
+        rc = lib().tern_recur_fwd(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), _ptr(h0), _ptr(offsets), S,
+                                  T, C, _row_ptr(Y), _rows(fn, [("Y", Y)]), _ptr(hT), _ptr(states), _ptr(workspace),
+                                  _bytes_of(workspace), _stream_of(K, stream))
+    _check(fn, rc)
+
+
+def tern_recur_bwd(K, V, R, dY, states, dK, dV, dR, workspace, h0=None, offsets=None, dhT=None, dh0=None,
+                   stream=None) -> None:
+    """Gradients of tern_recur_fwd from dY (fp32 or K's dtype) and dhT (the
+    gradient of hT); states as the forward wrote them."""
+    fn = "tern_recur_bwd"
+    T, C, S, ld = _recur_checks(fn, K, V, R, h0, offsets)
+    _need(fn, "dY", dY, (T, C), (torch.float32, K.dtype))
+    for name, t in (("dK", dK), ("dV", dV), ("dR", dR)):
+        _need(fn, name, t, (T, C), (K.dtype,))
+    for name, t in (("dhT", dhT), ("dh0", dh0)):
+        if t is not None:
+            _need(fn, name, t, (S, C), _F32)
+    _need_bytes(fn, "states", states, tern_recur_states_bytes(T, C))
+    _need_device(fn, K, V, R, dY, states, dK, dV, dR, workspace, h0, offsets, dhT, dh0)
+    with torch.cuda.device(K.device):
+        rc = lib().tern_recur_bwd(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), _ptr(h0), _ptr(offsets), S,
+                                  T, C, _ptr(states), _row_ptr(dY), _rows(fn, [("dY", dY)]), _act_code(dY), _ptr(dhT),
+                                  _row_ptr(dK), _row_ptr(dV), _row_ptr(dR),
+                                  _rows(fn, [("dK", dK), ("dV", dV), ("dR", dR)]), _ptr(dh0), _ptr(workspace),
+                                  _bytes_of(workspace), _stream_of(K, stream))
+    _check(fn, rc)
+
+
+def tern_recur_step(K, V, R, h, Y, h_out=None, stream=None) -> None:
+    """One token of each sequence (rows of K, V, R): the state moves from h to
+    h_out (None: in place) and Y = sigmoid(R) h_out."""
+    fn = "tern_recur_step"
+    rows, C, _, ld = _recur_checks(fn, K, V, R, None, None)
+    h_out = h if h_out is None else h_out
+    _need(fn, "h", h, (rows, C), _F32)
+    _need(fn, "h_out", h_out, (rows, C), _F32)
+    _need(fn, "Y", Y, (rows, C), (K.dtype,))
+    _need_device(fn, K, V, R, h, h_out, Y)
+    with torch.cuda.device(K.device):
+        rc = lib().tern_recur_step(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), rows, C, _ptr(h),
+                                   _ptr(h_out), _row_ptr(Y), _rows(fn, [("Y", Y)]), _stream_of(K, stream))
+    _check(fn, rc)
+
+
+def empty_recur_states(T: int, C: int, device="cuda") -> torch.Tensor:
+    """Checkpoints of tern_recur_fwd for tern_recur_bwd: one state row every
+    RECUR_BLOCK tokens."""
+    return torch.empty((-(-T // RECUR_BLOCK), C), dtype=torch.float32, device=device)
+
+
+def empty_recur_workspace(T: int, C: int, device="cuda") -> torch.Tensor:
+    """Workspace of tern_recur_fwd and tern_recur_bwd, either activation type."""
+    return torch.empty((max(tern_recur_workspace_bytes(T, C), 16),), dtype=torch.uint8, device=device)
 
 
 def tern_graph_begin(stream) -> None:

@@ -1,0 +1,43 @@
+// tern_cursor.h -- where a token stands among packed sequences (host and
+// device; no HIP headers, so that it is tested on the CPU).
+#pragma once
+
+#include <stdint.h>
+
+#include "tern_plan.h"
+
+namespace tern {
+
+// cur is the last i in [0, S] with off[i] <= t (-1 before off[0]): the token
+// belongs to sequence cur when 0 <= cur < S.  Offsets that do not ascend are
+// only ever compared with t, so cur stays in [-1, S] and off is read at
+// [0, S] whatever it holds.  off null: one sequence of T tokens.
+struct Cursor {
+    const int64_t *off;
+    int64_t S, T, cur;
+
+    TERN_HD int64_t at(int64_t i) const { return off ? off[i] : i * T; }
+    TERN_HD bool live() const { return cur >= 0 && cur < S; }
+    // first token of the sequence at the cursor, and of what follows it
+    TERN_HD int64_t begin() const { return cur >= 0 ? at(cur) : INT64_MIN; }
+    TERN_HD int64_t end() const { return cur < S ? at(cur + 1) : INT64_MAX; }
+
+    TERN_HD void seek(int64_t t) {
+        int64_t lo = -1, hi = S;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (at(mid) <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        cur = lo;
+    }
+    // to a later / an earlier token
+    TERN_HD void forth(int64_t t) {
+        while (cur < S && at(cur + 1) <= t) cur++;
+    }
+    TERN_HD void back(int64_t t) {
+        while (cur >= 0 && at(cur) > t) cur--;
+    }
+};
+
+}  // namespace tern

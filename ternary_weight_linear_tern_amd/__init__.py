@@ -521,49 +521,93 @@ def tern_recur_workspace_bytes(T: int, C: int) -> int:
     return int(lib().tern_recur_workspace_bytes(int(T), int(C)))
 
 
-def _rows(fn: str, ts):
-    """Shared row stride (elements) of [rows, cols] tensors whose rows are
-    contiguous: whole matrices, or column slices of a wider one."""
-    for name, t in ts:
-        if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{fn}: the rows of {name} must be contiguous")
-    # the stride of a single row means nothing
-    lds = {t.stride(0) for _, t in ts if t.shape[0] > 1} or {ts[0][1].shape[1]}
-    if len(lds) > 1:
-        names = ", ".join(n for n, _ in ts)
-        raise ValueError(f"{fn}: {names} must share one row stride, got {sorted(lds)}")
-    return lds.pop()
+# The calls below run once per generated token, where the host's share of a
+# call is most of its time: each check is first made in its cheapest form, and
+# only a mismatch goes through the helpers above, which word the error.
+
+def _shaped(fn, name, t, shape, dtypes) -> None:
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype not in dtypes:
+        _need(fn, name, t, shape, dtypes)
 
 
-def _row_ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() else None
+def _device_of(fn, t0, *ts) -> int:
+    """Index of the one GPU every tensor (None: not given) lives on."""
+    d = t0.get_device()
+    for t in ts:
+        if t is not None and t.get_device() != d:
+            _need_device(fn, t0, *ts)
+    if d < 0:
+        _need_device(fn, t0, *ts)
+    return d
 
 
-def _stream_of(t: torch.Tensor, stream):
-    """The stream handle for a call on t's device: the given stream, or the
-    current stream of that device."""
-    return _stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+def _addr(t):
+    """Address of a contiguous tensor (None: not given)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libtern must be contiguous")
+    return t.data_ptr()
 
 
-def _recur_checks(fn, K, V, R, h0, offsets):
-    for name, t in (("K", K), ("V", V), ("R", R)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{fn}: {name} must be a tensor")
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """Run an entry point on `stream` (None: the current stream of GPU dev),
+    with dev the current device."""
+    # the raw handle of torch.cuda.current_stream(dev), without building the object
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, s)
+    if rc:
+        raise TernError(fn, rc)
+
+
+def _row_stride(fn: str, name: str, t) -> int:
+    """Row stride (elements) of a [rows, cols] tensor whose rows are
+    contiguous: a matrix, or a column slice of a wider one."""
+    rows, cols = t.shape
+    if rows <= 1:
+        ld = cols          # the stride of a single row means nothing
+    else:
+        ld = t.stride(0)
+    if cols > 1 and rows and t.stride(1) != 1:
+        raise ValueError(f"{fn}: the rows of {name} must be contiguous")
+    return ld
+
+
+def _row_strides(fn: str, names, a, b, c) -> int:
+    """The row stride three [rows, cols] tensors share."""
+    ld = _row_stride(fn, names[0], a)
+    if _row_stride(fn, names[1], b) != ld or _row_stride(fn, names[2], c) != ld:
+        raise ValueError(f"{fn}: {', '.join(names)} must share one row stride")
+    return ld
+
+
+def _recur_inputs(fn, K, V, R):
+    if not isinstance(K, torch.Tensor):
+        raise TypeError(f"{fn}: K must be a tensor")
     if K.dim() != 2:
         raise ValueError(f"{fn}: K must be [T, C]")
-    T, C = K.shape
-    _need(fn, "K", K, (T, C), _ACT)
-    _need(fn, "V", V, (T, C), (K.dtype,))
-    _need(fn, "R", R, (T, C), (K.dtype,))
+    shape = K.shape
+    _shaped(fn, "K", K, shape, _ACT)
+    _shaped(fn, "V", V, shape, (K.dtype,))
+    _shaped(fn, "R", R, shape, (K.dtype,))
+    return shape, _row_strides(fn, ("K", "V", "R"), K, V, R)
+
+
+def _recur_sequences(fn, C, h0, offsets) -> int:
     S = 1
     if offsets is not None:
         if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
             raise ValueError(f"{fn}: offsets must be a tensor [n_seq + 1]")
         S = offsets.shape[0] - 1
-        _need(fn, "offsets", offsets, (S + 1,), (torch.int64,))
+        _shaped(fn, "offsets", offsets, (S + 1,), (torch.int64,))
     if h0 is not None:
-        _need(fn, "h0", h0, (S, C), _F32)
-    return T, C, S, _rows(fn, [("K", K), ("V", V), ("R", R)])
+        _shaped(fn, "h0", h0, (S, C), _F32)
+    return S
 
 
 def _bytes_of(t) -> int:
@@ -576,18 +620,17 @@ def tern_recur_fwd(K, V, R, Y, workspace, h0=None, offsets=None, hT=None, states
     device; None: one sequence).  K, V, R may be column slices of one matrix;
     hT receives the final states, states the backward's checkpoints."""
     fn = "tern_recur_fwd"
-    T, C, S, ld = _recur_checks(fn, K, V, R, h0, offsets)
-    _need(fn, "Y", Y, (T, C), (K.dtype,))
+    (T, C), ld = _recur_inputs(fn, K, V, R)
+    S = _recur_sequences(fn, C, h0, offsets)
+    _shaped(fn, "Y", Y, (T, C), (K.dtype,))
     if hT is not None:
-        _need(fn, "hT", hT, (S, C), _F32)
+        _shaped(fn, "hT", hT, (S, C), _F32)
     if states is not None:
         _need_bytes(fn, "states", states, tern_recur_states_bytes(T, C))
-    _need_device(fn, K, V, R, Y, workspace, h0, offsets, hT, states)
-    with torch.cuda.device(K.device):
-        rc = lib().tern_recur_fwd(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), _ptr(h0), _ptr(offsets), S,
-                                  T, C, _row_ptr(Y), _rows(fn, [("Y", Y)]), _ptr(hT), _ptr(states), _ptr(workspace),
-                                  _bytes_of(workspace), _stream_of(K, stream))
-    _check(fn, rc)
+    dev = _device_of(fn, K, V, R, Y, workspace, h0, offsets, hT, states)
+    _call(fn, dev, stream, K.data_ptr(), V.data_ptr(), R.data_ptr(), ld, _act_code(K), _addr(h0), _addr(offsets), S,
+          T, C, Y.data_ptr(), _row_stride(fn, "Y", Y), _addr(hT), _addr(states), _addr(workspace),
+          _bytes_of(workspace))
 
 
 def tern_recur_bwd(K, V, R, dY, states, dK, dV, dR, workspace, h0=None, offsets=None, dhT=None, dh0=None,
@@ -595,38 +638,34 @@ def tern_recur_bwd(K, V, R, dY, states, dK, dV, dR, workspace, h0=None, offsets=
     """Gradients of tern_recur_fwd from dY (fp32 or K's dtype) and dhT (the
     gradient of hT); states as the forward wrote them."""
     fn = "tern_recur_bwd"
-    T, C, S, ld = _recur_checks(fn, K, V, R, h0, offsets)
-    _need(fn, "dY", dY, (T, C), (torch.float32, K.dtype))
+    (T, C), ld = _recur_inputs(fn, K, V, R)
+    S = _recur_sequences(fn, C, h0, offsets)
+    _shaped(fn, "dY", dY, (T, C), (torch.float32, K.dtype))
     for name, t in (("dK", dK), ("dV", dV), ("dR", dR)):
-        _need(fn, name, t, (T, C), (K.dtype,))
+        _shaped(fn, name, t, (T, C), (K.dtype,))
     for name, t in (("dhT", dhT), ("dh0", dh0)):
         if t is not None:
-            _need(fn, name, t, (S, C), _F32)
+            _shaped(fn, name, t, (S, C), _F32)
     _need_bytes(fn, "states", states, tern_recur_states_bytes(T, C))
-    _need_device(fn, K, V, R, dY, states, dK, dV, dR, workspace, h0, offsets, dhT, dh0)
-    with torch.cuda.device(K.device):
-        rc = lib().tern_recur_bwd(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), _ptr(h0), _ptr(offsets), S,
-                                  T, C, _ptr(states), _row_ptr(dY), _rows(fn, [("dY", dY)]), _act_code(dY), _ptr(dhT),
-                                  _row_ptr(dK), _row_ptr(dV), _row_ptr(dR),
-                                  _rows(fn, [("dK", dK), ("dV", dV), ("dR", dR)]), _ptr(dh0), _ptr(workspace),
-                                  _bytes_of(workspace), _stream_of(K, stream))
-    _check(fn, rc)
+    dev = _device_of(fn, K, V, R, dY, states, dK, dV, dR, workspace, h0, offsets, dhT, dh0)
+    _call(fn, dev, stream, K.data_ptr(), V.data_ptr(), R.data_ptr(), ld, _act_code(K), _addr(h0), _addr(offsets), S,
+          T, C, _addr(states), dY.data_ptr(), _row_stride(fn, "dY", dY), _act_code(dY), _addr(dhT), dK.data_ptr(),
+          dV.data_ptr(), dR.data_ptr(), _row_strides(fn, ("dK", "dV", "dR"), dK, dV, dR), _addr(dh0),
+          _addr(workspace), _bytes_of(workspace))
 
 
 def tern_recur_step(K, V, R, h, Y, h_out=None, stream=None) -> None:
     """One token of each sequence (rows of K, V, R): the state moves from h to
     h_out (None: in place) and Y = sigmoid(R) h_out."""
     fn = "tern_recur_step"
-    rows, C, _, ld = _recur_checks(fn, K, V, R, None, None)
+    shape, ld = _recur_inputs(fn, K, V, R)
     h_out = h if h_out is None else h_out
-    _need(fn, "h", h, (rows, C), _F32)
-    _need(fn, "h_out", h_out, (rows, C), _F32)
-    _need(fn, "Y", Y, (rows, C), (K.dtype,))
-    _need_device(fn, K, V, R, h, h_out, Y)
-    with torch.cuda.device(K.device):
-        rc = lib().tern_recur_step(_row_ptr(K), _row_ptr(V), _row_ptr(R), ld, _act_code(K), rows, C, _ptr(h),
-                                   _ptr(h_out), _row_ptr(Y), _rows(fn, [("Y", Y)]), _stream_of(K, stream))
-    _check(fn, rc)
+    _shaped(fn, "h", h, shape, _F32)
+    _shaped(fn, "h_out", h_out, shape, _F32)
+    _shaped(fn, "Y", Y, shape, (K.dtype,))
+    dev = _device_of(fn, K, V, R, h, h_out, Y)
+    _call(fn, dev, stream, K.data_ptr(), V.data_ptr(), R.data_ptr(), ld, _act_code(K), shape[0], shape[1], _addr(h),
+          _addr(h_out), Y.data_ptr(), _row_stride(fn, "Y", Y))
 
 
 def empty_recur_states(T: int, C: int, device="cuda") -> torch.Tensor:

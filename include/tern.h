@@ -466,6 +466,49 @@ int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int
                     void *stream);
 
 /*
+ * Products of a few rows with 4-bit weights and group scales: the form in
+ * which a layer's matrices are served, one or a few tokens at a time.  The
+ * codes are those of the SR4 accumulator (q clamped to +-7 fits), with one
+ * scale per `group` consecutive input rows and output column:
+ *   Y[t, c] = sum_r X[t, r] q[r, c] gscale[r / group, c].
+ *
+ * tern_q4_packed_bytes -- bytes of the packed handle of an [in, out] matrix
+ *   (-1 for sizes that are negative, too large or no multiples of 8).
+ * tern_q4_pack -- q int8 [in, out] (values outside [-8, 7] are clamped) to
+ *   `packed` (device, 16-byte aligned), in the order the product reads it:
+ *   blocks of 16 columns x 128 rows, 4 bits a weight.  Done once a matrix.
+ *   Errors: NULL, SHAPE, ALIGN, ALIAS, HIP.
+ * tern_q4_matvec -- Y [T, out] from X [T, in].
+ *   X          act_dtype TERN_F32 or TERN_BF16; Y as in tern_linear_fwd:
+ *              TERN_F32, or TERN_BF16 (rounded once) with bf16 activations.
+ *   gscale     [ceil(in / group), out] of scale_dtype (TERN_F32 or
+ *              TERN_BF16); group 32, 64 or 128 (TERN_ERR_VALUE otherwise); the
+ *              last group may be short.
+ *   T          any, 16 rows share one pass over the weights (at most 1048560).
+ *   Products of the integer codes with X are exact, sums are fp32, the scale
+ *   multiplies each group's sum once; the order of the sums is fixed.  A row of
+ *   X that holds a non-finite value spoils its own row of Y only.
+ * tern_layer_q4_matvec -- the same for 1 to 8 projections that share T and the
+ *   types (a layer's receptance, key and value on one token), in one launch.
+ *   Inputs may be shared; no output may overlap an input or another output.
+ * Errors: NULL, SHAPE, DTYPE, VALUE (group), ALIGN, ALIAS, HIP.
+ */
+typedef struct tern_q4_proj {
+    int64_t in, out, group;
+    const uint32_t *packed;
+    const void *gscale;
+    const void *X;
+    void *Y;
+} tern_q4_proj_t;
+int64_t tern_q4_packed_bytes(int64_t in, int64_t out);
+int tern_q4_pack(const int8_t *q, int64_t in, int64_t out, uint32_t *packed, void *stream);
+int tern_q4_matvec(const void *X, int32_t act_dtype, const uint32_t *packed, const void *gscale,
+                   int32_t scale_dtype, int64_t group, int64_t T, int64_t in, int64_t out, void *Y,
+                   int32_t y_dtype, void *stream);
+int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int32_t act_dtype,
+                         int32_t scale_dtype, int32_t y_dtype, void *stream);
+
+/*
  * Graphs of library calls.  The page's trainer launches every glue kernel and
  * GEMM of a step separately and notes that it is launch-bound; a caller can
  * instead record any sequence of the calls above (for example materialize,

@@ -63,6 +63,10 @@ SIGNATURES = {
     "tern_recur_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i32,
                                       _vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "tern_recur_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "tern_q4_packed_bytes": (_i64, [_i64, _i64]),
+    "tern_q4_pack": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp]),
+    "tern_q4_matvec": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp]),
+    "tern_layer_q4_matvec": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _vp]),
     "tern_graph_begin": (ctypes.c_int, [_vp]),
     "tern_graph_end": (ctypes.c_int, [_vp, ctypes.POINTER(_vp)]),
     "tern_graph_launch": (ctypes.c_int, [_vp, _vp]),
@@ -677,6 +681,87 @@ def empty_recur_states(T: int, C: int, device="cuda") -> torch.Tensor:
 def empty_recur_workspace(T: int, C: int, device="cuda") -> torch.Tensor:
     """Workspace of tern_recur_fwd and tern_recur_bwd, either activation type."""
     return torch.empty((max(tern_recur_workspace_bytes(T, C), 16),), dtype=torch.uint8, device=device)
+
+
+class TernQ4Proj(ctypes.Structure):
+    """tern_q4_proj_t: one projection of a 4-bit layer call."""
+    _fields_ = [("in_", _i64), ("out", _i64), ("group", _i64), ("packed", _vp), ("gscale", _vp), ("X", _vp),
+                ("Y", _vp)]
+
+
+def tern_q4_packed_bytes(n_in: int, n_out: int) -> int:
+    return int(lib().tern_q4_packed_bytes(int(n_in), int(n_out)))
+
+
+def empty_q4_packed(n_in: int, n_out: int, device="cuda") -> torch.Tensor:
+    """Handle of tern_q4_pack for an [n_in, n_out] matrix."""
+    return torch.empty((max(tern_q4_packed_bytes(n_in, n_out), 16) // 4,), dtype=torch.int32, device=device)
+
+
+def tern_q4_pack(q: torch.Tensor, packed: torch.Tensor, stream=None) -> None:
+    """q int8 [in, out] (clamped to [-8, 7]) -> 4-bit handle (see empty_q4_packed)."""
+    fn = "tern_q4_pack"
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError(f"{fn}: q must be a tensor [in, out]")
+    n_in, n_out = q.shape
+    _need(fn, "q", q, (n_in, n_out), (torch.int8,))
+    _need_bytes(fn, "packed", packed, max(tern_q4_packed_bytes(n_in, n_out), 0))
+    _call(fn, _device_of(fn, q, packed), stream, _addr(q), n_in, n_out, _addr(packed))
+
+
+def _q4_packed(fn, packed, n_in: int, n_out: int) -> None:
+    if not isinstance(packed, torch.Tensor) or packed.dtype != torch.int32:
+        raise TypeError(f"{fn}: packed must be an int32 tensor (see empty_q4_packed)")
+    # 16 columns x 128 rows a block of 256 words
+    if packed.numel() < -(-n_out // 16) * -(-n_in // 128) * 256:
+        _need_bytes(fn, "packed", packed, tern_q4_packed_bytes(n_in, n_out))
+
+
+def tern_q4_matvec(X, packed, gscale, group: int, Y, stream=None) -> None:
+    """Y [T, out] = X [T, in] . (q * scale of the group), with q as packed by
+    tern_q4_pack and gscale [ceil(in / group), out] (fp32 or bf16)."""
+    fn = "tern_q4_matvec"
+    if X.dim() != 2 or Y.dim() != 2:
+        raise ValueError(f"{fn}: X must be [T, in] and Y [T, out]")
+    T, n_in = X.shape
+    n_out = Y.shape[1]
+    _shaped(fn, "X", X, (T, n_in), _ACT)
+    _shaped(fn, "Y", Y, (T, n_out), (torch.float32, X.dtype))
+    group = int(group)
+    _shaped(fn, "gscale", gscale, (-(-n_in // group) if group > 0 else 0, n_out), _ACT)
+    _q4_packed(fn, packed, n_in, n_out)
+    dev = _device_of(fn, X, packed, gscale, Y)
+    _call(fn, dev, stream, _addr(X), _act_code(X), _addr(packed), _addr(gscale), _act_code(gscale), group, T, n_in,
+          n_out, _addr(Y), _act_code(Y))
+
+
+def tern_layer_q4_matvec(projs, stream=None) -> None:
+    """tern_q4_matvec of 1 to 8 projections in one launch.  projs: dicts with
+    n_in, n_out, group and the tensors packed, gscale, X, Y; they share T and
+    the types of X, gscale and Y."""
+    fn = "tern_layer_q4_matvec"
+    n = len(projs)
+    if not 1 <= n <= 8:
+        raise ValueError(f"{fn}: 1 to 8 projections, got {n}")
+    arr = (TernQ4Proj * n)()
+    first = projs[0]
+    X0, s0, Y0 = first["X"], first["gscale"], first["Y"]
+    T = X0.shape[0]
+    if X0.dtype not in _ACT or s0.dtype not in _ACT or Y0.dtype not in (torch.float32, X0.dtype):
+        raise TypeError(f"{fn}: X and gscale must be bfloat16 or float32, Y float32 or X's dtype")
+    xd, sd, yd = (X0.dtype,), (s0.dtype,), (Y0.dtype,)
+    used = []
+    for a, d in zip(arr, projs):
+        n_in, n_out, group = d["n_in"], d["n_out"], d["group"]
+        X, s, Y, pk = d["X"], d["gscale"], d["Y"], d["packed"]
+        _shaped(fn, "X", X, (T, n_in), xd)
+        _shaped(fn, "gscale", s, (-(-n_in // group) if group > 0 else 0, n_out), sd)
+        _shaped(fn, "Y", Y, (T, n_out), yd)
+        _q4_packed(fn, pk, n_in, n_out)
+        a.in_, a.out, a.group = n_in, n_out, group
+        a.packed, a.gscale, a.X, a.Y = _addr(pk), _addr(s), _addr(X), _addr(Y)
+        used += (X, s, Y, pk)
+    _call(fn, _device_of(fn, *used), stream, arr, n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
 
 
 def tern_graph_begin(stream) -> None:

@@ -116,6 +116,22 @@ __device__ inline void wave_pos(const RecurArgs &a, int &c, int64_t &y) {
     c = (int)(b - y * a.ncb);
 }
 
+// The rows of one checkpoint block (rows beyond the chunk's end repeat its
+// last one), all loads issued together.
+template <class E>
+__device__ inline void load_rows(typename E::Raw *x, const void *p, int64_t ld, int64_t tb, int64_t t1, int col) {
+    constexpr int es = 4 / E::N;
+    const char *base = (const char *)p + (tb * ld + col) * es;
+#pragma unroll
+    for (int j = 0; j < kBlk; j++) {
+        const int64_t r = tb + j < t1 ? j : t1 - 1 - tb;
+        x[j] = *(const typename E::Raw *)(base + r * ld * es);
+    }
+}
+
+// Keeps loads that were issued before it from sinking to their uses.
+__device__ inline void issued() { __builtin_amdgcn_sched_barrier(0); }
+
 // Sequences without tokens pass their state through: dst[s] = src[s].
 template <int N>
 __device__ inline void copy_empty(const RecurArgs &a, int64_t group, int col, const float *src, float *dst) {
@@ -138,6 +154,7 @@ __device__ inline void copy_empty(const RecurArgs &a, int64_t group, int col, co
 template <class E>
 __global__ __launch_bounds__(64) void recur_agg_kernel(RecurArgs a) {
     constexpr int N = E::N;
+    using Raw = typename E::Raw;
     int cb;
     int64_t ch;
     wave_pos(a, cb, ch);
@@ -151,40 +168,51 @@ __global__ __launch_bounds__(64) void recur_agg_kernel(RecurArgs a) {
     float A[N], B[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
+    auto row = [&](Raw kr, Raw vr) {
+        float kf[N], vf[N];
+        E::unpack(kr, kf);
+        E::unpack(vr, vf);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float w = sigmoid(kf[i]);
+            A[i] = fmaf(-w, A[i], A[i]);
+            B[i] = fmaf(w, vf[i] - B[i], B[i]);
+        }
+    };
+    Raw k[kBlk], v[kBlk];
+    load_rows<E>(k, a.K, a.ld, t0, t1, col);
+    load_rows<E>(v, a.V, a.ld, t0, t1, col);
     for (int64_t tb = t0; tb < t1; tb += kBlk) {
-        typename E::Raw k[kBlk], v[kBlk];
-        const int n = (int)(t1 - tb < kBlk ? t1 - tb : kBlk);
+        // the next block's loads fly while this one is worked on
+        const int64_t tn = tb + kBlk < t1 ? tb + kBlk : tb;
+        Raw k2[kBlk], v2[kBlk];
+        load_rows<E>(k2, a.K, a.ld, tn, t1, col);
+        load_rows<E>(v2, a.V, a.ld, tn, t1, col);
+        issued();
+        if (!first && cu.live() && nb >= tb + kBlk && tb + kBlk <= t1) {
 #pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            const int64_t t = tb + (j < n ? j : n - 1);
-            k[j] = *(const typename E::Raw *)((const char *)a.K + (t * a.ld + col) * (4 / N));
-            v[j] = *(const typename E::Raw *)((const char *)a.V + (t * a.ld + col) * (4 / N));
-        }
+            for (int j = 0; j < kBlk; j++) row(k[j], v[j]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            if (j >= n) break;
-            if (tb + j >= nb) {
-                cu.forth(tb + j);
-                nb = cu.end();
-                first = cu.live();
-            }
-            if (first) {
-                first = false;
+            for (int j = 0; j < kBlk; j++) {
+                const int64_t t = tb + j;
+                if (t >= t1) continue;
+                if (t >= nb) {
+                    cu.forth(t);
+                    nb = cu.end();
+                    first = cu.live();
+                }
+                if (first) {
+                    first = false;
 #pragma unroll
-                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
-                if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, B);
-            }
-            if (!cu.live()) continue;
-            float kf[N], vf[N];
-            E::unpack(k[j], kf);
-            E::unpack(v[j], vf);
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                const float w = sigmoid(kf[i]);
-                A[i] = fmaf(-w, A[i], A[i]);
-                B[i] = fmaf(w, vf[i] - B[i], B[i]);
+                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
+                    if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, B);
+                }
+                if (cu.live()) row(k[j], v[j]);
             }
         }
+#pragma unroll
+        for (int j = 0; j < kBlk; j++) k[j] = k2[j], v[j] = v2[j];
     }
     float *g = a.agg + ch * 2 * a.C + col;
     store_f<N>(g, A);
@@ -243,6 +271,7 @@ __global__ __launch_bounds__(1024) void recur_carry_kernel(RecurArgs a) {
 template <class E>
 __global__ __launch_bounds__(64) void recur_fwd_kernel(RecurArgs a) {
     constexpr int N = E::N;
+    using Raw = typename E::Raw;
     int cb;
     int64_t ch;
     wave_pos(a, cb, ch);
@@ -259,45 +288,56 @@ __global__ __launch_bounds__(64) void recur_fwd_kernel(RecurArgs a) {
     bool first = cu.live() && cu.begin() == t0;
     float h[N] = {};
     if (a.carry) load_f<N>(a.carry + ch * a.C + col, h);
+    auto row = [&](Raw kr, Raw vr, Raw rr, int64_t t) {
+        float kf[N], vf[N], rf[N], y[N];
+        E::unpack(kr, kf);
+        E::unpack(vr, vf);
+        E::unpack(rr, rf);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            h[i] = fmaf(sigmoid(kf[i]), vf[i] - h[i], h[i]);
+            y[i] = sigmoid(rf[i]) * h[i];
+        }
+        *(Raw *)((char *)a.Y + (t * a.ldy + col) * (4 / N)) = E::pack(y);
+    };
+    Raw k[kBlk], v[kBlk], r[kBlk];
+    load_rows<E>(k, a.K, a.ld, t0, t1, col);
+    load_rows<E>(v, a.V, a.ld, t0, t1, col);
+    load_rows<E>(r, a.R, a.ld, t0, t1, col);
     for (int64_t tb = t0; tb < t1; tb += kBlk) {
-        typename E::Raw k[kBlk], v[kBlk], r[kBlk];
-        const int n = (int)(t1 - tb < kBlk ? t1 - tb : kBlk);
-#pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            const int64_t o = ((tb + (j < n ? j : n - 1)) * a.ld + col) * (4 / N);
-            k[j] = *(const typename E::Raw *)((const char *)a.K + o);
-            v[j] = *(const typename E::Raw *)((const char *)a.V + o);
-            r[j] = *(const typename E::Raw *)((const char *)a.R + o);
-        }
+        const int64_t tn = tb + kBlk < t1 ? tb + kBlk : tb;
+        Raw k2[kBlk], v2[kBlk], r2[kBlk];
+        load_rows<E>(k2, a.K, a.ld, tn, t1, col);
+        load_rows<E>(v2, a.V, a.ld, tn, t1, col);
+        load_rows<E>(r2, a.R, a.ld, tn, t1, col);
+        issued();
         if (a.states) store_f<N>(a.states + tb / kBlk * a.C + col, h);
+        if (!first && cu.live() && nb > tb + kBlk && tb + kBlk <= t1) {
 #pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            if (j >= n) break;
-            const int64_t t = tb + j;
-            if (t >= nb) {
-                cu.forth(t);
-                nb = cu.end();
-                first = cu.live();
-            }
-            if (first) {
-                first = false;
+            for (int j = 0; j < kBlk; j++) row(k[j], v[j], r[j], tb + j);
+        } else {
 #pragma unroll
-                for (int i = 0; i < N; i++) h[i] = 0.0f;
-                if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, h);
-            }
-            if (!cu.live()) continue;
-            float kf[N], vf[N], rf[N], y[N];
-            E::unpack(k[j], kf);
-            E::unpack(v[j], vf);
-            E::unpack(r[j], rf);
+            for (int j = 0; j < kBlk; j++) {
+                const int64_t t = tb + j;
+                if (t >= t1) continue;
+                if (t >= nb) {
+                    cu.forth(t);
+                    nb = cu.end();
+                    first = cu.live();
+                }
+                if (first) {
+                    first = false;
 #pragma unroll
-            for (int i = 0; i < N; i++) {
-                h[i] = fmaf(sigmoid(kf[i]), vf[i] - h[i], h[i]);
-                y[i] = sigmoid(rf[i]) * h[i];
+                    for (int i = 0; i < N; i++) h[i] = 0.0f;
+                    if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, h);
+                }
+                if (!cu.live()) continue;
+                row(k[j], v[j], r[j], t);
+                if (a.hT && t + 1 == nb) store_f<N>(a.hT + cu.cur * a.C + col, h);
             }
-            *(typename E::Raw *)((char *)a.Y + (t * a.ldy + col) * (4 / N)) = E::pack(y);
-            if (a.hT && t + 1 == nb) store_f<N>(a.hT + cu.cur * a.C + col, h);
         }
+#pragma unroll
+        for (int j = 0; j < kBlk; j++) k[j] = k2[j], v[j] = v2[j], r[j] = r2[j];
     }
 }
 

@@ -509,6 +509,46 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
                          int32_t scale_dtype, int32_t y_dtype, void *stream);
 
 /*
+ * A weight update orthogonalised by Newton-Schulz products, as a step on a
+ * matrix's momentum or gradient (gq of tern_linear_bwd_dw) takes it: with
+ * X = G / (|G|_F + 1e-7), each of `steps` steps is
+ *   A = X X^T,   X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ * (X^T X for a G of more rows than columns), and O = gain * X.  A step maps
+ * every singular value x to 3.4445 x - 4.7750 x^3 + 2.0315 x^5; five bring
+ * those above 0.01 |G|_F to between 0.68 and 1.13.
+ *
+ *   G     [rows, cols] of g_dtype (TERN_F32 or TERN_BF16), rows and cols
+ *         multiples of 8, 16-byte aligned; only read.
+ *   O     bf16 [rows, cols], rounded once from the fp32 result; must not
+ *         overlap G or another output.
+ *   gain  factor of the result (a learning rate, sqrt(rows / cols), ...).
+ *   steps 1 to 64 (TERN_ERR_VALUE otherwise).
+ *   workspace  at least tern_orthogonalize_workspace_bytes(rows, cols) bytes.
+ * Arithmetic: products on the fp16 matrix cores, sums in fp32, |G|_F in f64;
+ * X, A and A's polynomial are held in fp16 (scaled by powers of two) between
+ * the products.  The error this leaves in O is about that of O's own rounding
+ * for a G whose singular values are of like size; directions in which G is
+ * below about 1e-4 of its norm receive noise of the order of 1e-3 each.  The
+ * order of every sum is fixed.  A non-finite G gives an unspecified O.
+ *
+ * tern_layer_orthogonalize -- the same for 1 to 8 matrices (the weight
+ * gradients of a layer): one launch a product for all of them.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, WORKSPACE, ALIGN, ALIAS, HIP.
+ */
+typedef struct tern_ortho {
+    int64_t rows, cols;
+    const void *G;
+    void *O;
+    float gain;
+} tern_ortho_t;
+size_t tern_orthogonalize_workspace_bytes(int64_t rows, int64_t cols);
+int tern_orthogonalize(const void *G, int32_t g_dtype, int64_t rows, int64_t cols, int32_t steps,
+                       float gain, void *O, void *workspace, size_t workspace_bytes, void *stream);
+size_t tern_layer_orthogonalize_workspace_bytes(const tern_ortho_t *mats, int32_t n);
+int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtype, int32_t steps,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Graphs of library calls.  The page's trainer launches every glue kernel and
  * GEMM of a step separately and notes that it is launch-bound; a caller can
  * instead record any sequence of the calls above (for example materialize,

@@ -67,6 +67,10 @@ SIGNATURES = {
     "tern_q4_pack": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp]),
     "tern_q4_matvec": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp]),
     "tern_layer_q4_matvec": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _vp]),
+    "tern_orthogonalize_workspace_bytes": (_sz, [_i64, _i64]),
+    "tern_orthogonalize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "tern_layer_orthogonalize_workspace_bytes": (_sz, [_vp, _i32]),
+    "tern_layer_orthogonalize": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _sz, _vp]),
     "tern_graph_begin": (ctypes.c_int, [_vp]),
     "tern_graph_end": (ctypes.c_int, [_vp, ctypes.POINTER(_vp)]),
     "tern_graph_launch": (ctypes.c_int, [_vp, _vp]),
@@ -762,6 +766,57 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
         a.packed, a.gscale, a.X, a.Y = _addr(pk), _addr(s), _addr(X), _addr(Y)
         used += (X, s, Y, pk)
     _call(fn, _device_of(fn, *used), stream, arr, n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
+
+
+class TernOrtho(ctypes.Structure):
+    """tern_ortho_t: one matrix of a layer's orthogonalisation."""
+    _fields_ = [("rows", _i64), ("cols", _i64), ("G", _vp), ("O", _vp), ("gain", ctypes.c_float)]
+
+
+def tern_orthogonalize_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().tern_orthogonalize_workspace_bytes(int(rows), int(cols)))
+
+
+def tern_layer_orthogonalize_workspace_bytes(shapes) -> int:
+    """Workspace of tern_layer_orthogonalize for matrices of these (rows, cols)."""
+    arr = (TernOrtho * max(len(shapes), 1))()
+    for a, (r, c) in zip(arr, shapes):
+        a.rows, a.cols = int(r), int(c)
+    return int(lib().tern_layer_orthogonalize_workspace_bytes(arr, len(shapes)))
+
+
+def empty_ortho_workspace(shapes, device="cuda") -> torch.Tensor:
+    """Workspace for matrices of these (rows, cols): one pair for
+    tern_orthogonalize, a layer's for tern_layer_orthogonalize."""
+    return torch.empty((max(tern_layer_orthogonalize_workspace_bytes(shapes), 16),), dtype=torch.uint8, device=device)
+
+
+def tern_orthogonalize(G, O, workspace, steps: int = 5, gain: float = 1.0, stream=None) -> None:
+    """O (bf16) = gain * the Newton-Schulz orthogonalisation of G (fp32 or bf16)."""
+    tern_layer_orthogonalize([dict(G=G, O=O, gain=gain)], workspace, steps, stream)
+
+
+def tern_layer_orthogonalize(mats, workspace, steps: int = 5, stream=None) -> None:
+    """tern_orthogonalize of 1 to 8 matrices together.  mats: dicts with G and O
+    [rows, cols] and, if not 1, gain; the G share one dtype."""
+    fn = "tern_layer_orthogonalize"
+    n = len(mats)
+    if not 1 <= n <= 8:
+        raise ValueError(f"{fn}: 1 to 8 matrices, got {n}")
+    arr = (TernOrtho * n)()
+    G0 = mats[0]["G"]
+    used = []
+    for a, d in zip(arr, mats):
+        G, O = d["G"], d["O"]
+        if not isinstance(G, torch.Tensor) or G.dim() != 2:
+            raise ValueError(f"{fn}: G must be a tensor [rows, cols]")
+        _shaped(fn, "G", G, G.shape, _ACT if G is G0 else (G0.dtype,))
+        _shaped(fn, "O", O, G.shape, (torch.bfloat16,))
+        a.rows, a.cols = G.shape
+        a.G, a.O, a.gain = _addr(G), _addr(O), float(d.get("gain", 1.0))
+        used += (G, O)
+    dev = _device_of(fn, *used, workspace)
+    _call(fn, dev, stream, arr, n, _act_code(G0), int(steps), _addr(workspace), _bytes_of(workspace))
 
 
 def tern_graph_begin(stream) -> None:

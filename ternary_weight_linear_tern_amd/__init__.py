@@ -747,25 +747,32 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
     n = len(projs)
     if not 1 <= n <= 8:
         raise ValueError(f"{fn}: 1 to 8 projections, got {n}")
-    arr = (TernQ4Proj * n)()
     first = projs[0]
     X0, s0, Y0 = first["X"], first["gscale"], first["Y"]
     T = X0.shape[0]
-    if X0.dtype not in _ACT or s0.dtype not in _ACT or Y0.dtype not in (torch.float32, X0.dtype):
+    act, sdt, ydt = X0.dtype, s0.dtype, Y0.dtype
+    if act not in _ACT or sdt not in _ACT or ydt not in (torch.float32, act):
         raise TypeError(f"{fn}: X and gscale must be bfloat16 or float32, Y float32 or X's dtype")
-    xd, sd, yd = (X0.dtype,), (s0.dtype,), (Y0.dtype,)
-    used = []
-    for a, d in zip(arr, projs):
+    dev = X0.get_device()
+    words = []   # the tern_q4_proj_t array: seven 64-bit members each
+    for d in projs:
         n_in, n_out, group = d["n_in"], d["n_out"], d["group"]
         X, s, Y, pk = d["X"], d["gscale"], d["Y"], d["packed"]
-        _shaped(fn, "X", X, (T, n_in), xd)
-        _shaped(fn, "gscale", s, (-(-n_in // group) if group > 0 else 0, n_out), sd)
-        _shaped(fn, "Y", Y, (T, n_out), yd)
+        if X.shape != (T, n_in) or X.dtype is not act:
+            _need(fn, "X", X, (T, n_in), (act,))
+        groups = -(-n_in // group) if group > 0 else 0
+        if s.shape != (groups, n_out) or s.dtype is not sdt:
+            _need(fn, "gscale", s, (groups, n_out), (sdt,))
+        if Y.shape != (T, n_out) or Y.dtype is not ydt:
+            _need(fn, "Y", Y, (T, n_out), (ydt,))
         _q4_packed(fn, pk, n_in, n_out)
-        a.in_, a.out, a.group = n_in, n_out, group
-        a.packed, a.gscale, a.X, a.Y = _addr(pk), _addr(s), _addr(X), _addr(Y)
-        used += (X, s, Y, pk)
-    _call(fn, _device_of(fn, *used), stream, arr, n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
+        if X.get_device() != dev or s.get_device() != dev or Y.get_device() != dev \
+                or pk.get_device() != dev:
+            _need_device(fn, X0, X, s, Y, pk)
+        words += (n_in, n_out, group, _addr(pk), _addr(s), _addr(X), _addr(Y))
+    if dev < 0:
+        _need_device(fn, X0)
+    _call(fn, dev, stream, (_i64 * (7 * n))(*words), n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
 
 
 class TernOrtho(ctypes.Structure):

@@ -19,6 +19,7 @@
 // exactly, and multiplied term by term.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "../../include/tern.h"
 #include "tern_plan.h"
@@ -33,7 +34,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCols = 16, kRows = 128;          // a block of the packed matrix: 1 KiB
 constexpr int kBlockWords = kCols * kRows / 8;
-constexpr int kMaxWaves = 16;
+// waves of a workgroup: 16 where 128 registers a lane are enough
+constexpr int max_waves(int terms, int nb) { return terms == 1 && nb == 1 ? 16 : 8; }
 
 // Word w of lane l of a block: rows 32 w + 8 (l / 16) + e (e < 8), column
 // l % 16.  Rows e = 2 d and 2 d + 1 stand at bits 4 d + 3 and 4 d + 19 (mod 32), so
@@ -69,8 +71,12 @@ struct Q4One {
 };
 struct Q4Args {
     Q4One p[kMaxGroup];
-    int n, T, waves;
+    int n, T, waves, y_bf16;
 };
+
+__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 
 __device__ inline bf16x8 weights(uint32_t w) {
     u32x4 r;
@@ -82,121 +88,181 @@ __device__ inline bf16x8 weights(uint32_t w) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// 8 activations of a lane's token as bf16 terms (TERMS 1: bf16 activations)
+// 8 activations of a lane's token: as loaded, and as bf16 terms (TERMS 1:
+// bf16 activations; 3: fp32, cut into three terms of 8 significant bits)
+template <int TERMS>
+struct RawActs {
+    u32x4 v[TERMS == 1 ? 1 : 2];
+};
 template <int TERMS>
 struct Acts {
     bf16x8 t[TERMS];
 };
 template <int TERMS>
-__device__ inline void load_acts(Acts<TERMS> &a, const void *X, int64_t at, bool ok) {
-    if constexpr (TERMS == 1) {
-        u32x4 v = {0, 0, 0, 0};
-        if (ok) v = *(const u32x4 *)((const uint16_t *)X + at);
-        a.t[0] = __builtin_bit_cast(bf16x8, v);
-    } else {
-        float v[8] = {};
-        if (ok) {
-            const f32x4 lo = *(const f32x4 *)((const float *)X + at), hi = *(const f32x4 *)((const float *)X + at + 4);
+__device__ inline void load_acts(RawActs<TERMS> &a, const void *X, int64_t at, bool ok) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = lo[i], v[4 + i] = hi[i];
-        }
+    for (int i = 0; i < (TERMS == 1 ? 1 : 2); i++) {
+        a.v[i] = u32x4{0, 0, 0, 0};
+        if (ok) a.v[i] = *((const u32x4 *)((const char *)X + at * (TERMS == 1 ? 2 : 4)) + i);
+    }
+}
+template <int TERMS>
+__device__ inline Acts<TERMS> terms(const RawActs<TERMS> &a) {
+    Acts<TERMS> r;
+    if constexpr (TERMS == 1) {
+        r.t[0] = __builtin_bit_cast(bf16x8, a.v[0]);
+    } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = a.v[i >> 2][i & 3];
 #pragma unroll
         for (int t = 0; t < 3; t++) {
             u32x4 o;
 #pragma unroll
-            for (int d = 0; d < 4; d++) {
-                uint32_t x[2];
+            for (int d = 0; d < 4; d++) o[d] = __builtin_amdgcn_perm(v[2 * d + 1], v[2 * d], 0x07060302u);   // upper halves
+            r.t[t] = __builtin_bit_cast(bf16x8, o);
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    x[i] = __builtin_bit_cast(uint32_t, v[2 * d + i]);
-                    v[2 * d + i] -= __builtin_bit_cast(float, x[i] & 0xFFFF0000u);
-                }
-                o[d] = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);   // the upper halves
-            }
-            a.t[t] = __builtin_bit_cast(bf16x8, o);
+            for (int i = 0; i < 8; i++)
+                v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, v[i]) -
+                                                        __builtin_bit_cast(float, v[i] & 0xFFFF0000u));
         }
     }
+    return r;
 }
 
+// the 4 scales of a lane's columns: as loaded, and as fp32
 template <bool SBF>
-__device__ inline f32x4 load_scale(const void *s, int64_t at) {
-    if constexpr (SBF) {
-        const u32x2 v = *(const u32x2 *)((const uint16_t *)s + at);
-        return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
-                     __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xFFFF0000u)};
-    } else {
-        return *(const f32x4 *)((const float *)s + at);
+struct Scales {
+    using Raw = std::conditional_t<SBF, u32x2, f32x4>;
+    __device__ static Raw load(const void *s, int64_t at) {
+        return *(const Raw *)((const char *)s + at * (SBF ? 2 : 4));
+    }
+    __device__ static f32x4 get(Raw v) {
+        if constexpr (SBF)
+            return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
+                         __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xFFFF0000u)};
+        else
+            return v;
+    }
+};
+
+// The activations and scales of 128 rows (GC: 32-row chunks of a scale group).
+template <int TERMS, bool SBF, int NB, int GC>
+struct Side {
+    RawActs<TERMS> x[4];
+    typename Scales<SBF>::Raw s[4 / GC][NB];
+};
+
+// Blocks k0 .. k1 - 1 of a wave's NB column blocks.  The weights, which come
+// from HBM, are loaded kAhead blocks ahead, the activations and scales, which
+// mostly come from L2, one block ahead.
+constexpr int kAhead = 2;
+template <int TERMS, bool SBF, int NB, int GC>
+__device__ inline void run_blocks(const Q4One &p, int T, int tok, int sub, const u32x4 *const (&W)[NB],
+                                  const int (&col)[NB], int k0, int k1, f32x4 (&y)[NB]) {
+    using S = Side<TERMS, SBF, NB, GC>;
+    const int64_t xrow = (int64_t)tok * p.in + sub * 8;
+    const int ng = (p.in + GC * 32 - 1) / (GC * 32);
+    u32x4 w[kAhead][NB];
+    auto load_w = [&](u32x4 (&o)[NB], int kb) {
+#pragma unroll
+        for (int i = 0; i < NB; i++) o[i] = W[i][(int64_t)(kb < k1 ? kb : k1 - 1) * 64];
+    };
+    auto load_side = [&](S &b, int kb) {
+        kb = kb < k1 ? kb : k1 - 1;
+#pragma unroll
+        for (int ck = 0; ck < 4; ck++) {
+            const int r = kb * kRows + ck * 32;
+            load_acts<TERMS>(b.x[ck], p.X, xrow + r, tok < T && r + sub * 8 < p.in);
+        }
+#pragma unroll
+        for (int g = 0; g < 4 / GC; g++) {
+            // a group past the last row (its weights multiply zeros) takes the last scale
+            const int at = kb * (4 / GC) + g;
+#pragma unroll
+            for (int i = 0; i < NB; i++)
+                b.s[g][i] = Scales<SBF>::load(p.gscale, (int64_t)(at < ng ? at : ng - 1) * p.out + col[i]);
+        }
+    };
+    bf16x8 off;
+#pragma unroll
+    for (int e = 0; e < 8; e++) off[e] = (__bf16)-24.0f;
+    auto work = [&](const u32x4 (&wb)[NB], const S &b) {
+#pragma unroll
+        for (int g = 0; g < 4 / GC; g++) {
+            f32x4 acc[NB];
+#pragma unroll
+            for (int c = 0; c < GC; c++) {
+                const int ck = g * GC + c;
+                const Acts<TERMS> x = terms<TERMS>(b.x[ck]);
+                f32x4 z = {0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < TERMS; t++) z = mfma(off, x.t[t], z);
+#pragma unroll
+                for (int i = 0; i < NB; i++) {
+                    acc[i] = c ? acc[i] + z : z;
+                    const bf16x8 q = weights(wb[i][ck]);
+#pragma unroll
+                    for (int t = 0; t < TERMS; t++) acc[i] = mfma(q, x.t[t], acc[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NB; i++) {
+                const f32x4 s = Scales<SBF>::get(b.s[g][i]);
+#pragma unroll
+                for (int r = 0; r < 4; r++) y[i][r] = fmaf(s[r], acc[i][r], y[i][r]);
+            }
+        }
+    };
+    S side[2];
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) load_w(w[j], k0 + j);
+    load_side(side[0], k0);
+    for (int kb = k0; kb < k1; kb += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) {
+            if (kb + j < k1) {
+                load_side(side[(j + 1) & 1], kb + j + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                work(w[j], side[j & 1]);
+                load_w(w[j], kb + j + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
 }
 
 // One workgroup: NB column blocks, 16 tokens, all rows, the rows' blocks
 // dealt to the waves in runs; the waves' sums meet in shared memory in the
 // order of the waves.
-template <int TERMS, bool SBF, bool YBF, int NB>
-__global__ __launch_bounds__(1024) void q4_kernel(Q4Args a) {
-    __shared__ float red[kMaxWaves][16][NB * kCols + 4];
+template <int TERMS, bool SBF, int NB>
+__global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a) {
+    __shared__ float red[max_waves(TERMS, NB)][16][NB * kCols + 4];
     int pi = 0;
     while (pi + 1 < a.n && (int)blockIdx.x >= a.p[pi + 1].start) pi++;
     const Q4One p = a.p[pi];
-    const int wg = (int)blockIdx.x - p.start;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tok0 = blockIdx.y * 16, tok = tok0 + (lane & 15), sub = lane >> 4;
     const int ncb = (p.out + kCols - 1) / kCols;
-    const int cb0 = wg * NB;
+    const int cb0 = ((int)blockIdx.x - p.start) * NB;
     const int per = (p.nkb + a.waves - 1) / a.waves;
     const int k0 = wave * per, k1 = k0 + per < p.nkb ? k0 + per : p.nkb;
 
     const u32x4 *W[NB];
     int col[NB];   // first of the 4 columns a lane accumulates
+    f32x4 y[NB];
 #pragma unroll
     for (int b = 0; b < NB; b++) {
         const int cb = cb0 + b < ncb ? cb0 + b : ncb - 1;
         W[b] = (const u32x4 *)p.packed + ((int64_t)cb * p.nkb) * 64 + lane;
         const int c = cb * kCols + sub * 4;
         col[b] = c < p.out ? c : 0;   // the last block may be half full (out is a multiple of 8)
+        y[b] = f32x4{0, 0, 0, 0};
     }
-    bf16x8 off;
-#pragma unroll
-    for (int e = 0; e < 8; e++) off[e] = (__bf16)-24.0f;
-
-    f32x4 y[NB];
-#pragma unroll
-    for (int b = 0; b < NB; b++) y[b] = f32x4{0, 0, 0, 0};
-    const bool tok_ok = tok < a.T;
-    for (int kb = k0; kb < k1; kb++) {
-        u32x4 w[NB];
-#pragma unroll
-        for (int b = 0; b < NB; b++) w[b] = W[b][(int64_t)kb * 64];
-        f32x4 acc[NB];
-#pragma unroll
-        for (int ck = 0; ck < 4; ck++) {
-            const int r = kb * kRows + ck * 32 + sub * 8;
-            Acts<TERMS> x;
-            load_acts<TERMS>(x, p.X, (int64_t)tok * p.in + r, tok_ok && r < p.in);
-            const bool head = (ck & (p.group_chunks - 1)) == 0;
-            f32x4 z = {0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < TERMS; t++) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, x.t[t], z, 0, 0, 0);
-#pragma unroll
-            for (int b = 0; b < NB; b++) {
-                acc[b] = head ? z : acc[b] + z;
-                const bf16x8 q = weights(w[b][ck]);
-#pragma unroll
-                for (int t = 0; t < TERMS; t++)
-                    acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, x.t[t], acc[b], 0, 0, 0);
-            }
-            if (((ck + 1) & (p.group_chunks - 1)) == 0) {
-                const int g = (kb * 4 + ck) / p.group_chunks;
-                if (kb * kRows + ck / p.group_chunks * p.group_chunks * 32 < p.in) {
-#pragma unroll
-                    for (int b = 0; b < NB; b++) {
-                        const f32x4 s = load_scale<SBF>(p.gscale, (int64_t)g * p.out + col[b]);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) y[b][i] = fmaf(s[i], acc[b][i], y[b][i]);
-                    }
-                }
-            }
-        }
+    if (k0 < k1) {
+        if (p.group_chunks == 1) run_blocks<TERMS, SBF, NB, 1>(p, a.T, tok, sub, W, col, k0, k1, y);
+        else if (p.group_chunks == 2) run_blocks<TERMS, SBF, NB, 2>(p, a.T, tok, sub, W, col, k0, k1, y);
+        else run_blocks<TERMS, SBF, NB, 4>(p, a.T, tok, sub, W, col, k0, k1, y);
     }
 #pragma unroll
     for (int b = 0; b < NB; b++) *(f32x4 *)&red[wave][lane & 15][b * kCols + sub * 4] = y[b];
@@ -209,7 +275,7 @@ __global__ __launch_bounds__(1024) void q4_kernel(Q4Args a) {
         const int oc = cb0 * kCols + c;
         if (oc < p.out) {
             const int64_t o = (int64_t)(tok0 + t) * p.out + oc;
-            if constexpr (YBF) ((__bf16 *)p.Y)[o] = (__bf16)v;
+            if (a.y_bf16) ((__bf16 *)p.Y)[o] = (__bf16)v;
             else ((float *)p.Y)[o] = v;
         }
     }
@@ -230,10 +296,10 @@ bool sizes_ok(int64_t in, int64_t out) {
     return in >= 0 && out >= 0 && in <= kMaxInOut && out <= kMaxInOut && in % 8 == 0 && out % 8 == 0;
 }
 
-template <int TERMS, bool SBF, bool YBF>
+template <int TERMS, bool SBF>
 void launch_nb(int nb, dim3 g, dim3 b, hipStream_t st, const qdev::Q4Args &a) {
-    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, YBF, 1>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, YBF, 2>), g, b, 0, st, a);
+    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 1>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 2>), g, b, 0, st, a);
 }
 
 }  // namespace
@@ -296,11 +362,25 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
             if (ranges_overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return TERN_ERR_ALIAS;
     }
     qdev::Q4Args a{};
-    int64_t maxk = 1;
-    for (int i = 0; i < n; i++) maxk = projs[i].in > maxk ? projs[i].in : maxk;
-    const int nb = 1;
+    // Shape of the launch.  From 1024 column blocks on (4 a compute unit) a
+    // wave takes two, which share its activations, and 4 waves share the rows:
+    // 4096 x 16384, one token 10.6 us against 11.8 with single blocks, 16 tokens
+    // 14.1 against 20.7.  Fewer blocks take one each (4096 x 4096 5.3 us against
+    // 6.1), and enough waves that each has about 4 row blocks, which is all it
+    // needs to hide its loads (16384 x 2048: 16 waves 10.9 us, 8 13.1, 4 20.0;
+    // three 2048 x 2048: 4 waves 5.2, 8 5.5, 16 7.7).
+    int64_t maxk = 1, ncb = 0;
+    for (int i = 0; i < n; i++) {
+        maxk = projs[i].in > maxk ? projs[i].in : maxk;
+        ncb += cdiv(projs[i].out, qdev::kCols);
+    }
+    const int nb = ncb >= 1024 ? 2 : 1;
     const int64_t nkb = cdiv(maxk, qdev::kRows);
-    a.waves = (int)(nkb < qdev::kMaxWaves ? nkb : qdev::kMaxWaves);
+    const int64_t most = qdev::max_waves(act_dtype == TERN_F32 ? 3 : 1, nb);
+    int64_t waves = nb == 2 || nkb < 16 ? 4 : nkb / 4;
+    if (waves > most) waves = most;
+    if (waves > nkb) waves = nkb;
+    a.waves = (int)waves;
     a.T = (int)T;
     int64_t wgs = 0;
     for (int i = 0; i < n; i++) {
@@ -316,16 +396,14 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
     if (wgs == 0 || T == 0) return TERN_OK;
     const dim3 g((unsigned)wgs, (unsigned)cdiv(T, 16)), b((unsigned)(a.waves * 64));
     hipStream_t st = (hipStream_t)stream;
-    const bool sbf = scale_dtype == TERN_BF16, ybf = y_dtype == TERN_BF16;
+    a.y_bf16 = y_dtype == TERN_BF16;
+    const bool sbf = scale_dtype == TERN_BF16;
     if (act_dtype == TERN_F32) {
-        if (sbf) launch_nb<3, true, false>(nb, g, b, st, a);
-        else launch_nb<3, false, false>(nb, g, b, st, a);
-    } else if (ybf) {
-        if (sbf) launch_nb<1, true, true>(nb, g, b, st, a);
-        else launch_nb<1, false, true>(nb, g, b, st, a);
+        if (sbf) launch_nb<3, true>(nb, g, b, st, a);
+        else launch_nb<3, false>(nb, g, b, st, a);
     } else {
-        if (sbf) launch_nb<1, true, false>(nb, g, b, st, a);
-        else launch_nb<1, false, false>(nb, g, b, st, a);
+        if (sbf) launch_nb<1, true>(nb, g, b, st, a);
+        else launch_nb<1, false>(nb, g, b, st, a);
     }
     return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP;
 }

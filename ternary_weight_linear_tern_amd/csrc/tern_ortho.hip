@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/tern.h"
 #include "tern_plan.h"
 
@@ -33,7 +35,8 @@ typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 b16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
 #define LDS_AS __attribute__((address_space(3)))
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
@@ -41,8 +44,6 @@ constexpr float kEps = 1e-7f;
 constexpr float kXScale = 16384.0f;
 constexpr int kPad = 64;        // rows and columns of the working matrices: multiples of this, zeros
 constexpr int kParts = 256;     // partial sums of |G|^2
-constexpr int kChunk = 32;      // K of a stage: 64 bytes a row
-constexpr int kStages = 4;
 
 struct OrthoOne {
     const void *G;
@@ -53,7 +54,7 @@ struct OrthoOne {
     int m, n, mp, np;         // of X: m <= n; padded
     float gain;
     int tall;                 // X = G^T
-    int start;                // first workgroup of the launch
+    int start, tiles;         // first workgroup of the launch; workgroups
 };
 struct OrthoArgs {
     OrthoOne p[kMaxGroup];
@@ -69,8 +70,17 @@ __device__ inline int problem_of(const OrthoArgs &a, int wg) {
     return pi;
 }
 
-__device__ inline float g_at(const void *G, int bf, int64_t i) {
-    return bf ? (float)((const __bf16 *)G)[i] : ((const float *)G)[i];
+__device__ inline void load4(const void *G, int bf, int64_t i, float *f) {
+    if (bf) {
+        const uint2 v = *(const uint2 *)((const uint16_t *)G + i);
+        f[0] = __builtin_bit_cast(float, v.x << 16);
+        f[1] = __builtin_bit_cast(float, v.x & 0xFFFF0000u);
+        f[2] = __builtin_bit_cast(float, v.y << 16);
+        f[3] = __builtin_bit_cast(float, v.y & 0xFFFF0000u);
+    } else {
+        const float4 v = *(const float4 *)((const float *)G + i);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    }
 }
 
 // |G|^2 in f64, one partial a workgroup, in a fixed order
@@ -81,18 +91,8 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs a) {
     double s = 0.0;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += kParts * 256) {
         float f[8];
-        if (a.g_bf16) {
-            const u32x4 v = ((const u32x4 *)p.G)[i];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                f[2 * j] = __builtin_bit_cast(float, v[j] << 16);
-                f[2 * j + 1] = __builtin_bit_cast(float, v[j] & 0xFFFF0000u);
-            }
-        } else {
-            const float4 v0 = ((const float4 *)p.G)[2 * i], v1 = ((const float4 *)p.G)[2 * i + 1];
-            f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
-            f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
-        }
+        load4(p.G, a.g_bf16, 8 * i, f);
+        load4(p.G, a.g_bf16, 8 * i + 4, f + 4);
 #pragma unroll
         for (int j = 0; j < 8; j++) s += (double)f[j] * (double)f[j];
     }
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs a) {
 // X and its transpose from G, 64 x 64 tiles, zeros in the padding
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
     __shared__ double red[256];
-    __shared__ h16 tile[64][66];
+    __shared__ h16 tile[64][68];
     const OrthoOne &p = a.p[problem_of(a, blockIdx.x)];
     red[threadIdx.x] = p.part[threadIdx.x];
     __syncthreads();
@@ -118,36 +118,45 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
     }
     const float f = (float)(16384.0 / (sqrt(red[0]) + (double)kEps));
     const int t = blockIdx.x - p.start, tn = p.np / 64;
-    // tile (gi, gj) of G
+    // tile (xi, xj) of X, at (r0, c0) of G
     const int xi = t / tn, xj = t % tn;
     const int64_t r0 = (int64_t)(p.tall ? xj : xi) * 64, c0 = (int64_t)(p.tall ? xi : xj) * 64;
-    const int c = threadIdx.x & 63;
+    // G's sides are multiples of 8: four columns are inside or outside together
+    const int c4 = (threadIdx.x & 15) * 4;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int r = (threadIdx.x >> 6) * 16 + i;
-        float v = 0.0f;
-        if (r0 + r < p.rows && c0 + c < p.cols) v = g_at(p.G, a.g_bf16, (r0 + r) * p.cols + c0 + c) * f;
-        tile[r][c] = (h16)v;
+    for (int i = 0; i < 4; i++) {
+        const int r = (threadIdx.x >> 4) + 16 * i;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (r0 + r < p.rows && c0 + c4 < p.cols) load4(p.G, a.g_bf16, (r0 + r) * p.cols + c0 + c4, v);
+        h16x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; j++) o[j] = (h16)(v[j] * f);
+        *(h16x4 *)&tile[r][c4] = o;
     }
     __syncthreads();
     // the tile as it lies and transposed, into X and X^T (or the other way round)
     h16 *same = p.tall ? p.XT[0] : p.X, *flip = p.tall ? p.X : p.XT[0];
     const int64_t lds = p.tall ? p.mp : p.np, ldf = p.tall ? p.np : p.mp;
+    const int c8 = (threadIdx.x & 7) * 8;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int r = (threadIdx.x >> 6) * 16 + i;
-        same[(r0 + r) * lds + c0 + c] = tile[r][c];
-        flip[(c0 + r) * ldf + r0 + c] = tile[c][r];
+    for (int i = 0; i < 2; i++) {
+        const int r = (threadIdx.x >> 3) + 32 * i;
+        const h16x4 lo = *(const h16x4 *)&tile[r][c8], hi = *(const h16x4 *)&tile[r][c8 + 4];
+        h16x8 s, q;
+#pragma unroll
+        for (int j = 0; j < 4; j++) s[j] = lo[j], s[4 + j] = hi[j];
+#pragma unroll
+        for (int j = 0; j < 8; j++) q[j] = tile[c8 + j][r];
+        *(h16x8 *)(same + (r0 + r) * lds + c0 + c8) = s;
+        *(h16x8 *)(flip + (c0 + r) * ldf + r0 + c8) = q;
     }
 }
 
 // ---------------------------------------------------------------------------
 // P Q^T: a workgroup of 2 x 2 waves computes a (2 WT)^2 tile, each wave
-// WT x WT in 32 x 32 blocks.  Stages of 32 K go to LDS by direct loads, three
+// WT x WT in 32 x 32 blocks.  Stages of KC K go to LDS by direct loads, ST - 1
 // ahead; the fragments of a stage are read into registers one stage ahead, so
-// the matrix cores run over the barrier (one a stage).  A row's four 16-byte
-// pieces lie permuted by its index, (row / 2) % 4, so that eight consecutive
-// rows' pieces fall in different banks.
+// the matrix cores run over the barrier (one a stage).
 // ---------------------------------------------------------------------------
 
 enum { GRAM = 0, POLY = 1, APPLY = 2 };
@@ -158,8 +167,8 @@ __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *p, int64_t bytes) {
 }
 
 // 16 bytes a lane to LDS, at lds + 16 lane; reads outside the resource give zeros
-__device__ inline void load_lds(__amdgpu_buffer_rsrc_t rs, char *lds, uint32_t voff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_AS void *)lds, 16, voff, 0, 0, 0);
+__device__ inline void load_lds(__amdgpu_buffer_rsrc_t rs, char *lds, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_AS void *)lds, 16, voff, soff, 0, 0);
 }
 
 template <int N>
@@ -175,77 +184,94 @@ __device__ inline f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
                                                   0);
 }
 
-template <int WT>
+// 4 x 4 transpose of 16-bit values among the 16 lanes of a group while reading
+__device__ inline u32x2 transposed(const char *at) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS v4i16 *)at));
+}
+
+template <int WT, int KC>
 struct Frags {
-    u32x4 a[2][WT / 32], b[2][WT / 32];   // [K half]
+    u32x4 a[KC / 16][WT / 32], b[KC / 16][WT / 32];
 };
 
-template <int WT, int MODE>
+template <int WT, int KC, int ST, int MODE>
 __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
-    constexpr int BT = 2 * WT, F = WT / 32;
-    constexpr int kOperand = BT * 64, kStage = 2 * kOperand;
+    constexpr int BT = 2 * WT, F = WT / 32, H = KC / 16;
+    constexpr int kRow = KC * 2, kPieces = KC / 8;
+    constexpr int kOperand = BT * kRow, kStage = 2 * kOperand;
     constexpr int NL = kStage / 1024 / 4;   // direct loads a wave and stage
-    __shared__ __attribute__((aligned(16))) char lds[kStages * kStage];
+    constexpr int kOut = 4 * WT * (WT * 2 + 16);
+    __shared__ __attribute__((aligned(16))) char lds[ST * kStage > kOut ? ST * kStage : kOut];
+    using Fr = Frags<WT, KC>;
+    // the place of a row's 16-byte piece: equal pieces of 16 consecutive rows
+    // fall in the 16 places of a 256-byte window of banks
+    auto swz = [](int row, int piece) { return piece ^ (row / (256 / kRow) % kPieces); };
     const OrthoOne &p = a.p[problem_of(a, blockIdx.x)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
 
     // the tile: rows ti of P, rows tj of Q
-    int ti, tj, t = blockIdx.x - p.start;
+    // (workgroups go round the 8 XCDs: each XCD takes one run of a problem's
+    // tiles, whose operands then meet in its L2)
+    const int wg = blockIdx.x - p.start, per = p.tiles >> 3, more = p.tiles & 7, run = wg & 7;
+    int ti, tj, t = (wg >> 3) + run * per + (run < more ? run : more);
     const int nt = (p.mp + BT - 1) / BT;
     if (MODE == APPLY) {
+        // down panels of 8 rows of tiles
         const int ntn = (p.np + BT - 1) / BT;
-        ti = t / ntn;
-        tj = t % ntn;
+        const int g = t / (8 * ntn), h = nt - 8 * g < 8 ? nt - 8 * g : 8;
+        t -= 8 * g * ntn;
+        ti = 8 * g + t % h;
+        tj = t / h;
     } else {
-        ti = 0;
-        while (t >= nt - ti) {
-            t -= nt - ti;
-            ti++;
+        // the triangle tj >= ti, down panels of 4 rows of tiles
+        int r = 0;
+        while (true) {
+            const int h = nt - r < 4 ? nt - r : 4, n = h * (nt - r) - h * (h - 1) / 2;
+            if (t < n) break;
+            t -= n;
+            r += 4;
         }
-        tj = ti + t;
+        tj = r;
+        for (int h = 1; t >= h; tj++, h += h < 4 && h < nt - r) t -= h;
+        ti = r + t;
     }
     const h16 *P = MODE == GRAM ? p.X : MODE == POLY ? p.A : p.B;
     const h16 *Q = MODE == GRAM ? p.X : MODE == POLY ? p.A : p.XT[a.flip];
     const int K = MODE == GRAM ? p.np : p.mp;
     const int64_t ld = K;
-    const int nk = K / kChunk;
+    const int nk = K / KC;
     const int prow = ti * BT, qrow = tj * BT;
     const int pall = p.mp, qall = MODE == APPLY ? p.np : p.mp;
     const char *pb = (const char *)(P + (int64_t)prow * ld), *qb = (const char *)(Q + (int64_t)qrow * ld);
     const int64_t pbytes = (int64_t)(pall - prow) * ld * 2, qbytes = (int64_t)(qall - qrow) * ld * 2;
 
-    // load i of a wave: 16 rows of 64 bytes; rows past the matrix read zeros
+    // load i of a wave: 1 KiB, whole rows; rows past the matrix read zeros
     uint32_t voff[NL / 2];
 #pragma unroll
     for (int i = 0; i < NL / 2; i++) {
-        const int row = (wave * (NL / 2) + i) * 16 + (lane >> 2);
-        voff[i] = (uint32_t)(row * ld * 2 + (((lane & 3) ^ ((row >> 1) & 3)) * 16));
+        const int row = (wave * (NL / 2) + i) * (64 / kPieces) + lane / kPieces;
+        voff[i] = (uint32_t)(row * ld * 2 + swz(row, lane % kPieces) * 16);
     }
-    auto issue = [&](int s) {
-        char *st = lds + (s & (kStages - 1)) * kStage;
-        const int64_t k = (int64_t)s * kChunk * 2;
-        const __amdgpu_buffer_rsrc_t rp = rsrc(pb + (s < nk ? k : 0), s < nk ? pbytes - k : 0);
-        const __amdgpu_buffer_rsrc_t rq = rsrc(qb + (s < nk ? k : 0), s < nk ? qbytes - k : 0);
-#pragma unroll
-        for (int i = 0; i < NL / 2; i++)
-            load_lds(rp, st + (wave * (NL / 2) + i) * 1024, voff[i]);
-#pragma unroll
-        for (int i = 0; i < NL / 2; i++)
-            load_lds(rq, st + kOperand + (wave * (NL / 2) + i) * 1024, voff[i]);
+    const __amdgpu_buffer_rsrc_t rp = rsrc(pb, pbytes), rq = rsrc(qb, qbytes);
+    // load i of stage s into its place (a stage past the last one loads that
+    // again, unread)
+    auto issue = [&](int s, int place, int i) {
+        char *st = lds + place + (wave * (NL / 2) + i % (NL / 2)) * 1024;
+        const uint32_t k = (uint32_t)(s < nk ? s : nk - 1) * kRow;
+        if (i < NL / 2) load_lds(rp, st, voff[i % (NL / 2)], k);
+        else load_lds(rq, st + kOperand, voff[i % (NL / 2)], k);
     };
     const int lr = lane & 31, lh = lane >> 5;
-    auto read = [&](Frags<WT> &f, int s) {
-        const char *st = lds + (s & (kStages - 1)) * kStage;
+    const int aoff = (wm * WT + lr) * kRow, boff = kOperand + (wn * WT + lr) * kRow;
+    int piece[H];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int piece = ((h * 2 + lh) ^ ((lr >> 1) & 3)) * 16;
-#pragma unroll
-            for (int i = 0; i < F; i++) {
-                f.a[h][i] = *(const u32x4 *)(st + (wm * WT + i * 32 + lr) * 64 + piece);
-                f.b[h][i] = *(const u32x4 *)(st + kOperand + (wn * WT + i * 32 + lr) * 64 + piece);
-            }
-        }
+    for (int h = 0; h < H; h++) piece[h] = swz(lr, h * 2 + lh) * 16;   // rows 32 apart share their permutation
+    // read i of a stage's fragments: those of K 16 h first, P's before Q's
+    auto read = [&](Fr &f, const char *st, int i) {
+        const int h = i / (2 * F), j = i % F;
+        if (i % (2 * F) < F) f.a[h][j] = *(const u32x4 *)(st + aoff + j * 32 * kRow + piece[h]);
+        else f.b[h][j] = *(const u32x4 *)(st + boff + j * 32 * kRow + piece[h]);
     };
     f32x16 acc[F][F];
 #pragma unroll
@@ -255,91 +281,119 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
-    Frags<WT> f0, f1;
-    auto mma = [&](const Frags<WT> &f) {
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-            for (int i = 0; i < F; i++)
-#pragma unroll
-                for (int j = 0; j < F; j++)
-                    acc[i][j] = mfma(f.a[h][i], f.b[h][j], acc[i][j]);
+    Fr f0, f1;
+    constexpr int nm = H * F * F, nr = 2 * H * F;
+    auto product = [&](const Fr &f, int k) {
+        const int h = k / (F * F), i = k / F % F, j = k % F;
+        acc[i][j] = mfma(f.a[h][i], f.b[h][j], acc[i][j]);
     };
-    issue(0);
-    issue(1);
-    issue(2);
-    wait_loads_barrier<2 * NL>();
-    read(f0, 0);
-    // nk is even (K is a multiple of 64)
-    for (int s = 0; s < nk; s += 2) {
-        wait_loads_barrier<NL>();
-        issue(s + 3);
-        read(f1, s + 1);
-        mma(f0);
-        wait_loads_barrier<NL>();
-        issue(s + 4);
-        read(f0, s + 2);
-        mma(f1);
+    // The products of stage s, already in registers, with the reads of the
+    // next stage and the loads of the one ST - 1 ahead dealt out between them
+    // (in a burst they fill the address units' queue and the matrix cores wait
+    // behind it).  The reads are over after three quarters of the products.
+    int here = kStage, there = (ST - 1) * kStage;   // places of stages s + 1 and s + ST - 1
+    auto step = [&](const Fr &f, Fr &next, int s) {
+        wait_loads_barrier<(ST - 3) * NL>();
+        const char *st = lds + here;
+#pragma unroll
+        for (int k = 0; k < nm; k++) {
+            product(f, k);
+            constexpr int span = nm * 3 / 4;
+#pragma unroll
+            for (int i = k * nr / span; i < (k + 1) * nr / span && i < nr; i++) read(next, st, i);
+#pragma unroll
+            for (int i = k * NL / nm; i < (k + 1) * NL / nm; i++) issue(s + ST - 1, there, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        here = here == (ST - 1) * kStage ? 0 : here + kStage;
+        there = there == (ST - 1) * kStage ? 0 : there + kStage;
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; s++)
+#pragma unroll
+        for (int i = 0; i < NL; i++) issue(s, s * kStage, i);
+    wait_loads_barrier<(ST - 2) * NL>();
+#pragma unroll
+    for (int i = 0; i < nr; i++) read(f0, lds, i);
+    for (int s = 0; s + 1 < nk; s += 2) {
+        step(f0, f1, s);
+        step(f1, f0, s + 1);
     }
-    wait_loads_barrier<0>();   // nothing in flight into LDS past the kernel's end
+    if (nk & 1)
+#pragma unroll
+        for (int k = 0; k < nm; k++) product(f0, k);
+    wait_loads_barrier<0>();   // every load has landed and every read is done
 
-    // Results: a lane holds columns (of Q) lr of each block and rows
-    // 8 g + 4 lh + 0..3 (of P), g < 4.
+    // Results.  A lane holds columns (of Q) lr of each block and rows
+    // 8 g + 4 lh + 0..3 (of P), g < 4.  Each wave brings its part through its own
+    // piece of shared memory, T[column][row], from where both orders leave in
+    // 16-byte pieces: T's rows as they lie, and transposed by the transposing
+    // reads.  (Stored from the registers, 8 and 2 bytes a lane, a 256 x 256 tile
+    // took 20 us.)
+    constexpr int kT = WT * 2 + 16;   // bytes of a column of T
+    char *T = lds + wave * WT * kT;
+    const int row0 = prow + wm * WT, col0 = qrow + wn * WT;
+    const h16 *old = MODE == APPLY ? p.XT[a.flip] : p.A;   // its term at [column][row] (A is symmetric)
+    if (MODE != GRAM) {
+#pragma unroll 16
+        for (int i = lane; i < WT * WT / 8; i += 64) {
+            const int c = i / (WT / 8), r = i % (WT / 8) * 8;
+            u32x4 v = {0, 0, 0, 0};
+            if (col0 + c < qall && row0 + r < p.mp) v = *(const u32x4 *)(old + (int64_t)(col0 + c) * p.mp + row0 + r);
+            *(u32x4 *)(T + c * kT + r * 2) = v;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < F; i++)
 #pragma unroll
         for (int j = 0; j < F; j++)
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                const int row = prow + wm * WT + i * 32 + g * 8 + lh * 4, col = qrow + wn * WT + j * 32 + lr;
-                float v[4];
+                h16x4 *at = (h16x4 *)(T + (j * 32 + lr) * kT + (i * 32 + g * 8 + lh * 4) * 2);
+                h16x4 x = {}, o;
+                if (MODE != GRAM) x = *at;
 #pragma unroll
-                for (int r = 0; r < 4; r++) v[r] = acc[i][j][g * 4 + r];
-                if (row >= p.mp || col >= qall) continue;
-                if (MODE == APPLY) {
-                    const int64_t at = (int64_t)col * p.mp + row;
-                    const h16x4 x = *(const h16x4 *)(p.XT[a.flip] + at);
-#pragma unroll
-                    for (int r = 0; r < 4; r++) v[r] = fmaf(kA, (float)x[r], v[r] * (1.0f / 8192.0f));
-                    if (!a.last) {
-                        h16x4 o;
-#pragma unroll
-                        for (int r = 0; r < 4; r++) o[r] = (h16)v[r];
-                        *(h16x4 *)(p.XT[a.flip ^ 1] + at) = o;
-#pragma unroll
-                        for (int r = 0; r < 4; r++) p.X[(int64_t)(row + r) * p.np + col] = o[r];
-                    } else if (col < p.n && row < p.m) {
-                        // row is a multiple of 4 and m of 8: all four rows exist
-                        b16x4 o;
-#pragma unroll
-                        for (int r = 0; r < 4; r++) o[r] = (__bf16)(v[r] * (1.0f / kXScale) * p.gain);
-                        if (p.tall) {
-                            *(b16x4 *)((__bf16 *)p.O + (int64_t)col * p.cols + row) = o;
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; r++) ((__bf16 *)p.O)[(int64_t)(row + r) * p.cols + col] = o[r];
-                        }
-                    }
-                } else {
-                    h16x4 o;
-                    const int64_t at = (int64_t)col * p.mp + row;   // the mirrored place
-                    if (MODE == POLY) {
-                        const h16x4 x = *(const h16x4 *)(p.A + at);   // A is symmetric
-#pragma unroll
-                        for (int r = 0; r < 4; r++)
-                            o[r] = (h16)fmaf(0.5f * kB, (float)x[r], v[r] * (kC / 32768.0f));
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; r++) o[r] = (h16)(v[r] * (1.0f / 16384.0f));
-                    }
-                    h16 *out = MODE == POLY ? p.B : p.A;
-                    *(h16x4 *)(out + at) = o;
-                    if (ti != tj) {
-#pragma unroll
-                        for (int r = 0; r < 4; r++) out[(int64_t)(row + r) * p.mp + col] = o[r];
+                for (int r = 0; r < 4; r++) {
+                    const float v = acc[i][j][g * 4 + r];
+                    if (MODE == GRAM) o[r] = (h16)(v * (1.0f / 16384.0f));
+                    else if (MODE == POLY) o[r] = (h16)fmaf(0.5f * kB, (float)x[r], v * (kC / 32768.0f));
+                    else {
+                        const float y = fmaf(kA, (float)x[r], v * (1.0f / 8192.0f));
+                        o[r] = a.last ? __builtin_bit_cast(h16, (__bf16)(y * (1.0f / kXScale) * p.gain)) : (h16)y;
                     }
                 }
+                *at = o;
             }
+    const bool out = MODE == APPLY && a.last;   // into O, without the padding
+    const int rows = out ? p.m : p.mp, cols = out ? p.n : qall;
+    // [column][row]: X^T, the mirrored tile of A or B, or O of a tall G
+    if (!out || p.tall) {
+        h16 *dst = MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.XT[a.flip ^ 1];
+        const int64_t ldd = out ? p.cols : p.mp;
+#pragma unroll 16
+        for (int i = lane; i < WT * WT / 8; i += 64) {
+            const int c = i / (WT / 8), r = i % (WT / 8) * 8;
+            if (col0 + c < cols && row0 + r < rows)
+                *(u32x4 *)(dst + (int64_t)(col0 + c) * ldd + row0 + r) = *(const u32x4 *)(T + c * kT + r * 2);
+        }
+    }
+    // [row][column]: X, the tile of A or B itself, or O of a wide G
+    if (MODE == APPLY ? !out || !p.tall : ti != tj) {
+        h16 *dst = MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.X;
+        const int64_t ldd = MODE != APPLY ? p.mp : out ? p.cols : p.np;
+        // 16 lanes: 16 rows of 8 columns, four columns a read (lane 4 e + q reads
+        // rows 4 q .. 4 q + 3 of column e and receives row 4 e + q)
+        const int e = lane >> 2 & 3, q = lane & 3, g = lane >> 4;
+#pragma unroll 16
+        for (int i = 0; i < (WT / 16) * (WT / 32); i++) {
+            const int r = i / (WT / 32) * 16, c = i % (WT / 32) * 32 + g * 8;
+            const char *at = T + (c + e) * kT + (r + 4 * q) * 2;
+            const u32x2 lo = transposed(at), hi = transposed(at + 4 * kT);
+            const int row = row0 + r + (lane & 15), col = col0 + c;
+            if (row < rows && col < cols)
+                *(u32x4 *)(dst + (int64_t)row * ldd + col) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+    }
 }
 
 }  // namespace ndev
@@ -380,18 +434,58 @@ bool sizes_ok(int64_t r, int64_t c) {
            cdiv(r, 64) * cdiv(c, 64) <= (1 << 20);
 }
 
-// tiles of a product with edge bt
-int64_t tri_tiles(int64_t mp, int64_t bt) {
-    const int64_t t = cdiv(mp, bt);
-    return t * (t + 1) / 2;
+int64_t tiles_of(int mode, const OrthoOne &p, int wt) {
+    const int64_t r = cdiv(p.mp, 2 * wt);
+    return mode == ndev::APPLY ? r * cdiv(p.np, 2 * wt) : r * (r + 1) / 2;
+}
+
+// The tile shapes, and what a tile costs: us for its first loads, its results
+// and the launch, and us per 32 K, alone on the chip and with every unit busy
+// (measured on the products of 512 x 2048 to 4096 x 16384).  Large tiles need
+// half the operand traffic a flop; small ones fill the chip sooner and
+// start and end faster.
+struct Shape {
+    int wt, per_cu;
+    double fixed, alone, busy;
+};
+constexpr Shape kShapes[] = {{128, 1, 14.0, 0.44, 1.10}, {96, 1, 9.0, 0.32, 0.65}, {64, 1, 6.0, 0.17, 0.33},
+                             {32, 2, 4.5, 0.09, 0.21}};
+
+// The cheapest shape: the launch ends no sooner than its longest tile and
+// than the mean load of a unit.
+int choose_shape(int mode, const OrthoArgs &a) {
+    int best = 0;
+    double least = 0.0;
+    for (const Shape &s : kShapes) {
+        double sum = 0.0, longest = 0.0, tiles = 0.0;
+        for (int i = 0; i < a.n; i++) {
+            const double n = (double)tiles_of(mode, a.p[i], s.wt);
+            const double k = (mode == ndev::GRAM ? a.p[i].np : a.p[i].mp) / 32.0;
+            tiles += n;
+            sum += n * k;
+            longest = k > longest ? k : longest;
+        }
+        const double slots = 256.0 * s.per_cu, load = tiles < slots ? tiles / slots : 1.0;
+        const double k = sum / slots > longest ? sum / slots : longest;
+        const double t = s.fixed + k * (s.alone + (s.busy - s.alone) * load);
+        if (!best || t < least) best = s.wt, least = t;
+    }
+    return best;
 }
 
 template <int MODE>
-void launch_product(int wt, int64_t wgs, const OrthoArgs &a, hipStream_t st) {
+void launch_product(int wt, OrthoArgs &a, hipStream_t st) {
+    int64_t wgs = 0;
+    for (int i = 0; i < a.n; i++) {
+        a.p[i].start = (int)wgs;
+        a.p[i].tiles = (int)tiles_of(MODE, a.p[i], wt);
+        wgs += a.p[i].tiles;
+    }
     const dim3 g((unsigned)wgs), b(256);
-    if (wt == 128) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<128, MODE>), g, b, 0, st, a);
-    else if (wt == 64) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<64, MODE>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((ndev::ortho_gemm_kernel<32, MODE>), g, b, 0, st, a);
+    if (wt == 128) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<128, 32, 4, MODE>), g, b, 0, st, a);
+    else if (wt == 96) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<96, 32, 4, MODE>), g, b, 0, st, a);
+    else if (wt == 64) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<64, 64, 5, MODE>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((ndev::ortho_gemm_kernel<32, 64, 5, MODE>), g, b, 0, st, a);
 }
 
 }  // namespace
@@ -441,7 +535,6 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
     OrthoArgs a{};
     a.g_bf16 = g_dtype == TERN_BF16;
     size_t at = 0;
-    int64_t tiles = 0;
     for (int i = 0; i < n; i++) {
         if (mats[i].rows == 0 || mats[i].cols == 0) continue;
         const OrthoLayout L = layout(mats[i].rows, mats[i].cols);
@@ -463,32 +556,22 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
     if (a.n == 0) return TERN_OK;
     hipStream_t st = (hipStream_t)stream;
     hipLaunchKernelGGL(ndev::ortho_norm_kernel, dim3(ndev::kParts, (unsigned)a.n), dim3(256), 0, st, a);
-    // the first workgroup of every problem in each kind of launch
-    auto starts = [&](int kind, int bt) {
-        int64_t s = 0;
-        for (int i = 0; i < a.n; i++) {
-            OrthoOne &p = a.p[i];
-            p.start = (int)s;
-            s += kind == ndev::APPLY ? cdiv(p.mp, bt) * cdiv(p.np, bt) : tri_tiles(p.mp, bt);
-        }
-        return s;
-    };
-    tiles = starts(ndev::APPLY, 64);
+    int64_t tiles = 0;
+    for (int i = 0; i < a.n; i++) {
+        a.p[i].start = (int)tiles;
+        tiles += (int64_t)(a.p[i].mp / 64) * (a.p[i].np / 64);
+    }
     hipLaunchKernelGGL(ndev::ortho_load_kernel, dim3((unsigned)tiles), dim3(256), 0, st, a);
-    auto tile_for = [&](int kind) {
-        for (int wt : {128, 64})
-            if (starts(kind, 2 * wt) >= 192) return wt;
-        return 32;
-    };
-    const int wt_tri = tile_for(ndev::GRAM), wt_app = tile_for(ndev::APPLY);
+    // the longest sums first
+    std::stable_sort(a.p, a.p + a.n, [](const OrthoOne &x, const OrthoOne &y) { return x.np > y.np; });
+    const int gram = choose_shape(ndev::GRAM, a), poly = choose_shape(ndev::POLY, a),
+              apply = choose_shape(ndev::APPLY, a);
     for (int s = 0; s < steps; s++) {
         a.flip = s & 1;
         a.last = s == steps - 1;
-        const int64_t tri = starts(ndev::GRAM, 2 * wt_tri);
-        launch_product<ndev::GRAM>(wt_tri, tri, a, st);
-        launch_product<ndev::POLY>(wt_tri, tri, a, st);
-        const int64_t app = starts(ndev::APPLY, 2 * wt_app);
-        launch_product<ndev::APPLY>(wt_app, app, a, st);
+        launch_product<ndev::GRAM>(gram, a, st);
+        launch_product<ndev::POLY>(poly, a, st);
+        launch_product<ndev::APPLY>(apply, a, st);
     }
     return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP;
 }

@@ -10,10 +10,21 @@
 //
 // A step is an affine map of the state, h -> (1 - w) h + w v, and affine maps
 // compose to affine maps (A, B): h -> A h + B.  So the T tokens (the packed
-// sequences laid end to end) are cut into chunks of `L` rows:
-//   recur_agg    the pair (A, B) of every chunk, from K and V;
-//   recur_carry  the state that enters every chunk, by composing the pairs;
-//   recur_fwd    the tokens again from the entering state, writing Y.
+// sequences laid end to end) are cut into chunks of a workgroup, 16 rows a wave,
+// and one pass over the data does:
+//   - every wave loads its rows into registers and composes their pair;
+//   - the workgroup publishes the chunk's pair, and finds the state that enters
+//     the chunk from the nearest chunk before it whose closing state is known
+//     and the pairs in between;
+//   - it publishes its own closing state, and every wave walks its rows again
+//     in registers, from the state that enters them, and writes Y.
+// K, V, R are read once and Y is written once (32768 x 4096 bf16 in one sequence:
+// 279 us, 3.9 TB/s of the 5.1 of a copy; with the pairs, the chain and the
+// output in three launches that read K and V twice 345 us).  What bounds it is
+// the time a chunk's registers are held: the loads, about 3 us for the words of
+// other chunks, the output.  The pairs in between are
+// applied in order to the state found, the same operations whichever chunk
+// that was: results do not depend on timing.
 // A sequence's first token drops what came before: the composition restarts
 // there with A = 0 and B = h0, and a pair with A = 0 returns B without
 // multiplying, so nothing of one sequence (a NaN, an infinity) reaches the
@@ -23,10 +34,13 @@
 //   g_t = u_t + (1 - w_{t+1}) g_{t+1}   (+ dhT behind the last token)
 //   dv = g w,  dk = g (v - h_{t-1}) w (1 - w),  dr = dy h s (1 - s)
 // p_t = (1 - w_t) g_t, the gradient of h_{t-1}, is again an affine chain, run
-// from the last token to the first, and cut into the same chunks.  The states
-// h_{t-1} come from the forward's checkpoints (one row every 16 tokens).
+// from the last token to the first, through the same chunks in reverse.  The
+// states h_{t-1} come from the forward's checkpoints (one row every 16 tokens).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "../../include/tern.h"
 #include "tern_cursor.h"
@@ -44,13 +58,15 @@ struct RecurArgs {
     const int64_t *off;        // [S + 1] or null (one sequence of T tokens)
     int64_t S, T;
     int C, ncb;                // channels; column blocks of a wave
-    int L, nch;                // rows of a chunk; chunks
+    int nch;                   // chunks
+    unsigned wgs;              // workgroups that take chunks
     void *Y;                   // [T, C], row stride ldy
     int64_t ldy;
     float *hT;                 // [S, C] or null
     float *states;             // [ceil(T / 16), C]: the state before each 16-row block
-    float *agg;                // [nch][2][C]
-    float *carry;              // [nch][C], or null with one chunk
+    unsigned long long *agg;   // [nch][C]: pairs of the chunks, in chain order
+    uint32_t *prefix;          // [nch][C]: states behind the chunks
+    uint32_t *ticket;          // [ncb], 128 bytes apart
     const void *dY;            // [T, C], row stride lddy
     int64_t lddy;
     const float *dhT;          // [S, C] or null (zeros)
@@ -59,83 +75,116 @@ struct RecurArgs {
     float *dh0;                // [S, C] or null
 };
 
-// One lane's channels: 4 bytes of a row (256 consecutive bytes a wave).
+// One lane's channels of a row: N of ES bytes.
+__device__ inline uint32_t round_bf16(float f) {   // to nearest even (NaN stays NaN)
+    return __builtin_bit_cast(unsigned short, (__bf16)f);
+}
 struct Bf {
-    static constexpr int N = 2;
+    static constexpr int N = 2, ES = 2;
     using Raw = uint32_t;
     __device__ static void unpack(Raw x, float *f) {
         f[0] = __builtin_bit_cast(float, x << 16);
         f[1] = __builtin_bit_cast(float, x & 0xFFFF0000u);
     }
-    // round to nearest even (NaN stays NaN)
-    __device__ static Raw pack(const float *f) {
-        Raw r = 0;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const __bf16 b = (__bf16)f[i];
-            r |= (Raw)__builtin_bit_cast(unsigned short, b) << (16 * i);
-        }
-        return r;
-    }
+    __device__ static Raw pack(const float *f) { return round_bf16(f[0]) | round_bf16(f[1]) << 16; }
+};
+struct Bh {
+    static constexpr int N = 1, ES = 2;
+    using Raw = uint16_t;
+    __device__ static void unpack(Raw x, float *f) { f[0] = __builtin_bit_cast(float, (uint32_t)x << 16); }
+    __device__ static Raw pack(const float *f) { return (Raw)round_bf16(f[0]); }
 };
 struct Fp {
-    static constexpr int N = 1;
+    static constexpr int N = 1, ES = 4;
     using Raw = float;
     __device__ static void unpack(Raw x, float *f) { f[0] = x; }
     __device__ static Raw pack(const float *f) { return f[0]; }
 };
 
+// a lane's channels of an fp32 row (8-byte aligned where there are two)
 template <int N>
 __device__ inline void load_f(const float *p, float *f) {
-#pragma unroll
-    for (int i = 0; i < N; i++) f[i] = p[i];
+    if constexpr (N == 2) {
+        const float2 v = *(const float2 *)p;
+        f[0] = v.x, f[1] = v.y;
+    } else {
+        f[0] = *p;
+    }
 }
 template <int N>
 __device__ inline void store_f(float *p, const float *f) {
-#pragma unroll
-    for (int i = 0; i < N; i++) p[i] = f[i];
+    if constexpr (N == 2) *(float2 *)p = float2{f[0], f[1]};
+    else *p = f[0];
 }
 
 __device__ inline float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * -1.44269504088896340736f); }
 __device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(x)); }
 
-// sigmoid(x) and its derivative sigmoid(x) sigmoid(-x), neither by a
-// difference that would cancel where the gate saturates
-__device__ inline float sigmoid_d(float x, float &d) {
-    const float e = exp_neg(fabsf(x));
-    const float i = __builtin_amdgcn_rcpf(1.0f + e);
-    d = e * i * i;
-    return x < 0.0f ? e * i : i;
+// sigmoid(x) and sigmoid(-x), neither by a difference that would cancel where
+// the gate saturates
+__device__ inline void gates(float x, float &on, float &off) {
+    const float e = exp_neg(fabsf(x)), i = __builtin_amdgcn_rcpf(1.0f + e), j = e * i;
+    on = x < 0.0f ? j : i;
+    off = x < 0.0f ? i : j;
 }
 
-// wave-uniform position of the wave: column block and chunk (or, beyond the
-// chunks, a group of 64 sequences)
-__device__ inline void wave_pos(const RecurArgs &a, int &c, int64_t &y) {
-    const int64_t b = blockIdx.x;
-    y = b / a.ncb;
-    c = (int)(b - y * a.ncb);
+// A cursor with the borders of its sequence at hand (the offsets are in memory).
+struct Span {
+    Cursor c;
+    int64_t b, e;
+    bool live;
+    __device__ void look() {
+        b = c.begin();
+        e = c.end();
+        live = c.live();
+    }
+    __device__ Span(const RecurArgs &a, int64_t t) : c{a.off, a.S, a.T, 0} {
+        c.seek(t);
+        look();
+    }
+    __device__ void forth(int64_t t) {
+        if (t < e) return;
+        c.forth(t);
+        look();
+    }
+    __device__ void back(int64_t t) {
+        if (t >= b) return;
+        c.back(t);
+        look();
+    }
+};
+
+// Is t the border between two sequences, or that behind the last one?
+__device__ inline bool starts_at(const RecurArgs &a, int64_t t) {
+    Cursor c{a.off, a.S, a.T, 0};
+    c.seek(t);
+    return c.cur > 0 && c.begin() == t;
 }
 
 // The rows of one checkpoint block (rows beyond the chunk's end repeat its
 // last one), all loads issued together.
-template <class E>
-__device__ inline void load_rows(typename E::Raw *x, const void *p, int64_t ld, int64_t tb, int64_t t1, int col) {
-    constexpr int es = 4 / E::N;
-    const char *base = (const char *)p + (tb * ld + col) * es;
-#pragma unroll
-    for (int j = 0; j < kBlk; j++) {
-        const int64_t r = tb + j < t1 ? j : t1 - 1 - tb;
-        x[j] = *(const typename E::Raw *)(base + r * ld * es);
-    }
+// A row's address is uniform in a wave, and lanes add 32 bits to it: that keeps
+// the addresses of 16 rows out of the vector registers.
+template <class T>
+__device__ inline T *at_row(T *p, int64_t row, int64_t ld, int es, uint32_t lane_bytes) {
+    using C = std::conditional_t<std::is_const_v<T>, const char, char>;
+    return (T *)((C *)p + row * ld * es + lane_bytes);
 }
-
-// Keeps loads that were issued before it from sinking to their uses.
-__device__ inline void issued() { __builtin_amdgcn_sched_barrier(0); }
+template <class E>
+__device__ inline void load_rows(typename E::Raw *x, const void *p, int64_t ld, int64_t tb, int64_t t1, uint32_t lane) {
+#pragma unroll
+    for (int j = 0; j < kBlk; j++)
+        x[j] = *(const typename E::Raw *)at_row(p, tb + j < t1 ? tb + j : t1 - 1, ld, E::ES, lane);
+}
+template <class E>
+__device__ inline void store_row(void *p, int64_t row, int64_t ld, uint32_t lane, const float *f) {
+    *(typename E::Raw *)at_row(p, row, ld, E::ES, lane) = E::pack(f);
+}
 
 // Sequences without tokens pass their state through: dst[s] = src[s].
 template <int N>
 __device__ inline void copy_empty(const RecurArgs &a, int64_t group, int col, const float *src, float *dst) {
-    const int64_t s = group * 64 + threadIdx.x;
+    const int64_t s = group * 64 + (threadIdx.x & 63);
     bool e = false;
     if (s < a.S) e = a.off ? a.off[s + 1] <= a.off[s] : a.T == 0;
     uint64_t m = __ballot(e);
@@ -150,375 +199,459 @@ __device__ inline void copy_empty(const RecurArgs &a, int64_t group, int col, co
     }
 }
 
-// (A, B) of a chunk in token order
-template <class E>
-__global__ __launch_bounds__(64) void recur_agg_kernel(RecurArgs a) {
-    constexpr int N = E::N;
-    using Raw = typename E::Raw;
-    int cb;
-    int64_t ch;
-    wave_pos(a, cb, ch);
-    const int col = (cb * 64 + (int)threadIdx.x) * N;
-    if (col >= a.C) return;
-    const int64_t t0 = ch * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    Cursor cu{a.off, a.S, a.T, 0};
-    cu.seek(t0);
-    int64_t nb = cu.end();
-    bool first = cu.live() && cu.begin() == t0;
-    float A[N], B[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
-    auto row = [&](Raw kr, Raw vr) {
-        float kf[N], vf[N];
-        E::unpack(kr, kf);
-        E::unpack(vr, vf);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float w = sigmoid(kf[i]);
-            A[i] = fmaf(-w, A[i], A[i]);
-            B[i] = fmaf(w, vf[i] - B[i], B[i]);
-        }
-    };
-    Raw k[kBlk], v[kBlk];
-    load_rows<E>(k, a.K, a.ld, t0, t1, col);
-    load_rows<E>(v, a.V, a.ld, t0, t1, col);
-    for (int64_t tb = t0; tb < t1; tb += kBlk) {
-        // the next block's loads fly while this one is worked on
-        const int64_t tn = tb + kBlk < t1 ? tb + kBlk : tb;
-        Raw k2[kBlk], v2[kBlk];
-        load_rows<E>(k2, a.K, a.ld, tn, t1, col);
-        load_rows<E>(v2, a.V, a.ld, tn, t1, col);
-        issued();
-        if (!first && cu.live() && nb >= tb + kBlk && tb + kBlk <= t1) {
-#pragma unroll
-            for (int j = 0; j < kBlk; j++) row(k[j], v[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kBlk; j++) {
-                const int64_t t = tb + j;
-                if (t >= t1) continue;
-                if (t >= nb) {
-                    cu.forth(t);
-                    nb = cu.end();
-                    first = cu.live();
-                }
-                if (first) {
-                    first = false;
-#pragma unroll
-                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
-                    if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, B);
-                }
-                if (cu.live()) row(k[j], v[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kBlk; j++) k[j] = k2[j], v[j] = v2[j];
-    }
-    float *g = a.agg + ch * 2 * a.C + col;
-    store_f<N>(g, A);
-    store_f<N>(g + a.C, B);
-}
-
 // (A, B) applied to h, and the A of (A1, B1) after (A0, B0).  A = 0 forgets
 // what came before, whatever it holds.
 __device__ inline float apply(float A, float B, float h) { return A == 0.0f ? B : fmaf(A, h, B); }
 __device__ inline float compose(float A1, float A0) { return A1 == 0.0f ? 0.0f : A1 * A0; }
 
-// carry[ch] = the state entering chunk ch (REV: chunks in descending order).
-// 16 columns x 64 segments of chunks: every thread composes its segment's
-// pairs, the segments are scanned by doubling in shared memory, and every
-// thread walks its segment again from the state that enters it.
-template <bool REV>
-__global__ __launch_bounds__(1024) void recur_carry_kernel(RecurArgs a) {
-    __shared__ float sA[64][17], sB[64][17];
-    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-    const int col = blockIdx.x * 16 + x;
-    const bool in = col < a.C;
-    const int per = (a.nch + 63) / 64;
-    const int i0 = y * per, i1 = i0 + per < a.nch ? i0 + per : a.nch;
-    auto ch = [&](int i) { return (int64_t)(REV ? a.nch - 1 - i : i); };
-    float A = 1.0f, B = 0.0f;
-    if (in)
-        for (int i = i0; i < i1; i++) {
-            const float *g = a.agg + ch(i) * 2 * a.C + col;
-            const float A1 = g[0], B1 = g[a.C];
-            B = apply(A1, B1, B);
-            A = compose(A1, A);
+// ---------------------------------------------------------------------------
+// The chain of chunks.  A pair (A, B) and a state are published as one 64-bit
+// and one 32-bit word that validate themselves: the workspace is filled with
+// ones beforehand (recur_init), and a value that would be all ones is stored
+// as another NaN.  The words are written and read past the XCDs' L2 caches
+// (agent scope), each by one access; nothing else has to be ordered with them.
+//
+// Workgroups take their chunk of a column block from a counter, in chain
+// order, so whoever waits for an earlier chunk waits for a workgroup that runs
+// already; that one publishes its pair before it waits for anything, and the
+// first chunk waits for nothing: every wait ends.
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kEmpty = 0xFFFFFFFFu;
+constexpr int kTicketStride = 32;   // words
+constexpr int kBack = 16;           // chunks looked back over
+
+__device__ inline uint32_t word_of(float x) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, x);
+    return w == kEmpty ? 0x7FC00000u : w;
+}
+__device__ inline void publish_pair(unsigned long long *p, float A, float B) {
+    __hip_atomic_store(p, (unsigned long long)word_of(A) | (unsigned long long)__builtin_bit_cast(uint32_t, B) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void publish_state(uint32_t *p, float h) {
+    __hip_atomic_store(p, word_of(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline unsigned long long pair_at(const unsigned long long *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline uint32_t state_at(const uint32_t *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(256) void recur_init_kernel(uint4 *empty, int64_t n16, uint32_t *ticket, int ncb) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n16) empty[i] = uint4{kEmpty, kEmpty, kEmpty, kEmpty};
+    if (i < ncb) ticket[i * kTicketStride] = 0;
+}
+
+// Lanes 0 .. 15 watch one column of the 16 chunks before chunk i until one has
+// its state and all chunks after that their pairs.
+__device__ inline void watch(const RecurArgs &a, int i, int col0) {
+    const int lane = threadIdx.x & 63, p = i - 1 - lane;
+    while (true) {
+        bool has_state = lane < kBack && p < 0, has_pair = false;   // before the first chunk the state is zero
+        if (lane < kBack && p >= 0) {
+            has_state = state_at(a.prefix + (int64_t)p * a.C + col0) != kEmpty;
+            has_pair = (uint32_t)pair_at(a.agg + (int64_t)p * a.C + col0) != kEmpty;
         }
-    sA[y][x] = A;
-    sB[y][x] = B;
+        const uint32_t states = (uint32_t)__ballot(has_state), pairs = (uint32_t)__ballot(has_pair);
+        const int d = states ? __builtin_ctz(states) : kBack;   // chunks in between
+        if (d < kBack && (~pairs & ((1u << d) - 1)) == 0) return;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// The state that enters each wave's rows; `order` is the wave's place in the
+// chain.  The waves' pairs meet in shared memory; the first wave composes and
+// publishes the chunk's.  A chunk in which a sequence starts (A = 0) closes with
+// the state B whatever enters it, and publishes that at once; one that begins
+// with a sequence's start (`fresh`) needs no state at all.  Work that does not
+// need the state is done in `between`, while the other chunks' words arrive.
+// Then all waves fetch the words of the 16 chunks before
+// (one trip to memory), the first finds the state before the chunk in them and
+// publishes the one behind it.
+template <int N, int W, class Between>
+__device__ inline void enter(const RecurArgs &a, int i, int order, bool fresh, int col, int col0, float *A, float *B,
+                             float *h, Between between) {
+    constexpr int J = kBack / W;   // chunks a wave fetches
+    __shared__ float sA[W][64 * N], sB[W][64 * N], sH[64 * N];
+    __shared__ unsigned long long sPair[kBack][64 * N];
+    __shared__ uint32_t sState[kBack][64 * N];
+    __shared__ int sKnown, sClosed, sHas[kBack];
+    const int at = (threadIdx.x & 63) * N;
+    store_f<N>(&sA[order][at], A);
+    store_f<N>(&sB[order][at], B);
     __syncthreads();
-    for (int d = 1; d < 64; d <<= 1) {
-        float A0 = 1.0f, B0 = 0.0f;
-        if (y >= d) A0 = sA[y - d][x], B0 = sB[y - d][x];
-        __syncthreads();
-        if (y >= d) {
-            sB[y][x] = apply(sA[y][x], sB[y][x], B0);
-            sA[y][x] = compose(sA[y][x], A0);
+#pragma unroll
+    for (int k = 0; k < N; k++) h[k] = 0.0f;
+    if (a.nch > 1) {
+        if (order == 0) {
+#pragma unroll
+            for (int q = 1; q < W; q++)
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    const float A1 = sA[q][at + k];
+                    B[k] = apply(A1, sB[q][at + k], B[k]);
+                    A[k] = compose(A1, A[k]);
+                }
+            bool closed = true;
+#pragma unroll
+            for (int k = 0; k < N; k++) closed = closed && A[k] == 0.0f;
+            closed = i == 0 || fresh || __ballot(col < a.C && !closed) == 0;
+            if (col < a.C)
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    if (closed) publish_state(a.prefix + (int64_t)i * a.C + col + k, apply(A[k], B[k], 0.0f));
+                    else publish_pair(a.agg + (int64_t)i * a.C + col + k, A[k], B[k]);
+                }
+            sClosed = closed;
+            sKnown = i == 0 || fresh;
         }
         __syncthreads();
     }
-    float h = y ? sB[y - 1][x] : 0.0f;   // the state before the first chunk is zero
-    if (in)
-        for (int i = i0; i < i1; i++) {
-            const float *g = a.agg + ch(i) * 2 * a.C + col;
-            a.carry[ch(i) * a.C + col] = h;
-            h = apply(g[0], g[a.C], h);
+    between();
+    if (a.nch > 1) {
+        // lanes past the last column take part with the last ones
+        const int c = col < a.C ? col : a.C - N;
+        for (bool first = true; !sKnown; first = false) {
+            if (!first) watch(a, i, col0);
+            unsigned long long pr[J][N];
+            uint32_t st[J][N];
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const int p = i - 1 - (order * J + j);
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    pr[j][k] = p < 0 ? 0 : pair_at(a.agg + (int64_t)p * a.C + c + k);
+                    st[j][k] = p < 0 ? 0 : state_at(a.prefix + (int64_t)p * a.C + c + k);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const int d = order * J + j;
+                bool has_state = true, has_pair = true;
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    sPair[d][at + k] = pr[j][k];
+                    sState[d][at + k] = st[j][k];
+                    has_state = has_state && st[j][k] != kEmpty;
+                    has_pair = has_pair && (uint32_t)pr[j][k] != kEmpty;
+                }
+                const uint64_t no_state = __ballot(!has_state), no_pair = __ballot(!has_pair);
+                if ((threadIdx.x & 63) == 0) sHas[d] = (no_state == 0) | (no_pair == 0) << 1;
+            }
+            __syncthreads();
+            if (order == 0) {
+                // the nearest chunk whose state is there for every column, and
+                // the pairs of those behind it
+                const int has = sHas[threadIdx.x & (kBack - 1)];
+                const uint32_t states = (uint32_t)__ballot(has & 1) & ((1u << kBack) - 1);
+                const uint32_t pairs = (uint32_t)__ballot(has & 2);
+                const int from = states ? __builtin_ctz(states) : kBack;
+                const bool all = from < kBack && (~pairs & ((1u << from) - 1)) == 0;
+                if (all) {
+#pragma unroll
+                    for (int k = 0; k < N; k++) h[k] = __builtin_bit_cast(float, sState[from][at + k]);
+#pragma unroll 4
+                    for (int d = from - 1; d >= 0; d--)
+#pragma unroll
+                        for (int k = 0; k < N; k++) {
+                            const unsigned long long pr = sPair[d][at + k];
+                            h[k] = apply(__builtin_bit_cast(float, (uint32_t)pr),
+                                         __builtin_bit_cast(float, (uint32_t)(pr >> 32)), h[k]);
+                        }
+                }
+                if (all && !sClosed && col < a.C)
+#pragma unroll
+                    for (int k = 0; k < N; k++)
+                        publish_state(a.prefix + (int64_t)i * a.C + col + k, apply(A[k], B[k], h[k]));
+                if (all) store_f<N>(&sH[at], h);
+                sKnown = all;
+            }
+            __syncthreads();
         }
+        if (i > 0 && !fresh) load_f<N>(&sH[at], h);
+    }
+    for (int q = 0; q < order; q++)
+#pragma unroll
+        for (int k = 0; k < N; k++) h[k] = apply(sA[q][at + k], sB[q][at + k], h[k]);
 }
 
-// Y, hT and the checkpoints of a chunk from the state that enters it
-template <class E>
-__global__ __launch_bounds__(64) void recur_fwd_kernel(RecurArgs a) {
+// The workgroup's next place in its column block's chain
+__device__ inline int take_ticket(const RecurArgs &a, int cb) {
+    __shared__ int t;
+    if (a.nch == 1) return 0;
+    if (threadIdx.x == 0)
+        t = (int)__hip_atomic_fetch_add(a.ticket + cb * kTicketStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(t);
+}
+
+template <class E, int W>
+__device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, int ch) {
     constexpr int N = E::N;
     using Raw = typename E::Raw;
-    int cb;
-    int64_t ch;
-    wave_pos(a, cb, ch);
-    const int col = (cb * 64 + (int)threadIdx.x) * N;
-    if (ch >= a.nch) {
-        if (a.hT) copy_empty<N>(a, ch - a.nch, col, a.h0, a.hT);
-        return;
-    }
-    if (col >= a.C) return;
-    const int64_t t0 = ch * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    Cursor cu{a.off, a.S, a.T, 0};
-    cu.seek(t0);
-    int64_t nb = cu.end();
-    bool first = cu.live() && cu.begin() == t0;
-    float h[N] = {};
-    if (a.carry) load_f<N>(a.carry + ch * a.C + col, h);
-    auto row = [&](Raw kr, Raw vr, Raw rr, int64_t t) {
-        float kf[N], vf[N], rf[N], y[N];
-        E::unpack(kr, kf);
-        E::unpack(vr, vf);
-        E::unpack(rr, rf);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            h[i] = fmaf(sigmoid(kf[i]), vf[i] - h[i], h[i]);
-            y[i] = sigmoid(rf[i]) * h[i];
+    const uint32_t lb = (uint32_t)col * E::ES;
+    const int64_t t0 = ((int64_t)ch * W + wave) * kBlk, t1 = t0 + kBlk < a.T ? t0 + kBlk : a.T;
+    const bool on = col < a.C && t0 < a.T;
+    float w[kBlk][N];
+    Raw v[kBlk], r[kBlk];
+    {
+        Raw k[kBlk];
+        if (on) {
+            load_rows<E>(k, a.K, a.ld, t0, t1, lb);
+            load_rows<E>(v, a.V, a.ld, t0, t1, lb);
+            load_rows<E>(r, a.R, a.ld, t0, t1, lb);
         }
-        *(Raw *)((char *)a.Y + (t * a.ldy + col) * (4 / N)) = E::pack(y);
-    };
-    Raw k[kBlk], v[kBlk], r[kBlk];
-    load_rows<E>(k, a.K, a.ld, t0, t1, col);
-    load_rows<E>(v, a.V, a.ld, t0, t1, col);
-    load_rows<E>(r, a.R, a.ld, t0, t1, col);
-    for (int64_t tb = t0; tb < t1; tb += kBlk) {
-        const int64_t tn = tb + kBlk < t1 ? tb + kBlk : tb;
-        Raw k2[kBlk], v2[kBlk], r2[kBlk];
-        load_rows<E>(k2, a.K, a.ld, tn, t1, col);
-        load_rows<E>(v2, a.V, a.ld, tn, t1, col);
-        load_rows<E>(r2, a.R, a.ld, tn, t1, col);
-        issued();
-        if (a.states) store_f<N>(a.states + tb / kBlk * a.C + col, h);
-        if (!first && cu.live() && nb > tb + kBlk && tb + kBlk <= t1) {
 #pragma unroll
-            for (int j = 0; j < kBlk; j++) row(k[j], v[j], r[j], tb + j);
+        for (int j = 0; j < kBlk; j++) {
+            float kf[N];
+            E::unpack(k[j], kf);
+#pragma unroll
+            for (int i = 0; i < N; i++) w[j][i] = sigmoid(kf[i]);
+        }
+    }
+    Span at(a, t0);
+    // no sequence starts or ends inside the rows, and they are all there
+    const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
+    float A[N], B[N], h[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
+    if (on) {
+        auto row = [&](int j) {
+            float vf[N];
+            E::unpack(v[j], vf);
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                A[i] = fmaf(-w[j][i], A[i], A[i]);
+                B[i] = fmaf(w[j][i], vf[i] - B[i], B[i]);
+            }
+        };
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < kBlk; j++) row(j);
         } else {
+            Span s = at;
 #pragma unroll
             for (int j = 0; j < kBlk; j++) {
-                const int64_t t = tb + j;
+                const int64_t t = t0 + j;
                 if (t >= t1) continue;
-                if (t >= nb) {
-                    cu.forth(t);
-                    nb = cu.end();
-                    first = cu.live();
-                }
-                if (first) {
-                    first = false;
+                s.forth(t);
+                if (!s.live) continue;
+                if (t == s.b) {
 #pragma unroll
-                    for (int i = 0; i < N; i++) h[i] = 0.0f;
-                    if (a.h0) load_f<N>(a.h0 + cu.cur * a.C + col, h);
+                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
+                    if (a.h0) load_f<N>(a.h0 + s.c.cur * a.C + col, B);
                 }
-                if (!cu.live()) continue;
-                row(k[j], v[j], r[j], t);
-                if (a.hT && t + 1 == nb) store_f<N>(a.hT + cu.cur * a.C + col, h);
+                row(j);
             }
         }
+    }
+    // does the chunk begin with a sequence's start?
+    const bool fresh = starts_at(a, (int64_t)ch * W * kBlk);
+    enter<N, W>(a, ch, wave, fresh, col, cb * 64 * N, A, B, h, [] {});
+    if (!on) return;
+    if (a.states) store_f<N>((float *)at_row(a.states, t0 / kBlk, a.C, 4, (uint32_t)col * 4), h);
+    auto row = [&](int j) {
+        float vf[N], rf[N], o[N];
+        E::unpack(v[j], vf);
+        E::unpack(r[j], rf);
 #pragma unroll
-        for (int j = 0; j < kBlk; j++) k[j] = k2[j], v[j] = v2[j], r[j] = r2[j];
-    }
-}
-
-// dY of one token, in the activations' type or in fp32
-template <class E, class D>
-__device__ inline void load_dy(const RecurArgs &a, int64_t t, int col, float *f) {
-    if constexpr (D::N == E::N) {
-        D::unpack(*(const typename D::Raw *)((const char *)a.dY + (t * a.lddy + col) * (4 / D::N)), f);
+        for (int i = 0; i < N; i++) {
+            h[i] = fmaf(w[j][i], vf[i] - h[i], h[i]);
+            o[i] = sigmoid(rf[i]) * h[i];
+        }
+        store_row<E>(a.Y, t0 + j, a.ldy, lb, o);
+    };
+    if (plain) {
+#pragma unroll
+        for (int j = 0; j < kBlk; j++) row(j);
     } else {
-        load_f<E::N>((const float *)a.dY + t * a.lddy + col, f);
+#pragma unroll
+        for (int j = 0; j < kBlk; j++) {
+            const int64_t t = t0 + j;
+            if (t >= t1) continue;
+            at.forth(t);
+            if (!at.live) continue;
+            if (t == at.b) {
+#pragma unroll
+                for (int i = 0; i < N; i++) h[i] = 0.0f;
+                if (a.h0) load_f<N>(a.h0 + at.c.cur * a.C + col, h);
+            }
+            row(j);
+            if (a.hT && t + 1 == at.e) store_f<N>(a.hT + at.c.cur * a.C + col, h);
+        }
     }
 }
 
-// (A, B) of a chunk for p_t, in descending token order
+// A workgroup for every chunk; behind those, one for every column block and 64
+// sequences passes on the empty ones' states.
+template <class E, int W>
+__global__ __launch_bounds__(64 * W, 4) void recur_fwd_kernel(RecurArgs a) {
+    const int b = blockIdx.x < a.wgs ? blockIdx.x : blockIdx.x - a.wgs, cb = b % a.ncb;
+    const int col = (cb * 64 + (int)(threadIdx.x & 63)) * E::N;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x >= a.wgs) {
+        if (wave == 0) copy_empty<E::N>(a, b / a.ncb, col, a.h0, a.hT);
+        return;
+    }
+    fwd_chunk<E, W>(a, cb, col, wave, take_ticket(a, cb));
+}
+
+// dY of one token, in the activations' type (D = E) or in fp32
 template <class E, class D>
-__global__ __launch_bounds__(64) void recur_bagg_kernel(RecurArgs a) {
+struct Grad {
+    using Raw = std::conditional_t<std::is_same_v<D, E>, typename E::Raw, std::conditional_t<E::N == 2, float2, float>>;
+    Raw x;
+    __device__ void load(const RecurArgs &a, int64_t t, int col) {
+        x = *(const Raw *)at_row(a.dY, t, a.lddy, D::ES, (uint32_t)col * D::ES);
+    }
+    __device__ void get(float *f) const {
+        if constexpr (std::is_same_v<D, E>) E::unpack(x, f);
+        else __builtin_memcpy(f, &x, sizeof x);
+    }
+};
+
+template <class E, class D, int W>
+__device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, int link) {
     constexpr int N = E::N;
-    int cb;
-    int64_t ch;
-    wave_pos(a, cb, ch);
-    const int col = (cb * 64 + (int)threadIdx.x) * N;
-    if (col >= a.C) return;
-    const int64_t t0 = ch * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    Cursor cu{a.off, a.S, a.T, 0};
-    cu.seek(t1 - 1);
+    using Raw = typename E::Raw;
+    const uint32_t lb = (uint32_t)col * E::ES;
+    const int64_t t0 = ((int64_t)(a.nch - 1 - link) * W + wave) * kBlk, t1 = t0 + kBlk < a.T ? t0 + kBlk : a.T;
+    const bool on = col < a.C && t0 < a.T;
+    Raw k[kBlk], v[kBlk], r[kBlk];
+    Grad<E, D> dy[kBlk];
+    float h[N] = {};
+    if (on) {
+        load_rows<E>(k, a.K, a.ld, t0, t1, lb);
+        load_rows<E>(r, a.R, a.ld, t0, t1, lb);
+#pragma unroll
+        for (int j = 0; j < kBlk; j++) dy[j].load(a, t0 + j < t1 ? t0 + j : t1 - 1, col);
+        load_rows<E>(v, a.V, a.ld, t0, t1, lb);
+        load_f<N>((float *)at_row(a.states, t0 / kBlk, a.C, 4, (uint32_t)col * 4), h);
+    }
+    Span at(a, t0);
+    const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
+    Span last = at;   // at the last row
+    if (on && !plain) last.forth(t1 - 1);
     float A[N], B[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
-    bool last = cu.live() && cu.end() == t1;
-    int64_t st = cu.begin();
-    const int nblk = (int)((t1 - t0 + kBlk - 1) / kBlk);
-    for (int b = nblk - 1; b >= 0; b--) {
-        const int64_t tb = t0 + (int64_t)b * kBlk;
-        const int n = (int)(t1 - tb < kBlk ? t1 - tb : kBlk);
-        typename E::Raw k[kBlk], r[kBlk];
-        float dy[kBlk][N];
-#pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            const int64_t t = tb + (j < n ? j : n - 1);
-            k[j] = *(const typename E::Raw *)((const char *)a.K + (t * a.ld + col) * (4 / N));
-            r[j] = *(const typename E::Raw *)((const char *)a.R + (t * a.ld + col) * (4 / N));
-            load_dy<E, D>(a, t, col, dy[j]);
-        }
-#pragma unroll
-        for (int j = kBlk - 1; j >= 0; j--) {
-            if (j >= n) continue;
-            const int64_t t = tb + j;
-            if (t < st) {
-                cu.back(t);
-                st = cu.begin();
-                last = cu.live();
-            }
-            if (last) {
-                last = false;
-#pragma unroll
-                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
-                if (a.dhT) load_f<N>(a.dhT + cu.cur * a.C + col, B);
-            }
-            if (!cu.live()) continue;
-            float kf[N], rf[N];
+    if (on) {
+        auto row = [&](int j) {
+            float kf[N], rf[N], d[N];
             E::unpack(k[j], kf);
             E::unpack(r[j], rf);
+            dy[j].get(d);
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                const float w = sigmoid(kf[i]);
-                const float g = fmaf(dy[j][i], sigmoid(rf[i]), B[i]);
+                const float w = sigmoid(kf[i]), g = fmaf(d[i], sigmoid(rf[i]), B[i]);
                 A[i] = fmaf(-w, A[i], A[i]);
                 B[i] = fmaf(-w, g, g);
             }
+        };
+        if (plain) {
+#pragma unroll
+            for (int j = kBlk - 1; j >= 0; j--) row(j);
+        } else {
+            Span s = last;
+#pragma unroll
+            for (int j = kBlk - 1; j >= 0; j--) {
+                const int64_t t = t0 + j;
+                if (t >= t1) continue;
+                s.back(t);
+                if (!s.live) continue;
+                if (t + 1 == s.e) {
+#pragma unroll
+                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
+                    if (a.dhT) load_f<N>(a.dhT + s.c.cur * a.C + col, B);
+                }
+                row(j);
+            }
         }
     }
-    float *g = a.agg + ch * 2 * a.C + col;
-    store_f<N>(g, A);
-    store_f<N>(g + a.C, B);
-}
-
-// dK, dV, dR and dh0 of a chunk from the gradient that enters it at its end;
-// h of each 16-row block is run forward from its checkpoint first
-template <class E, class D>
-__global__ __launch_bounds__(64) void recur_bwd_kernel(RecurArgs a) {
-    constexpr int N = E::N;
-    int cb;
-    int64_t ch;
-    wave_pos(a, cb, ch);
-    const int col = (cb * 64 + (int)threadIdx.x) * N;
-    if (ch >= a.nch) {
-        if (a.dh0) copy_empty<N>(a, ch - a.nch, col, a.dhT, a.dh0);
-        return;
-    }
-    if (col >= a.C) return;
-    const int64_t t0 = ch * a.L, t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
-    Cursor cu{a.off, a.S, a.T, 0};
-    cu.seek(t1 - 1);
-    float p[N] = {};
-    if (a.carry) load_f<N>(a.carry + ch * a.C + col, p);
-    bool last = cu.live() && cu.end() == t1;
-    int64_t st = cu.begin();
-    const int nblk = (int)((t1 - t0 + kBlk - 1) / kBlk);
-    for (int b = nblk - 1; b >= 0; b--) {
-        const int64_t tb = t0 + (int64_t)b * kBlk;
-        const int n = (int)(t1 - tb < kBlk ? t1 - tb : kBlk);
-        typename E::Raw k[kBlk], v[kBlk], r[kBlk];
-        float dy[kBlk][N], h[kBlk + 1][N];   // h[j]: the state before row j
-        load_f<N>(a.states + tb / kBlk * a.C + col, h[0]);
+    float p[N], hb[kBlk][N];
+    // does the chunk end with a sequence's last token?
+    const bool fresh = starts_at(a, (int64_t)(a.nch - link) * W * kBlk);
+    enter<N, W>(a, link, W - 1 - wave, fresh, col, cb * 64 * N, A, B, p, [&] {
+        // forward through the rows: the state before each
+        if (!on) return;
+        Span s = at;
 #pragma unroll
         for (int j = 0; j < kBlk; j++) {
-            const int64_t t = tb + (j < n ? j : n - 1);
-            const int64_t o = (t * a.ld + col) * (4 / N);
-            k[j] = *(const typename E::Raw *)((const char *)a.K + o);
-            v[j] = *(const typename E::Raw *)((const char *)a.V + o);
-            r[j] = *(const typename E::Raw *)((const char *)a.R + o);
-            load_dy<E, D>(a, t, col, dy[j]);
-        }
-        // forward through the block: the state before every row
-        {
-            Cursor f = cu;
-            f.back(tb);
-            int64_t nb = f.end();
-            bool first = f.live() && f.begin() == tb;
+            const int64_t t = t0 + j;
+            if (!plain && t < t1) {
+                s.forth(t);
+                if (s.live && t == s.b) {
 #pragma unroll
-            for (int j = 0; j < kBlk; j++) {
-                if (j < n) {
-                    if (tb + j >= nb) {
-                        f.forth(tb + j);
-                        nb = f.end();
-                        first = f.live();
-                    }
-                    if (first) {
-                        first = false;
-#pragma unroll
-                        for (int i = 0; i < N; i++) h[j][i] = 0.0f;
-                        if (a.h0) load_f<N>(a.h0 + f.cur * a.C + col, h[j]);
-                    }
+                    for (int i = 0; i < N; i++) h[i] = 0.0f;
+                    if (a.h0) load_f<N>(a.h0 + s.c.cur * a.C + col, h);
                 }
-                float kf[N], vf[N];
-                E::unpack(k[j], kf);
-                E::unpack(v[j], vf);
-#pragma unroll
-                for (int i = 0; i < N; i++) h[j + 1][i] = fmaf(sigmoid(kf[i]), vf[i] - h[j][i], h[j][i]);
             }
-        }
-#pragma unroll
-        for (int j = kBlk - 1; j >= 0; j--) {
-            if (j >= n) continue;
-            const int64_t t = tb + j;
-            if (t < st) {
-                cu.back(t);
-                st = cu.begin();
-                last = cu.live();
-            }
-            if (last) {
-                last = false;
-#pragma unroll
-                for (int i = 0; i < N; i++) p[i] = 0.0f;
-                if (a.dhT) load_f<N>(a.dhT + cu.cur * a.C + col, p);
-            }
-            if (!cu.live()) continue;
-            float kf[N], vf[N], rf[N], dk[N], dv[N], dr[N];
+            float kf[N], vf[N];
             E::unpack(k[j], kf);
             E::unpack(v[j], vf);
-            E::unpack(r[j], rf);
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                float wd, sd;
-                const float w = sigmoid_d(kf[i], wd), s = sigmoid_d(rf[i], sd);
-                const float g = fmaf(dy[j][i], s, p[i]);
-                // the state behind the row from the one before it (a sequence's
-                // first row starts from h0, not from the checkpoint's chain)
-                const float hb = h[j][i], hn = fmaf(w, vf[i] - hb, hb);
-                dr[i] = dy[j][i] * hn * sd;
-                dv[i] = g * w;
-                dk[i] = g * (vf[i] - hb) * wd;
-                p[i] = fmaf(-w, g, g);
+                hb[j][i] = h[i];
+                h[i] = fmaf(sigmoid(kf[i]), vf[i] - h[i], h[i]);
             }
-            const int64_t o = (t * a.ldd + col) * (4 / N);
-            *(typename E::Raw *)((char *)a.dK + o) = E::pack(dk);
-            *(typename E::Raw *)((char *)a.dV + o) = E::pack(dv);
-            *(typename E::Raw *)((char *)a.dR + o) = E::pack(dr);
-            if (a.dh0 && t == st) store_f<N>(a.dh0 + cu.cur * a.C + col, p);
+        }
+    });
+    if (!on) return;
+    auto row = [&](int j) {
+        float kf[N], vf[N], rf[N], d[N], dk[N], dv[N], dr[N];
+        E::unpack(k[j], kf);
+        E::unpack(v[j], vf);
+        E::unpack(r[j], rf);
+        dy[j].get(d);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            float w, keep, s, off;
+            gates(kf[i], w, keep);
+            gates(rf[i], s, off);
+            const float u = d[i] * s, g = u + p[i], x = vf[i] - hb[j][i];
+            dr[i] = u * off * fmaf(w, x, hb[j][i]);
+            dv[i] = g * w;
+            dk[i] = dv[i] * x * keep;
+            p[i] = fmaf(-w, g, g);
+        }
+        store_row<E>(a.dK, t0 + j, a.ldd, lb, dk);
+        store_row<E>(a.dV, t0 + j, a.ldd, lb, dv);
+        store_row<E>(a.dR, t0 + j, a.ldd, lb, dr);
+    };
+    if (plain) {
+#pragma unroll
+        for (int j = kBlk - 1; j >= 0; j--) row(j);
+    } else {
+#pragma unroll
+        for (int j = kBlk - 1; j >= 0; j--) {
+            const int64_t t = t0 + j;
+            if (t >= t1) continue;
+            last.back(t);
+            if (!last.live) continue;
+            if (t + 1 == last.e) {
+#pragma unroll
+                for (int i = 0; i < N; i++) p[i] = 0.0f;
+                if (a.dhT) load_f<N>(a.dhT + last.c.cur * a.C + col, p);
+            }
+            row(j);
+            if (a.dh0 && t == last.b) store_f<N>(a.dh0 + last.c.cur * a.C + col, p);
         }
     }
+}
+
+template <class E, class D, int W>
+__global__ __launch_bounds__(64 * W, 3) void recur_bwd_kernel(RecurArgs a) {
+    const int b = blockIdx.x < a.wgs ? blockIdx.x : blockIdx.x - a.wgs, cb = b % a.ncb;
+    const int col = (cb * 64 + (int)(threadIdx.x & 63)) * E::N;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x >= a.wgs) {
+        if (wave == 0) copy_empty<E::N>(a, b / a.ncb, col, a.dhT, a.dh0);
+        return;
+    }
+    bwd_chunk<E, D, W>(a, cb, col, wave, take_ticket(a, cb));   // the chain runs from the last chunk
 }
 
 // One token of every sequence: a row each, elementwise.
@@ -532,7 +665,7 @@ __global__ __launch_bounds__(256) void recur_step_kernel(const void *K, const vo
     const int64_t row = i / per;
     if (row >= rows) return;
     const int col = (int)(i - row * per) * N;
-    const int64_t o = (row * ld + col) * (4 / N);
+    const int64_t o = (row * ld + col) * E::ES;
     float k[N], v[N], r[N], h[N], y[N];
     E::unpack(*(const typename E::Raw *)((const char *)K + o), k);
     E::unpack(*(const typename E::Raw *)((const char *)V + o), v);
@@ -544,7 +677,7 @@ __global__ __launch_bounds__(256) void recur_step_kernel(const void *K, const vo
         y[j] = sigmoid(r[j]) * h[j];
     }
     store_f<N>(h_out + row * C + col, h);
-    *(typename E::Raw *)((char *)Y + (row * ldy + col) * (4 / N)) = E::pack(y);
+    *(typename E::Raw *)((char *)Y + (row * ldy + col) * E::ES) = E::pack(y);
 }
 
 }  // namespace rdev
@@ -555,23 +688,31 @@ using rdev::RecurArgs;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Chunks: enough waves to fill the chip (16 a compute unit), no shorter than
-// a checkpoint block.
+// Waves of a chunk, and a lane's share of a bf16 row.  What decides is how many
+// waves the registers leave room for while each holds 16 rows, and how many
+// chunks the chain passes through:
+//   forward   8 waves, two channels a lane (122 registers, 16 waves a compute
+//             unit): 32768 x 4096 279 us; 4 waves 372, 16 waves 355, one channel
+//             321;
+//   backward  4 waves, one channel a lane (137 registers, 12 waves): 32768 x
+//             4096 569 us; 8 waves 755, two channels 587.
+constexpr int kFwdWaves = 8, kBwdWaves = 4;
+constexpr int kFwdCols = 128, kBwdCols = 64;   // columns of a workgroup, bf16 (fp32: 64)
 struct RecurPlan {
-    int64_t ncb, L, nch;
+    int64_t ncb, nch;
+    size_t agg, prefix, ticket, total;   // workspace: byte offsets
 };
-RecurPlan plan_recur(int64_t T, int64_t C, int32_t act) {
-    RecurPlan p;
-    p.ncb = cdiv(C, act == TERN_BF16 ? 128 : 64);
-    const int64_t waves = 4096;
-    p.L = cdiv(cdiv(T * p.ncb, waves), TERN_RECUR_BLOCK) * TERN_RECUR_BLOCK;
-    if (p.L < TERN_RECUR_BLOCK) p.L = TERN_RECUR_BLOCK;
-    if (p.L > (1 << 30)) p.L = 1 << 30;
-    p.nch = cdiv(T, p.L);
+RecurPlan plan_recur(int64_t T, int64_t C, int cols, int waves) {
+    RecurPlan p{};
+    p.ncb = cdiv(C, cols);
+    p.nch = cdiv(T, (int64_t)waves * TERN_RECUR_BLOCK);
+    if (p.nch <= 1) return p;
+    const size_t n = (size_t)p.nch * (size_t)C;
+    p.prefix = n * 8;                      // C is a multiple of 8: 16-byte pieces
+    p.ticket = n * 12;
+    p.total = p.ticket + (size_t)p.ncb * rdev::kTicketStride * 4;
     return p;
 }
-
-size_t plan_ws(const RecurPlan &p, int64_t C) { return p.nch <= 1 ? 0 : (size_t)p.nch * (size_t)C * 3 * 4; }
 
 // A strided [rows, cols] buffer (a column slice of a wider one).
 struct Mat {
@@ -617,6 +758,18 @@ int check_sizes(int64_t T, int64_t C, int64_t n_seq, const int64_t *offsets, con
 }
 
 dim3 grid_of(int64_t n) { return dim3((unsigned)n); }
+
+// The chain's words, emptied by a launch of their own (none with one chunk).
+void start_chain(RecurArgs &a, const RecurPlan &p, void *workspace, hipStream_t st) {
+    if (!p.total) return;
+    char *w = (char *)workspace;
+    a.agg = (unsigned long long *)w;
+    a.prefix = (uint32_t *)(w + p.prefix);
+    a.ticket = (uint32_t *)(w + p.ticket);
+    const int64_t n16 = (int64_t)(p.ticket / 16), n = n16 > p.ncb ? n16 : p.ncb;
+    hipLaunchKernelGGL(rdev::recur_init_kernel, grid_of(cdiv(n, 256)), dim3(256), 0, st, (uint4 *)w, n16, a.ticket,
+                       (int)p.ncb);
+}
 // a launch counts its threads in 32 bits
 bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= INT64_C(0xFFFFFFFF) / threads; }
 
@@ -634,8 +787,9 @@ size_t tern_recur_states_bytes(int64_t T, int64_t C) {
 
 size_t tern_recur_workspace_bytes(int64_t T, int64_t C) {
     if (T < 0 || T > kMaxT || C < 0 || C > kMaxInOut || C % 8 != 0) return 0;
-    const size_t a = plan_ws(plan_recur(T, C, TERN_BF16), C), b = plan_ws(plan_recur(T, C, TERN_F32), C);
-    return ((a > b ? a : b) + 255) & ~size_t(255);
+    size_t most = 0;
+    for (int waves : {kFwdWaves, kBwdWaves}) most = std::max(most, plan_recur(T, C, 64, waves).total);
+    return (most + 255) & ~size_t(255);
 }
 
 int tern_recur_fwd(const void *K, const void *V, const void *R, int64_t ld, int32_t act_dtype, const float *h0,
@@ -647,8 +801,8 @@ int tern_recur_fwd(const void *K, const void *V, const void *R, int64_t ld, int3
     if (!act_ok(act_dtype)) return TERN_ERR_DTYPE;
     const bool tok = T > 0 && C > 0;
     if (tok && (!K || !V || !R || !Y)) return TERN_ERR_NULL;
-    const RecurPlan p = plan_recur(T, C, act_dtype);
-    const size_t wsb = plan_ws(p, C);
+    const RecurPlan p = plan_recur(T, C, act_dtype == TERN_BF16 ? kFwdCols : 64, kFwdWaves);
+    const size_t wsb = p.total;
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (misaligned(K) || misaligned(V) || misaligned(R) || misaligned(Y) || misaligned(h0) || misaligned(hT) ||
         misaligned(states) || misaligned(workspace) || ((uintptr_t)offsets & 7u))
@@ -663,23 +817,17 @@ int tern_recur_fwd(const void *K, const void *V, const void *R, int64_t ld, int3
     if (any_overlap(outs, 4, ins, 5)) return TERN_ERR_ALIAS;
     const int64_t empties = hT ? cdiv(n_seq, 64) : 0;
     if (C == 0 || (p.nch + empties) == 0) return TERN_OK;
-    if (!grid_fits(p.ncb * (p.nch + empties), 64)) return TERN_ERR_SHAPE;
+    if (!grid_fits(p.ncb * (p.nch + empties), 64 * kFwdWaves)) return TERN_ERR_SHAPE;
     RecurArgs a{};
     a.K = K; a.V = V; a.R = R; a.ld = ld; a.h0 = h0; a.off = offsets; a.S = n_seq; a.T = T;
-    a.C = (int)C; a.ncb = (int)p.ncb; a.L = (int)p.L; a.nch = (int)p.nch;
+    a.C = (int)C; a.ncb = (int)p.ncb; a.nch = (int)p.nch;
     a.Y = Y; a.ldy = ldy; a.hT = hT; a.states = states;
-    a.agg = (float *)workspace;
-    a.carry = wsb ? (float *)workspace + (size_t)p.nch * 2 * C : nullptr;
     hipStream_t st = (hipStream_t)stream;
-    const bool bf = act_dtype == TERN_BF16;
-    const dim3 g1 = grid_of(p.ncb * p.nch), g3 = grid_of(p.ncb * (p.nch + empties));
-    if (a.carry) {
-        if (bf) hipLaunchKernelGGL(rdev::recur_agg_kernel<rdev::Bf>, g1, dim3(64), 0, st, a);
-        else hipLaunchKernelGGL(rdev::recur_agg_kernel<rdev::Fp>, g1, dim3(64), 0, st, a);
-        hipLaunchKernelGGL(rdev::recur_carry_kernel<false>, grid_of(cdiv(C, 16)), dim3(1024), 0, st, a);
-    }
-    if (bf) hipLaunchKernelGGL(rdev::recur_fwd_kernel<rdev::Bf>, g3, dim3(64), 0, st, a);
-    else hipLaunchKernelGGL(rdev::recur_fwd_kernel<rdev::Fp>, g3, dim3(64), 0, st, a);
+    start_chain(a, p, workspace, st);
+    a.wgs = (unsigned)(p.ncb * p.nch);
+    const dim3 g = grid_of(a.wgs + p.ncb * empties), b(64 * kFwdWaves);
+    if (act_dtype == TERN_BF16) hipLaunchKernelGGL((rdev::recur_fwd_kernel<rdev::Bf, kFwdWaves>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((rdev::recur_fwd_kernel<rdev::Fp, kFwdWaves>), g, b, 0, st, a);
     return launched();
 }
 
@@ -693,8 +841,8 @@ int tern_recur_bwd(const void *K, const void *V, const void *R, int64_t ld, int3
     if (!act_ok(act_dtype) || !(dy_dtype == TERN_F32 || dy_dtype == act_dtype)) return TERN_ERR_DTYPE;
     const bool tok = T > 0 && C > 0;
     if (tok && (!K || !V || !R || !states || !dY || !dK || !dV || !dR)) return TERN_ERR_NULL;
-    const RecurPlan p = plan_recur(T, C, act_dtype);
-    const size_t wsb = plan_ws(p, C);
+    const RecurPlan p = plan_recur(T, C, act_dtype == TERN_BF16 ? kBwdCols : 64, kBwdWaves);
+    const size_t wsb = p.total;
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (misaligned(K) || misaligned(V) || misaligned(R) || misaligned(h0) || misaligned(states) || misaligned(dY) ||
         misaligned(dhT) || misaligned(dK) || misaligned(dV) || misaligned(dR) || misaligned(dh0) ||
@@ -709,26 +857,22 @@ int tern_recur_bwd(const void *K, const void *V, const void *R, int64_t ld, int3
     if (any_overlap(outs, 5, ins, 8)) return TERN_ERR_ALIAS;
     const int64_t empties = dh0 ? cdiv(n_seq, 64) : 0;
     if (C == 0 || (p.nch + empties) == 0) return TERN_OK;
-    if (!grid_fits(p.ncb * (p.nch + empties), 64)) return TERN_ERR_SHAPE;
+    if (!grid_fits(p.ncb * (p.nch + empties), 64 * kBwdWaves)) return TERN_ERR_SHAPE;
     RecurArgs a{};
     a.K = K; a.V = V; a.R = R; a.ld = ld; a.h0 = h0; a.off = offsets; a.S = n_seq; a.T = T;
-    a.C = (int)C; a.ncb = (int)p.ncb; a.L = (int)p.L; a.nch = (int)p.nch;
+    a.C = (int)C; a.ncb = (int)p.ncb; a.nch = (int)p.nch;
     a.states = const_cast<float *>(states);
     a.dY = dY; a.lddy = lddy; a.dhT = dhT; a.dK = dK; a.dV = dV; a.dR = dR; a.ldd = ldd; a.dh0 = dh0;
-    a.agg = (float *)workspace;
-    a.carry = wsb ? (float *)workspace + (size_t)p.nch * 2 * C : nullptr;
     hipStream_t st = (hipStream_t)stream;
-    const dim3 g1 = grid_of(p.ncb * p.nch), g3 = grid_of(p.ncb * (p.nch + empties)), b(64);
-    const int form = act_dtype == TERN_F32 ? 2 : dy_dtype == TERN_F32 ? 1 : 0;
-    if (a.carry) {
-        if (form == 0) hipLaunchKernelGGL((rdev::recur_bagg_kernel<rdev::Bf, rdev::Bf>), g1, b, 0, st, a);
-        else if (form == 1) hipLaunchKernelGGL((rdev::recur_bagg_kernel<rdev::Bf, rdev::Fp>), g1, b, 0, st, a);
-        else hipLaunchKernelGGL((rdev::recur_bagg_kernel<rdev::Fp, rdev::Fp>), g1, b, 0, st, a);
-        hipLaunchKernelGGL(rdev::recur_carry_kernel<true>, grid_of(cdiv(C, 16)), dim3(1024), 0, st, a);
-    }
-    if (form == 0) hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Bf, rdev::Bf>), g3, b, 0, st, a);
-    else if (form == 1) hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Bf, rdev::Fp>), g3, b, 0, st, a);
-    else hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Fp, rdev::Fp>), g3, b, 0, st, a);
+    start_chain(a, p, workspace, st);
+    a.wgs = (unsigned)(p.ncb * p.nch);
+    const dim3 g = grid_of(a.wgs + p.ncb * empties), b(64 * kBwdWaves);
+    if (act_dtype == TERN_F32)
+        hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Fp, rdev::Fp, kBwdWaves>), g, b, 0, st, a);
+    else if (dy_dtype == TERN_F32)
+        hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Bh, rdev::Fp, kBwdWaves>), g, b, 0, st, a);
+    else
+        hipLaunchKernelGGL((rdev::recur_bwd_kernel<rdev::Bh, rdev::Bh, kBwdWaves>), g, b, 0, st, a);
     return launched();
 }
 

@@ -122,7 +122,7 @@ def test_sizes(L):
     assert tl.tern_recur_states_bytes(33, 60) == 0
     assert tl.tern_recur_workspace_bytes(-1, 64) == 0
     assert tl.tern_recur_workspace_bytes(16, 64) == 0          # one chunk
-    for T, C in ((17, 64), (16384, 2048), (32768, 4096)):
+    for T, C in ((1000, 64), (16384, 2048), (32768, 4096)):
         assert tl.tern_recur_workspace_bytes(T, C) % 256 == 0 and tl.tern_recur_workspace_bytes(T, C) > 0
 
 

@@ -171,6 +171,13 @@ __device__ inline void load_lds(__amdgpu_buffer_rsrc_t rs, char *lds, uint32_t v
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_AS void *)lds, 16, voff, soff, 0, 0);
 }
 
+__device__ inline u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+}
+__device__ inline void store16(u32x4 v, __amdgpu_buffer_rsrc_t rs, uint32_t off) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
+}
+
 template <int N>
 __device__ inline void wait_loads_barrier() {
     __builtin_amdgcn_sched_barrier(0);
@@ -333,65 +340,102 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
     constexpr int kT = WT * 2 + 16;   // bytes of a column of T
     char *T = lds + wave * WT * kT;
     const int row0 = prow + wm * WT, col0 = qrow + wn * WT;
-    const h16 *old = MODE == APPLY ? p.XT[a.flip] : p.A;   // its term at [column][row] (A is symmetric)
+    // A piece outside the matrix is loaded as zeros and not stored: its offset
+    // lies behind the resource's end (columns past the last do by themselves).
+    constexpr uint32_t kNone = 0x7FFFFFF0u;
+    constexpr int kAll = WT * WT / 8 / 64;     // pieces a lane, and how many at a time
+    constexpr int NB = kAll % 8 == 0 ? 8 : kAll % 6 == 0 ? 6 : kAll;
     if (MODE != GRAM) {
-#pragma unroll 16
-        for (int i = lane; i < WT * WT / 8; i += 64) {
-            const int c = i / (WT / 8), r = i % (WT / 8) * 8;
-            u32x4 v = {0, 0, 0, 0};
-            if (col0 + c < qall && row0 + r < p.mp) v = *(const u32x4 *)(old + (int64_t)(col0 + c) * p.mp + row0 + r);
-            *(u32x4 *)(T + c * kT + r * 2) = v;
+        // the old matrix's term at [column][row] (A is symmetric)
+        const h16 *old = (MODE == APPLY ? p.XT[a.flip] : p.A) + (int64_t)col0 * p.mp;
+        const __amdgpu_buffer_rsrc_t ro = rsrc(old, (int64_t)(qall - col0) * p.mp * 2);
+#pragma unroll 1
+        for (int n = 0; n < kAll; n += NB) {
+            u32x4 v[NB];
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = lane + (n + m) * 64, c = i / (WT / 8), r = row0 + i % (WT / 8) * 8;
+                v[m] = load16(ro, r < p.mp ? (uint32_t)(c * p.mp + r) * 2 : kNone);
+            }
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = lane + (n + m) * 64;
+                *(u32x4 *)(T + i / (WT / 8) * kT + i % (WT / 8) * 16) = v[m];
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < F; i++)
+    for (int i = 0; i < F; i++) {
+        char *at = T + lr * kT + (i * 32 + lh * 4) * 2;
+        h16x4 x[F][4];
+        if (MODE != GRAM)
+#pragma unroll
+            for (int j = 0; j < F; j++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) x[j][g] = *(const h16x4 *)(at + j * 32 * kT + g * 16);
 #pragma unroll
         for (int j = 0; j < F; j++)
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                h16x4 *at = (h16x4 *)(T + (j * 32 + lr) * kT + (i * 32 + g * 8 + lh * 4) * 2);
-                h16x4 x = {}, o;
-                if (MODE != GRAM) x = *at;
+                h16x4 o;
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
                     const float v = acc[i][j][g * 4 + r];
                     if (MODE == GRAM) o[r] = (h16)(v * (1.0f / 16384.0f));
-                    else if (MODE == POLY) o[r] = (h16)fmaf(0.5f * kB, (float)x[r], v * (kC / 32768.0f));
+                    else if (MODE == POLY) o[r] = (h16)fmaf(0.5f * kB, (float)x[j][g][r], v * (kC / 32768.0f));
                     else {
-                        const float y = fmaf(kA, (float)x[r], v * (1.0f / 8192.0f));
+                        const float y = fmaf(kA, (float)x[j][g][r], v * (1.0f / 8192.0f));
                         o[r] = a.last ? __builtin_bit_cast(h16, (__bf16)(y * (1.0f / kXScale) * p.gain)) : (h16)y;
                     }
                 }
-                *at = o;
+                *(h16x4 *)(at + j * 32 * kT + g * 16) = o;
             }
+    }
     const bool out = MODE == APPLY && a.last;   // into O, without the padding
     const int rows = out ? p.m : p.mp, cols = out ? p.n : qall;
     // [column][row]: X^T, the mirrored tile of A or B, or O of a tall G
     if (!out || p.tall) {
-        h16 *dst = MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.XT[a.flip ^ 1];
         const int64_t ldd = out ? p.cols : p.mp;
-#pragma unroll 16
-        for (int i = lane; i < WT * WT / 8; i += 64) {
-            const int c = i / (WT / 8), r = i % (WT / 8) * 8;
-            if (col0 + c < cols && row0 + r < rows)
-                *(u32x4 *)(dst + (int64_t)(col0 + c) * ldd + row0 + r) = *(const u32x4 *)(T + c * kT + r * 2);
+        h16 *dst = (MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.XT[a.flip ^ 1]) + col0 * ldd;
+        const __amdgpu_buffer_rsrc_t rd = rsrc(dst, (cols - col0) * ldd * 2);
+#pragma unroll 1
+        for (int n = 0; n < kAll; n += NB) {
+            u32x4 v[NB];
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = lane + (n + m) * 64;
+                v[m] = *(const u32x4 *)(T + i / (WT / 8) * kT + i % (WT / 8) * 16);
+            }
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = lane + (n + m) * 64, c = i / (WT / 8), r = row0 + i % (WT / 8) * 8;
+                store16(v[m], rd, r < rows ? (uint32_t)(c * ldd + r) * 2 : kNone);
+            }
         }
     }
     // [row][column]: X, the tile of A or B itself, or O of a wide G
     if (MODE == APPLY ? !out || !p.tall : ti != tj) {
-        h16 *dst = MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.X;
         const int64_t ldd = MODE != APPLY ? p.mp : out ? p.cols : p.np;
+        h16 *dst = (MODE == GRAM ? p.A : MODE == POLY ? p.B : out ? (h16 *)p.O : p.X) + row0 * ldd;
+        const __amdgpu_buffer_rsrc_t rd = rsrc(dst, (rows - row0) * ldd * 2);
         // 16 lanes: 16 rows of 8 columns, four columns a read (lane 4 e + q reads
         // rows 4 q .. 4 q + 3 of column e and receives row 4 e + q)
         const int e = lane >> 2 & 3, q = lane & 3, g = lane >> 4;
-#pragma unroll 16
-        for (int i = 0; i < (WT / 16) * (WT / 32); i++) {
-            const int r = i / (WT / 32) * 16, c = i % (WT / 32) * 32 + g * 8;
-            const char *at = T + (c + e) * kT + (r + 4 * q) * 2;
-            const u32x2 lo = transposed(at), hi = transposed(at + 4 * kT);
-            const int row = row0 + r + (lane & 15), col = col0 + c;
-            if (row < rows && col < cols)
-                *(u32x4 *)(dst + (int64_t)row * ldd + col) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll 1
+        for (int n = 0; n < kAll; n += NB) {
+            u32x4 v[NB];
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = n + m, r = i / (WT / 32) * 16, c = i % (WT / 32) * 32 + g * 8;
+                const char *at = T + (c + e) * kT + (r + 4 * q) * 2;
+                const u32x2 lo = transposed(at), hi = transposed(at + 4 * kT);
+                v[m] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            }
+#pragma unroll
+            for (int m = 0; m < NB; m++) {
+                const int i = n + m, r = i / (WT / 32) * 16 + (lane & 15), col = col0 + i % (WT / 32) * 32 + g * 8;
+                store16(v[m], rd, col < cols ? (uint32_t)(r * ldd + col) * 2 : kNone);
+            }
         }
     }
 }
@@ -485,7 +529,7 @@ void launch_product(int wt, OrthoArgs &a, hipStream_t st) {
     if (wt == 128) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<128, 32, 4, MODE>), g, b, 0, st, a);
     else if (wt == 96) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<96, 32, 4, MODE>), g, b, 0, st, a);
     else if (wt == 64) hipLaunchKernelGGL((ndev::ortho_gemm_kernel<64, 64, 5, MODE>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((ndev::ortho_gemm_kernel<32, 64, 5, MODE>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((ndev::ortho_gemm_kernel<32, 64, (MODE == ndev::APPLY ? 3 : 5), MODE>), g, b, 0, st, a);
 }
 
 }  // namespace

@@ -73,8 +73,8 @@ def parse():
                          "HBM traffic counters)")
     ap.add_argument("--extras", action="store_true",
                     help="instead of the step: per-call times of the accumulating backward, the q/k/v "
-                         "group, the health panel and the scale step on the workload's shapes (eager, one "
-                         "JSON line)")
+                         "group, the health panel, the scale step, the recurrence, the 4-bit products and "
+                         "the orthogonalisation on the workload's shapes (eager, one JSON line)")
     return ap.parse_args()
 
 
@@ -83,7 +83,8 @@ def extras(a):
     projections (eager calls, events on the current stream, median of a few
     timed repetitions): dX and dW plain against accumulating, the fused q/k/v
     group against three separate projections, the gather that builds it, the
-    health panel with churn, and the scale's AdamW step.  HBM-bound calls are
+    health panel with churn, the scale's AdamW step, and the operators around
+    the projections (layer_operators).  HBM-bound calls are
     also given against their algorithmic bytes and the 8 TB/s peak."""
     import statistics
 
@@ -204,10 +205,68 @@ def extras(a):
         sb = timed(sep_bwd)
         out["qkv_group"] = {"fwd_ms": round(gf, 4), "fwd_separate_ms": round(sf, 4), "bwd_ms": round(gb, 4),
                             "bwd_separate_ms": round(sb, 4)}
+    out.update(layer_operators(w, projs, timed))
     torch.cuda.synchronize()
     print(json.dumps({"metric": "per-call times of the entry points beyond the step", "workload": w.name,
                       "T": w.T, "projections": [[d["name"], d["n_in"], d["n_out"]] for d in projs],
                       "launch": "eager", "entries": out}), flush=True)
+
+
+def layer_operators(w, projs, timed):
+    """The operators around a layer's projections on the workload's sizes: the
+    gated linear recurrence (over sequences of 1024 tokens; 256 in the small
+    workload), one token of 32 sequences through it, one token through every
+    projection as a 4-bit product, and the layer's weight gradients
+    orthogonalised."""
+    import torch
+
+    import ternary_weight_linear_tern_amd as tl
+
+    def hbm(ms, nbytes):
+        return {"bytes": nbytes, "gbs": round(nbytes / ms / 1e6, 1),
+                "hbm_frac": round(nbytes / ms / 1e6 / PEAK_HBM_GBS, 4)}
+
+    out = {}
+    g = torch.Generator(device="cuda").manual_seed(1)
+    N = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    T, d = w.T, projs[0]["n_in"]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    n_seq = T // (256 if T <= 2048 else 1024)
+    off = torch.arange(n_seq + 1, device="cuda", dtype=torch.int64) * (T // n_seq)
+    buf, grad = N(T, 3 * d).bfloat16(), torch.empty((T, 3 * d), **bf)
+    buf[:, d:2 * d] -= 3.0   # a write gate that keeps some 20 tokens
+    cut = lambda b: (b[:, d:2 * d], b[:, 2 * d:], b[:, :d])
+    Y, dY = torch.empty((T, d), **bf), N(T, d) * 0.01
+    states, ws = tl.empty_recur_states(T, d), tl.empty_recur_workspace(T, d)
+    ms = timed(lambda: tl.tern_recur_fwd(*cut(buf), Y, ws, offsets=off, states=states))
+    out["recur_fwd"] = {"ms": round(ms, 4), "sequences": n_seq, **hbm(ms, 8 * T * d)}
+    ms = timed(lambda: tl.tern_recur_bwd(*cut(buf), dY, states, *cut(grad), ws, offsets=off))
+    out["recur_bwd"] = {"ms": round(ms, 4), "sequences": n_seq, **hbm(ms, 16 * T * d)}
+    h = torch.zeros((32, d), device="cuda")
+    row = buf[:32].contiguous()
+    ms = timed(lambda: tl.tern_recur_step(*cut(row), h, Y[:32]))
+    out["recur_step"] = {"us": round(1e3 * ms, 2), "sequences": 32}
+
+    q4 = []
+    for p in projs:
+        pk = tl.empty_q4_packed(p["n_in"], p["n_out"])
+        tl.tern_q4_pack(p["q"], pk)
+        q4.append(dict(n_in=p["n_in"], n_out=p["n_out"], group=128, packed=pk, X=p["X"][:1],
+                       gscale=p["scale"].expand(-(-p["n_in"] // 128), -1).contiguous(),
+                       Y=torch.empty((1, p["n_out"]), **bf)))
+    ms = timed(lambda: tl.tern_layer_q4_matvec(q4))
+    out["q4_one_token"] = {"us": round(1e3 * ms, 2), "group": 128,
+                           **hbm(ms, sum(p["packed"].numel() * 4 + p["gscale"].numel() * 4 for p in q4))}
+
+    mats = [dict(G=p["gq"], O=torch.empty((p["n_in"], p["n_out"]), **bf)) for p in projs]
+    shapes = [(p["n_in"], p["n_out"]) for p in projs]
+    ws = tl.empty_ortho_workspace(shapes)
+    ms = timed(lambda: tl.tern_layer_orthogonalize(mats, ws))
+    # a step's products, the symmetric ones by half: m^2 n + m^3 + 2 m^2 n
+    flops = sum(5.0 * min(s) ** 2 * (3 * max(s) + min(s)) for s in shapes)
+    out["orthogonalize"] = {"ms": round(ms, 4), "steps": 5, "tflops": round(flops / ms / 1e9, 1),
+                            "mfma_frac": round(flops / ms / 1e9 / PEAK_TFLOPS["bf16"], 4)}
+    return out
 
 
 def ready_events(events, stream):

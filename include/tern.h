@@ -14,9 +14,15 @@
  *     G = X^T . dY, gq = G * scale[c] (tg_gq) and the scale gradient
  *     sgrad[c] = sum_r G[r, c] * tern[r, c] (tg_scale_grad).
  *
+ * Around the projections stand the operators that a layer of them needs besides
+ * (their own formulas, further below): the gated linear recurrence between the
+ * receptance / key / value projections and the output projection
+ * (tern_recur_*), products of a few rows with 4-bit weights for serving
+ * (tern_q4_*), and the orthogonalisation of an update (tern_orthogonalize).
+ *
  * Conventions for every entry point:
- *   - All array pointers are DEVICE pointers owned by the caller: contiguous,
- *     row-major, 16-byte aligned.  The library allocates nothing, frees
+ *   - All array pointers are DEVICE pointers owned by the caller: contiguous
+ *     (tern_recur_*: contiguous rows), row-major, 16-byte aligned.  The library allocates nothing, frees
  *     nothing, keeps no state between calls and never synchronises.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).  All
  *     work is enqueued on it in order; results are ready when the caller's
@@ -57,7 +63,8 @@ extern "C" {
 #define TERN_ERR_WORKSPACE -6  /* workspace missing or smaller than required */
 #define TERN_ERR_ALIAS     -7  /* an output overlaps an input or another output */
 #define TERN_ERR_HIP       -8  /* the HIP runtime refused a launch */
-#define TERN_ERR_VALUE     -9  /* a scalar argument outside its range (optimizer step, learning rate) */
+#define TERN_ERR_VALUE     -9  /* a scalar argument outside its range (optimizer step, learning rate,
+                                * group of 4-bit scales, Newton-Schulz steps) */
 #define TERN_ERR_SCRATCH  -10  /* the sizes need more than the library's static scratch */
 
 /* Number of uint32 words of a packed ternary handle for an [in, out] matrix

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -563,8 +564,8 @@ def _call(fn: str, dev: int, stream, *args) -> None:
     with dev the current device."""
     # the raw handle of torch.cuda.current_stream(dev), without building the object
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == dev:
+    f = getattr(_lib or lib(), fn)
+    if torch._C._cuda_getDevice() == dev:
         rc = f(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -595,14 +596,19 @@ def _row_strides(fn: str, names, a, b, c) -> int:
 
 
 def _recur_inputs(fn, K, V, R):
+    """Shape of K, V and R, and the row stride they share."""
     if not isinstance(K, torch.Tensor):
         raise TypeError(f"{fn}: K must be a tensor")
-    if K.dim() != 2:
+    shape, dt = K.shape, K.dtype
+    if len(shape) != 2:
         raise ValueError(f"{fn}: K must be [T, C]")
-    shape = K.shape
-    _shaped(fn, "K", K, shape, _ACT)
-    _shaped(fn, "V", V, shape, (K.dtype,))
-    _shaped(fn, "R", R, shape, (K.dtype,))
+    if dt not in _ACT or V.shape != shape or R.shape != shape or V.dtype is not dt or R.dtype is not dt:
+        _need(fn, "K", K, shape, _ACT)
+        _need(fn, "V", V, shape, (dt,))
+        _need(fn, "R", R, shape, (dt,))
+    strides = K.stride()
+    if strides[1] == 1 and shape[0] > 1 and V.stride() == strides and R.stride() == strides:
+        return shape, strides[0]
     return shape, _row_strides(fn, ("K", "V", "R"), K, V, R)
 
 
@@ -667,13 +673,20 @@ def tern_recur_step(K, V, R, h, Y, h_out=None, stream=None) -> None:
     h_out (None: in place) and Y = sigmoid(R) h_out."""
     fn = "tern_recur_step"
     shape, ld = _recur_inputs(fn, K, V, R)
-    h_out = h if h_out is None else h_out
-    _shaped(fn, "h", h, shape, _F32)
-    _shaped(fn, "h_out", h_out, shape, _F32)
-    _shaped(fn, "Y", Y, shape, (K.dtype,))
-    dev = _device_of(fn, K, V, R, h, h_out, Y)
-    _call(fn, dev, stream, K.data_ptr(), V.data_ptr(), R.data_ptr(), ld, _act_code(K), shape[0], shape[1], _addr(h),
-          _addr(h_out), Y.data_ptr(), _row_stride(fn, "Y", Y))
+    if h_out is None:
+        h_out = h
+    dt, f32 = K.dtype, torch.float32
+    if h.shape != shape or h.dtype is not f32 or h_out.shape != shape or h_out.dtype is not f32 \
+            or Y.shape != shape or Y.dtype is not dt:
+        _need(fn, "h", h, shape, _F32)
+        _need(fn, "h_out", h_out, shape, _F32)
+        _need(fn, "Y", Y, shape, (dt,))
+    dev = K.get_device()
+    if dev < 0 or V.get_device() != dev or R.get_device() != dev or h.get_device() != dev \
+            or h_out.get_device() != dev or Y.get_device() != dev:
+        _need_device(fn, K, V, R, h, h_out, Y)
+    _call(fn, dev, stream, K.data_ptr(), V.data_ptr(), R.data_ptr(), ld, TERN_BF16 if dt is torch.bfloat16 else
+          TERN_F32, shape[0], shape[1], _addr(h), _addr(h_out), Y.data_ptr(), _row_stride(fn, "Y", Y))
 
 
 def empty_recur_states(T: int, C: int, device="cuda") -> torch.Tensor:
@@ -755,6 +768,7 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
         raise TypeError(f"{fn}: X and gscale must be bfloat16 or float32, Y float32 or X's dtype")
     dev = X0.get_device()
     words = []   # the tern_q4_proj_t array: seven 64-bit members each
+    int32 = torch.int32
     for d in projs:
         n_in, n_out, group = d["n_in"], d["n_out"], d["group"]
         X, s, Y, pk = d["X"], d["gscale"], d["Y"], d["packed"]
@@ -765,14 +779,18 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
             _need(fn, "gscale", s, (groups, n_out), (sdt,))
         if Y.shape != (T, n_out) or Y.dtype is not ydt:
             _need(fn, "Y", Y, (T, n_out), (ydt,))
-        _q4_packed(fn, pk, n_in, n_out)
+        if pk.dtype is not int32 or pk.numel() < -(-n_out // 16) * -(-n_in // 128) * 256:
+            _q4_packed(fn, pk, n_in, n_out)
         if X.get_device() != dev or s.get_device() != dev or Y.get_device() != dev \
                 or pk.get_device() != dev:
             _need_device(fn, X0, X, s, Y, pk)
-        words += (n_in, n_out, group, _addr(pk), _addr(s), _addr(X), _addr(Y))
+        if not (X.is_contiguous() and s.is_contiguous() and Y.is_contiguous() and pk.is_contiguous()):
+            raise ValueError("tensors passed to libtern must be contiguous")
+        words += (n_in, n_out, group, pk.data_ptr(), s.data_ptr(), X.data_ptr(), Y.data_ptr())
     if dev < 0:
         _need_device(fn, X0)
-    _call(fn, dev, stream, (_i64 * (7 * n))(*words), n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
+    arr = array("q", words)   # alive for the call
+    _call(fn, dev, stream, arr.buffer_info()[0], n, T, _act_code(X0), _act_code(s0), _act_code(Y0))
 
 
 class TernOrtho(ctypes.Structure):

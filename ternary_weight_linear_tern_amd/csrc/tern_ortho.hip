@@ -85,7 +85,7 @@ __device__ inline void load4(const void *G, int bf, int64_t i, float *f) {
 
 // |G|^2 in f64, one partial a workgroup, in a fixed order
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs a) {
-    __shared__ double red[256];
+    __shared__ double red[4];
     const OrthoOne &p = a.p[blockIdx.y];
     const int64_t n8 = p.rows * p.cols / 8;
     double s = 0.0;
@@ -96,27 +96,25 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; j++) s += (double)f[j] * (double)f[j];
     }
-    red[threadIdx.x] = s;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
-    for (int d = 128; d; d >>= 1) {
-        if ((int)threadIdx.x < d) red[threadIdx.x] += red[threadIdx.x + d];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) p.part[blockIdx.x] = red[0];
+    if (threadIdx.x == 0) p.part[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 // X and its transpose from G, 64 x 64 tiles, zeros in the padding
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
-    __shared__ double red[256];
     __shared__ h16 tile[64][68];
     const OrthoOne &p = a.p[problem_of(a, blockIdx.x)];
-    red[threadIdx.x] = p.part[threadIdx.x];
-    __syncthreads();
-    for (int d = 128; d; d >>= 1) {
-        if ((int)threadIdx.x < d) red[threadIdx.x] += red[threadIdx.x + d];
-        __syncthreads();
-    }
-    const float f = (float)(16384.0 / (sqrt(red[0]) + (double)kEps));
+    // every wave adds up the partials (in the same order)
+    const int lane = threadIdx.x & 63;
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kParts / 64; i++) sum += p.part[lane + 64 * i];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    const float f = (float)(16384.0 / (sqrt(sum) + (double)kEps));
     const int t = blockIdx.x - p.start, tn = p.np / 64;
     // tile (xi, xj) of X, at (r0, c0) of G
     const int xi = t / tn, xj = t % tn;
@@ -343,8 +341,8 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
     // A piece outside the matrix is loaded as zeros and not stored: its offset
     // lies behind the resource's end (columns past the last do by themselves).
     constexpr uint32_t kNone = 0x7FFFFFF0u;
-    constexpr int kAll = WT * WT / 8 / 64;     // pieces a lane, and how many at a time
-    constexpr int NB = kAll % 8 == 0 ? 8 : kAll % 6 == 0 ? 6 : kAll;
+    constexpr int kAll = WT * WT / 8 / 64;                             // pieces a lane
+    constexpr int NB = kAll % 8 == 0 ? 8 : kAll % 6 == 0 ? 6 : kAll;   // and how many at a time
     if (MODE != GRAM) {
         // the old matrix's term at [column][row] (A is symmetric)
         const h16 *old = (MODE == APPLY ? p.XT[a.flip] : p.A) + (int64_t)col0 * p.mp;

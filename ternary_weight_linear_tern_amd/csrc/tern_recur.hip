@@ -154,13 +154,6 @@ struct Span {
     }
 };
 
-// Is t the border between two sequences, or that behind the last one?
-__device__ inline bool starts_at(const RecurArgs &a, int64_t t) {
-    Cursor c{a.off, a.S, a.T, 0};
-    c.seek(t);
-    return c.cur > 0 && c.begin() == t;
-}
-
 // The rows of one checkpoint block (rows beyond the chunk's end repeat its
 // last one), all loads issued together.
 // A row's address is uniform in a wave, and lanes add 32 bits to it: that keeps
@@ -307,6 +300,7 @@ __device__ inline void enter(const RecurArgs &a, int i, int order, bool fresh, i
                 }
             sClosed = closed;
             sKnown = i == 0 || fresh;
+            store_f<N>(&sH[at], h);   // zero; a fresh chunk does not use it
         }
         __syncthreads();
     }
@@ -371,7 +365,7 @@ __device__ inline void enter(const RecurArgs &a, int i, int order, bool fresh, i
             }
             __syncthreads();
         }
-        if (i > 0 && !fresh) load_f<N>(&sH[at], h);
+        load_f<N>(&sH[at], h);
     }
     for (int q = 0; q < order; q++)
 #pragma unroll
@@ -396,25 +390,24 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     const int64_t t0 = ((int64_t)ch * W + wave) * kBlk, t1 = t0 + kBlk < a.T ? t0 + kBlk : a.T;
     const bool on = col < a.C && t0 < a.T;
     float w[kBlk][N];
-    Raw v[kBlk], r[kBlk];
-    {
-        Raw k[kBlk];
-        if (on) {
-            load_rows<E>(k, a.K, a.ld, t0, t1, lb);
-            load_rows<E>(v, a.V, a.ld, t0, t1, lb);
-            load_rows<E>(r, a.R, a.ld, t0, t1, lb);
-        }
-#pragma unroll
-        for (int j = 0; j < kBlk; j++) {
-            float kf[N];
-            E::unpack(k[j], kf);
-#pragma unroll
-            for (int i = 0; i < N; i++) w[j][i] = sigmoid(kf[i]);
-        }
+    Raw k[kBlk], v[kBlk], r[kBlk];
+    if (on) {
+        load_rows<E>(k, a.K, a.ld, t0, t1, lb);
+        load_rows<E>(v, a.V, a.ld, t0, t1, lb);
+        load_rows<E>(r, a.R, a.ld, t0, t1, lb);
     }
+    // the search among the offsets runs while the rows arrive
     Span at(a, t0);
+    __builtin_amdgcn_sched_barrier(0);
     // no sequence starts or ends inside the rows, and they are all there
     const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
+#pragma unroll
+    for (int j = 0; j < kBlk; j++) {
+        float kf[N];
+        E::unpack(k[j], kf);
+#pragma unroll
+        for (int i = 0; i < N; i++) w[j][i] = sigmoid(kf[i]);
+    }
     float A[N], B[N], h[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
@@ -448,9 +441,8 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             }
         }
     }
-    // does the chunk begin with a sequence's start?
-    const bool fresh = starts_at(a, (int64_t)ch * W * kBlk);
-    enter<N, W>(a, ch, wave, fresh, col, cb * 64 * N, A, B, h, [] {});
+    // the first wave's answer counts: does the chunk begin with a sequence's start?
+    enter<N, W>(a, ch, wave, at.b == t0, col, cb * 64 * N, A, B, h, [] {});
     if (!on) return;
     if (a.states) store_f<N>((float *)at_row(a.states, t0 / kBlk, a.C, 4, (uint32_t)col * 4), h);
     auto row = [&](int j) {
@@ -535,6 +527,7 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
     Span last = at;   // at the last row
     if (on && !plain) last.forth(t1 - 1);
+    __builtin_amdgcn_sched_barrier(0);
     float A[N], B[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
@@ -572,9 +565,8 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         }
     }
     float p[N], hb[kBlk][N];
-    // does the chunk end with a sequence's last token?
-    const bool fresh = starts_at(a, (int64_t)(a.nch - link) * W * kBlk);
-    enter<N, W>(a, link, W - 1 - wave, fresh, col, cb * 64 * N, A, B, p, [&] {
+    // the last wave's answer counts: does the chunk end with a sequence's last token?
+    enter<N, W>(a, link, W - 1 - wave, last.e == t0 + kBlk, col, cb * 64 * N, A, B, p, [&] {
         // forward through the rows: the state before each
         if (!on) return;
         Span s = at;

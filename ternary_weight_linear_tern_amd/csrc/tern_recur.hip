@@ -128,28 +128,32 @@ __device__ inline void gates(float x, float &on, float &off) {
     off = x < 0.0f ? i : j;
 }
 
-// A cursor with the borders of its sequence at hand (the offsets are in memory).
+// A cursor among the rows from t0 on, with its sequence's borders as rows
+// relative to t0 (clamped to [-1, 32]): comparing them costs one instruction a
+// row, and the offsets in memory are read only where a border is crossed.
 struct Span {
     Cursor c;
-    int64_t b, e;
+    int64_t t0;
+    int b, e;
     bool live;
+    __device__ int row_of(int64_t t) const { return t <= t0 - 1 ? -1 : t >= t0 + 32 ? 32 : (int)(t - t0); }
     __device__ void look() {
-        b = c.begin();
-        e = c.end();
+        b = row_of(c.begin());
+        e = row_of(c.end());
         live = c.live();
     }
-    __device__ Span(const RecurArgs &a, int64_t t) : c{a.off, a.S, a.T, 0} {
-        c.seek(t);
+    __device__ Span(const RecurArgs &a, int64_t first) : c{a.off, a.S, a.T, 0}, t0(first) {
+        c.seek(first);
         look();
     }
-    __device__ void forth(int64_t t) {
-        if (t < e) return;
-        c.forth(t);
+    __device__ void forth(int j) {
+        if (j < e) return;
+        c.forth(t0 + j);
         look();
     }
-    __device__ void back(int64_t t) {
-        if (t >= b) return;
-        c.back(t);
+    __device__ void back(int j) {
+        if (j >= b) return;
+        c.back(t0 + j);
         look();
     }
 };
@@ -398,9 +402,12 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     }
     // the search among the offsets runs while the rows arrive
     Span at(a, t0);
+    // the rows are all there and one sequence's, whose first they may be
+    const int n = (int)(t1 - t0);   // rows
+    const bool whole = at.live && at.e >= kBlk && n == kBlk, begins = whole && at.b == 0;
+    float start[N] = {};
+    if (begins && on && a.h0) load_f<N>(a.h0 + at.c.cur * a.C + col, start);
     __builtin_amdgcn_sched_barrier(0);
-    // no sequence starts or ends inside the rows, and they are all there
-    const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
 #pragma unroll
     for (int j = 0; j < kBlk; j++) {
         float kf[N];
@@ -421,18 +428,20 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
                 B[i] = fmaf(w[j][i], vf[i] - B[i], B[i]);
             }
         };
-        if (plain) {
+        if (whole) {
+            if (begins)
+#pragma unroll
+                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = start[i];
 #pragma unroll
             for (int j = 0; j < kBlk; j++) row(j);
         } else {
             Span s = at;
 #pragma unroll
             for (int j = 0; j < kBlk; j++) {
-                const int64_t t = t0 + j;
-                if (t >= t1) continue;
-                s.forth(t);
+                if (j >= n) continue;
+                s.forth(j);
                 if (!s.live) continue;
-                if (t == s.b) {
+                if (j == s.b) {
 #pragma unroll
                     for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
                     if (a.h0) load_f<N>(a.h0 + s.c.cur * a.C + col, B);
@@ -442,7 +451,7 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         }
     }
     // the first wave's answer counts: does the chunk begin with a sequence's start?
-    enter<N, W>(a, ch, wave, at.b == t0, col, cb * 64 * N, A, B, h, [] {});
+    enter<N, W>(a, ch, wave, at.b == 0, col, cb * 64 * N, A, B, h, [] {});
     if (!on) return;
     if (a.states) store_f<N>((float *)at_row(a.states, t0 / kBlk, a.C, 4, (uint32_t)col * 4), h);
     auto row = [&](int j) {
@@ -456,23 +465,26 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         }
         store_row<E>(a.Y, t0 + j, a.ldy, lb, o);
     };
-    if (plain) {
+    if (whole) {
+        if (begins)
+#pragma unroll
+            for (int i = 0; i < N; i++) h[i] = start[i];
 #pragma unroll
         for (int j = 0; j < kBlk; j++) row(j);
+        if (a.hT && at.e == kBlk) store_f<N>(a.hT + at.c.cur * a.C + col, h);
     } else {
 #pragma unroll
         for (int j = 0; j < kBlk; j++) {
-            const int64_t t = t0 + j;
-            if (t >= t1) continue;
-            at.forth(t);
+            if (j >= n) continue;
+            at.forth(j);
             if (!at.live) continue;
-            if (t == at.b) {
+            if (j == at.b) {
 #pragma unroll
                 for (int i = 0; i < N; i++) h[i] = 0.0f;
                 if (a.h0) load_f<N>(a.h0 + at.c.cur * a.C + col, h);
             }
             row(j);
-            if (a.hT && t + 1 == at.e) store_f<N>(a.hT + at.c.cur * a.C + col, h);
+            if (a.hT && j + 1 == at.e) store_f<N>(a.hT + at.c.cur * a.C + col, h);
         }
     }
 }
@@ -524,9 +536,18 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         load_f<N>((float *)at_row(a.states, t0 / kBlk, a.C, 4, (uint32_t)col * 4), h);
     }
     Span at(a, t0);
-    const bool plain = at.live && at.b < t0 && at.e > t0 + kBlk && t0 + kBlk <= a.T;
+    // the rows are all there and one sequence's, whose first and last they may hold
+    const int n = (int)(t1 - t0);   // rows
+    const bool whole = at.live && at.e >= kBlk && n == kBlk, begins = whole && at.b == 0,
+               ends = whole && at.e == kBlk;
+    float stop[N] = {};
+    if (on && begins) {
+        h[0] = h[N - 1] = 0.0f;
+        if (a.h0) load_f<N>(a.h0 + at.c.cur * a.C + col, h);
+    }
+    if (on && ends && a.dhT) load_f<N>(a.dhT + at.c.cur * a.C + col, stop);
     Span last = at;   // at the last row
-    if (on && !plain) last.forth(t1 - 1);
+    if (on && !whole) last.forth(n - 1);
     __builtin_amdgcn_sched_barrier(0);
     float A[N], B[N];
 #pragma unroll
@@ -544,18 +565,20 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
                 B[i] = fmaf(-w, g, g);
             }
         };
-        if (plain) {
+        if (whole) {
+            if (ends)
+#pragma unroll
+                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = stop[i];
 #pragma unroll
             for (int j = kBlk - 1; j >= 0; j--) row(j);
         } else {
             Span s = last;
 #pragma unroll
             for (int j = kBlk - 1; j >= 0; j--) {
-                const int64_t t = t0 + j;
-                if (t >= t1) continue;
-                s.back(t);
+                if (j >= n) continue;
+                s.back(j);
                 if (!s.live) continue;
-                if (t + 1 == s.e) {
+                if (j + 1 == s.e) {
 #pragma unroll
                     for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
                     if (a.dhT) load_f<N>(a.dhT + s.c.cur * a.C + col, B);
@@ -566,16 +589,15 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     }
     float p[N], hb[kBlk][N];
     // the last wave's answer counts: does the chunk end with a sequence's last token?
-    enter<N, W>(a, link, W - 1 - wave, last.e == t0 + kBlk, col, cb * 64 * N, A, B, p, [&] {
+    enter<N, W>(a, link, W - 1 - wave, last.e == kBlk, col, cb * 64 * N, A, B, p, [&] {
         // forward through the rows: the state before each
         if (!on) return;
         Span s = at;
 #pragma unroll
         for (int j = 0; j < kBlk; j++) {
-            const int64_t t = t0 + j;
-            if (!plain && t < t1) {
-                s.forth(t);
-                if (s.live && t == s.b) {
+            if (!whole && j < n) {
+                s.forth(j);
+                if (s.live && j == s.b) {
 #pragma unroll
                     for (int i = 0; i < N; i++) h[i] = 0.0f;
                     if (a.h0) load_f<N>(a.h0 + s.c.cur * a.C + col, h);
@@ -613,23 +635,26 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         store_row<E>(a.dV, t0 + j, a.ldd, lb, dv);
         store_row<E>(a.dR, t0 + j, a.ldd, lb, dr);
     };
-    if (plain) {
+    if (whole) {
+        if (ends)
+#pragma unroll
+            for (int i = 0; i < N; i++) p[i] = stop[i];
 #pragma unroll
         for (int j = kBlk - 1; j >= 0; j--) row(j);
+        if (a.dh0 && begins) store_f<N>(a.dh0 + at.c.cur * a.C + col, p);
     } else {
 #pragma unroll
         for (int j = kBlk - 1; j >= 0; j--) {
-            const int64_t t = t0 + j;
-            if (t >= t1) continue;
-            last.back(t);
+            if (j >= n) continue;
+            last.back(j);
             if (!last.live) continue;
-            if (t + 1 == last.e) {
+            if (j + 1 == last.e) {
 #pragma unroll
                 for (int i = 0; i < N; i++) p[i] = 0.0f;
                 if (a.dhT) load_f<N>(a.dhT + last.c.cur * a.C + col, p);
             }
             row(j);
-            if (a.dh0 && t == last.b) store_f<N>(a.dh0 + last.c.cur * a.C + col, p);
+            if (a.dh0 && j == last.b) store_f<N>(a.dh0 + last.c.cur * a.C + col, p);
         }
     }
 }

@@ -428,8 +428,8 @@ int tern_layer_bwd_dw(const tern_proj_t *projs, int32_t n, int64_t T, int32_t ac
  *   output (TERN_ERR_ALIAS).
  * All states, gradients and sums are fp32; Y, dK, dV and dR are rounded once
  * (nearest even) to act_dtype.  The order of every sum is fixed: repeated
- * calls are bitwise identical.  Values of one sequence (a NaN among them)
- * never reach another.
+ * calls are bitwise identical.  A NaN or an infinity goes on to its
+ * sequence's end as the formulas carry it, and never reaches another.
  *
  * tern_recur_fwd -- Y [T, C] (row stride ldy).
  *   hT      fp32 [n_seq, C], the state behind each sequence's last token (h0
@@ -437,7 +437,8 @@ int tern_layer_bwd_dw(const tern_proj_t *projs, int32_t n, int64_t T, int32_t ac
  *   states  checkpoints for the backward, tern_recur_states_bytes(T, C) bytes
  *           (the state before every TERN_RECUR_BLOCK-th row), or NULL.
  *   workspace  at least tern_recur_workspace_bytes(T, C) bytes (NULL when that
- *           is 0), for this call only.
+ *           is 0).  Calls that may run at the same time (on two streams, or in
+ *           two graphs replayed side by side) need one each.
  *
  * tern_recur_bwd -- from dY [T, C] (row stride lddy; dy_dtype TERN_F32, as the
  *   dX of the output projection is, or act_dtype) and dhT (fp32 [n_seq, C],
@@ -493,8 +494,9 @@ int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int
  *              last group may be short.
  *   T          any, 16 rows share one pass over the weights (at most 1048560).
  *   Products of the integer codes with X are exact, sums are fp32, the scale
- *   multiplies each group's sum once; the order of the sums is fixed.  A row of
- *   X that holds a non-finite value spoils its own row of Y only.
+ *   multiplies each group's sum once; the order of the sums is fixed.  The
+ *   sums hold terms up to 31 |X|: a group's must stay within fp32's range.  A
+ *   row of X that holds a non-finite value spoils its own row of Y only.
  * tern_layer_q4_matvec -- the same for 1 to 8 projections that share T and the
  *   types (a layer's receptance, key and value on one token), in one launch.
  *   Inputs may be shared; no output may overlap an input or another output.

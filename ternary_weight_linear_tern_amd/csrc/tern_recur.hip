@@ -196,10 +196,15 @@ __device__ inline void copy_empty(const RecurArgs &a, int64_t group, int col, co
     }
 }
 
-// (A, B) applied to h, and the A of (A1, B1) after (A0, B0).  A = 0 forgets
-// what came before, whatever it holds.
+// (A, B) applied to h, and the A of (A1, B1) after (A0, B0).  A = 0 means that a
+// sequence starts among the rows, and forgets what came before, whatever it
+// holds.  Without a start A stays above 0 where the product of the kept shares
+// would reach it, so that a NaN or an infinity goes on to its sequence's end as it
+// does token by token (a finite state adds 1e-45 of itself).
+constexpr float kTiny = 1.401298464e-45f;
+__device__ inline float kept(float A, bool restart) { return restart ? 0.0f : fmaxf(A, kTiny); }
 __device__ inline float apply(float A, float B, float h) { return A == 0.0f ? B : fmaf(A, h, B); }
-__device__ inline float compose(float A1, float A0) { return A1 == 0.0f ? 0.0f : A1 * A0; }
+__device__ inline float compose(float A1, float A0) { return kept(A1 * A0, A1 == 0.0f || A0 == 0.0f); }
 
 // ---------------------------------------------------------------------------
 // The chain of chunks.  A pair (A, B) and a state are published as one 64-bit
@@ -211,12 +216,16 @@ __device__ inline float compose(float A1, float A0) { return A1 == 0.0f ? 0.0f :
 // Workgroups take their chunk of a column block from a counter, in chain
 // order, so whoever waits for an earlier chunk waits for a workgroup that runs
 // already; that one publishes its pair before it waits for anything, and the
-// first chunk waits for nothing: every wait ends.
+// first chunk waits for nothing: every wait ends.  Two calls at once that share
+// a workspace against the rules wipe each other's words and tickets: a ticket
+// past the last chunk has no work, and a wait gives up after a few seconds and
+// goes on with a NaN.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr int kTicketStride = 32;   // words
 constexpr int kBack = 16;           // chunks looked back over
+constexpr int kPatience = 1 << 21;  // looks at other chunks' words, each above 1 us
 
 __device__ inline uint32_t word_of(float x) {
     const uint32_t w = __builtin_bit_cast(uint32_t, x);
@@ -243,10 +252,11 @@ __global__ __launch_bounds__(256) void recur_init_kernel(uint4 *empty, int64_t n
 }
 
 // Lanes 0 .. 15 watch one column of the 16 chunks before chunk i until one has
-// its state and all chunks after that their pairs.
-__device__ inline void watch(const RecurArgs &a, int i, int col0) {
+// its state and all chunks after that their pairs, or until `looks` reaches the
+// limit.
+__device__ inline void watch(const RecurArgs &a, int i, int col0, int &looks) {
     const int lane = threadIdx.x & 63, p = i - 1 - lane;
-    while (true) {
+    while (looks++ < kPatience) {
         bool has_state = lane < kBack && p < 0, has_pair = false;   // before the first chunk the state is zero
         if (lane < kBack && p >= 0) {
             has_state = state_at(a.prefix + (int64_t)p * a.C + col0) != kEmpty;
@@ -312,8 +322,9 @@ __device__ inline void enter(const RecurArgs &a, int i, int order, bool fresh, i
     if (a.nch > 1) {
         // lanes past the last column take part with the last ones
         const int c = col < a.C ? col : a.C - N;
+        int looks = 0;
         for (bool first = true; !sKnown; first = false) {
-            if (!first) watch(a, i, col0);
+            if (!first) watch(a, i, col0, looks);
             unsigned long long pr[J][N];
             uint32_t st[J][N];
 #pragma unroll
@@ -360,12 +371,16 @@ __device__ inline void enter(const RecurArgs &a, int i, int order, bool fresh, i
                                          __builtin_bit_cast(float, (uint32_t)(pr >> 32)), h[k]);
                         }
                 }
-                if (all && !sClosed && col < a.C)
+                const bool done = all || looks >= kPatience;
+                if (!all)
+#pragma unroll
+                    for (int k = 0; k < N; k++) h[k] = __builtin_nanf("");
+                if (done && !sClosed && col < a.C)
 #pragma unroll
                     for (int k = 0; k < N; k++)
                         publish_state(a.prefix + (int64_t)i * a.C + col + k, apply(A[k], B[k], h[k]));
-                if (all) store_f<N>(&sH[at], h);
-                sKnown = all;
+                if (done) store_f<N>(&sH[at], h);
+                sKnown = done;
             }
             __syncthreads();
         }
@@ -418,6 +433,7 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     float A[N], B[N], h[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
+    bool restart = false;
     if (on) {
         auto row = [&](int j) {
             float vf[N];
@@ -429,9 +445,10 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             }
         };
         if (whole) {
+            restart = begins;
             if (begins)
 #pragma unroll
-                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = start[i];
+                for (int i = 0; i < N; i++) B[i] = start[i];
 #pragma unroll
             for (int j = 0; j < kBlk; j++) row(j);
         } else {
@@ -442,13 +459,16 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
                 s.forth(j);
                 if (!s.live) continue;
                 if (j == s.b) {
+                    restart = true;
 #pragma unroll
-                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
+                    for (int i = 0; i < N; i++) B[i] = 0.0f;
                     if (a.h0) load_f<N>(a.h0 + s.c.cur * a.C + col, B);
                 }
                 row(j);
             }
         }
+#pragma unroll
+        for (int i = 0; i < N; i++) A[i] = kept(A[i], restart);
     }
     // the first wave's answer counts: does the chunk begin with a sequence's start?
     enter<N, W>(a, ch, wave, at.b == 0, col, cb * 64 * N, A, B, h, [] {});
@@ -500,7 +520,8 @@ __global__ __launch_bounds__(64 * W, 4) void recur_fwd_kernel(RecurArgs a) {
         if (wave == 0) copy_empty<E::N>(a, b / a.ncb, col, a.h0, a.hT);
         return;
     }
-    fwd_chunk<E, W>(a, cb, col, wave, take_ticket(a, cb));
+    const int i = take_ticket(a, cb);
+    if (i < a.nch) fwd_chunk<E, W>(a, cb, col, wave, i);
 }
 
 // dY of one token, in the activations' type (D = E) or in fp32
@@ -552,6 +573,7 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
     float A[N], B[N];
 #pragma unroll
     for (int i = 0; i < N; i++) A[i] = 1.0f, B[i] = 0.0f;
+    bool restart = false;
     if (on) {
         auto row = [&](int j) {
             float kf[N], rf[N], d[N];
@@ -566,9 +588,10 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             }
         };
         if (whole) {
+            restart = ends;
             if (ends)
 #pragma unroll
-                for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = stop[i];
+                for (int i = 0; i < N; i++) B[i] = stop[i];
 #pragma unroll
             for (int j = kBlk - 1; j >= 0; j--) row(j);
         } else {
@@ -579,13 +602,16 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
                 s.back(j);
                 if (!s.live) continue;
                 if (j + 1 == s.e) {
+                    restart = true;
 #pragma unroll
-                    for (int i = 0; i < N; i++) A[i] = 0.0f, B[i] = 0.0f;
+                    for (int i = 0; i < N; i++) B[i] = 0.0f;
                     if (a.dhT) load_f<N>(a.dhT + s.c.cur * a.C + col, B);
                 }
                 row(j);
             }
         }
+#pragma unroll
+        for (int i = 0; i < N; i++) A[i] = kept(A[i], restart);
     }
     float p[N], hb[kBlk][N];
     // the last wave's answer counts: does the chunk end with a sequence's last token?
@@ -668,7 +694,8 @@ __global__ __launch_bounds__(64 * W, 3) void recur_bwd_kernel(RecurArgs a) {
         if (wave == 0) copy_empty<E::N>(a, b / a.ncb, col, a.dhT, a.dh0);
         return;
     }
-    bwd_chunk<E, D, W>(a, cb, col, wave, take_ticket(a, cb));   // the chain runs from the last chunk
+    const int i = take_ticket(a, cb);
+    if (i < a.nch) bwd_chunk<E, D, W>(a, cb, col, wave, i);   // the chain runs from the last chunk
 }
 
 // One token of every sequence: a row each, elementwise.

@@ -154,6 +154,30 @@ def test_recur_saturated_gates(act):
         c.check()
 
 
+@pytest.mark.parametrize("gate", [(-3.0, 3.0), (3.0, 6.0), (22.0, 25.0)])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["V", "K", "h0", "dY", "dhT"])
+def test_non_finite_value_lasts_to_its_sequences_end(where, act, gate):
+    """However little of a state the gates keep (with gates near 1 the product of
+    the kept shares underflows within a few rows), a NaN stays in the state, token
+    by token, and the outputs are finite exactly where the definition's are."""
+    log(f"recur NaN in {where}, {act}, gates {gate}")
+    c = Case(1003, 136, act, [900, 0, 103], gate=gate, seed=5)
+    bad = getattr(c, where)
+    row = {"V": 37, "K": 37, "h0": 0, "dY": 850, "dhT": 0}[where]
+    bad[row, 3] = float("nan")
+    bad[row, 135] = float("inf") if where in ("V", "h0") else float("nan")
+    c.fwd()
+    c.bwd()
+    torch.cuda.synchronize()
+    i, dY, dhT = c.host()
+    with np.errstate(all="ignore"):
+        want = list(ref.forward(**i)[:2]) + list(ref.backward(**i, dY=dY, dhT=dhT)[:4])
+    for name, got, w in zip(("Y", "hT", "dK", "dV", "dR", "dh0"), c.outputs(), want):
+        got = np.isfinite(got.double().cpu().numpy())
+        assert np.array_equal(got, np.isfinite(w)), f"{name}: first {np.argwhere(got != np.isfinite(w))[0]}"
+
+
 @pytest.mark.parametrize("C", [40, 2056])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_recur_sequences_are_apart(bad, C):

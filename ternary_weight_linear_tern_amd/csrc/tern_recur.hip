@@ -18,13 +18,14 @@
 //     and the pairs in between;
 //   - it publishes its own closing state, and every wave walks its rows again
 //     in registers, from the state that enters them, and writes Y.
-// K, V, R are read once and Y is written once (32768 x 4096 bf16 in one sequence:
-// 279 us, 3.9 TB/s of the 5.1 of a copy; with the pairs, the chain and the
-// output in three launches that read K and V twice 345 us).  What bounds it is
-// the time a chunk's registers are held: the loads, about 3 us for the words of
-// other chunks, the output.  The pairs in between are
-// applied in order to the state found, the same operations whichever chunk
-// that was: results do not depend on timing.
+// K, V, R are read once and Y is written once: 32768 x 4096 bf16 in one sequence
+// 289 us, 3.7 TB/s of the 5.1 of a copy (with the pairs, the chain and the
+// output in three launches, which read K and V twice, 345 us); backward, with
+// fp32 dY, 560 us, 3.8 TB/s.  What bounds it is the time a chunk's registers are
+// held: the loads, about 3 us for the words of other chunks, the output.  Short
+// calls (2048 x 512: 12 us) are two launches and one such chunk's time.
+// The pairs in between are applied in order to the state found, the same
+// operations whichever chunk that was: results do not depend on timing.
 // A sequence's first token drops what came before: the composition restarts
 // there with A = 0 and B = h0, and a pair with A = 0 returns B without
 // multiplying, so nothing of one sequence (a NaN, an infinity) reaches the
@@ -735,11 +736,11 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Waves of a chunk, and a lane's share of a bf16 row.  What decides is how many
 // waves the registers leave room for while each holds 16 rows, and how many
 // chunks the chain passes through:
-//   forward   8 waves, two channels a lane (122 registers, 16 waves a compute
-//             unit): 32768 x 4096 279 us; 4 waves 372, 16 waves 355, one channel
-//             321;
-//   backward  4 waves, one channel a lane (137 registers, 12 waves): 32768 x
-//             4096 569 us; 8 waves 755, two channels 587.
+//   forward   8 waves, two channels a lane (118 registers, 16 waves a compute
+//             unit): 32768 x 4096 289 us; 4 waves 377, 16 waves 385, one channel
+//             309;
+//   backward  4 waves, one channel a lane (135 registers, 12 waves): 32768 x
+//             4096 560 us; 8 waves 686, two channels 714.
 constexpr int kFwdWaves = 8, kBwdWaves = 4;
 constexpr int kFwdCols = 128, kBwdCols = 64;   // columns of a workgroup, bf16 (fp32: 64)
 struct RecurPlan {

@@ -493,23 +493,31 @@ struct Shape {
 constexpr Shape kShapes[] = {{128, 1, 14.0, 0.44, 1.10}, {96, 1, 9.0, 0.32, 0.65}, {64, 1, 6.0, 0.17, 0.33},
                              {32, 2, 4.5, 0.09, 0.21}};
 
-// The cheapest shape: the launch ends no sooner than its longest tile and
-// than the mean load of a unit.
+// The cheapest shape.  Units that are all busy take the tiles in full rounds, and
+// what is left over (the shortest sums, which come last) in one with less
+// company; and the launch ends no sooner than its longest tile.  (Over 19 sizes,
+// single and of six matrices, 128 x 8192 to 4096 x 16384, the choice is within
+// 0.5 % of the best shape in the mean and 3 % but for two; without the last round
+// 2048 x 2048 took the smallest tiles, 24 us against 18.)
 int choose_shape(int mode, const OrthoArgs &a) {
     int best = 0;
     double least = 0.0;
     for (const Shape &s : kShapes) {
-        double sum = 0.0, longest = 0.0, tiles = 0.0;
+        double sum = 0.0, longest = 0.0, shortest = 0.0;
+        int64_t tiles = 0;
         for (int i = 0; i < a.n; i++) {
-            const double n = (double)tiles_of(mode, a.p[i], s.wt);
+            const int64_t n = tiles_of(mode, a.p[i], s.wt);
             const double k = (mode == ndev::GRAM ? a.p[i].np : a.p[i].mp) / 32.0;
             tiles += n;
-            sum += n * k;
+            sum += (double)n * k;
             longest = k > longest ? k : longest;
+            shortest = i == 0 || k < shortest ? k : shortest;
         }
-        const double slots = 256.0 * s.per_cu, load = tiles < slots ? tiles / slots : 1.0;
-        const double k = sum / slots > longest ? sum / slots : longest;
-        const double t = s.fixed + k * (s.alone + (s.busy - s.alone) * load);
+        const int slots = 256 * s.per_cu;
+        auto rate = [&](int64_t n) { return s.alone + (s.busy - s.alone) * (double)(n < slots ? n : slots) / slots; };
+        const int64_t left = tiles % slots;
+        const double rounds = (sum - (double)left * shortest) / slots * s.busy + (left ? shortest * rate(left) : 0.0);
+        const double t = s.fixed + std::max(rounds, longest * rate(tiles));
         if (!best || t < least) best = s.wt, least = t;
     }
     return best;

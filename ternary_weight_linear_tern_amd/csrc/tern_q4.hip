@@ -88,24 +88,54 @@ __device__ inline bf16x8 weights(uint32_t w) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
+// A wave's activations of 128 rows.  They are loaded in whole lines, a lane 16
+// bytes of a token's row, and brought through shared memory into the order of the
+// matrix instruction, whose lanes stand at 16 different tokens (loaded in that order,
+// every lane's 16 bytes cost the L1 cache an access of their own, which bound the
+// kernel: 13 rows of 16384 x 4096 in fp32 took 33.7 us, 16 in bf16 23.8).
+// The 16-byte pieces of a token's row are permuted by its number, so that
+// equal pieces of the 16 tokens fall in different banks.
+template <int TERMS>
+struct Rows {
+    static constexpr int ES = TERMS == 1 ? 2 : 4, kRowBytes = kRows * ES, kBytes = 16 * kRowBytes;
+    static constexpr int kPieces = kRowBytes / 16, kPer = 64 / kPieces, kLoads = 16 / kPer;   // kPer: tokens a load
+    u32x4 v[kLoads];
+    // rows r0 .. of the tokens at X (nt of them)
+    __device__ void load(const char *X, int nt, int in, int r0, int lane) {
+        const int t = lane / kPieces, piece = lane % kPieces;
+        const uint32_t at = (uint32_t)(t * in * ES + piece * 16);
+        const bool ok = r0 + piece * (16 / ES) < in;
+        const char *p = X + (int64_t)r0 * ES;
+#pragma unroll
+        for (int j = 0; j < kLoads; j++) {
+            v[j] = u32x4{0, 0, 0, 0};
+            if (ok && j * kPer + t < nt) v[j] = *(const u32x4 *)(p + (int64_t)j * kPer * in * ES + at);
+        }
+    }
+    __device__ void store(char *lds, int lane) const {
+        const int t = lane / kPieces, piece = lane % kPieces;
+#pragma unroll
+        for (int j = 0; j < kLoads; j++)
+            *(u32x4 *)(lds + (j * kPer + t) * kRowBytes + ((piece ^ (j * kPer + t)) * 16)) = v[j];
+    }
+};
+
 // 8 activations of a lane's token: as loaded, and as bf16 terms (TERMS 1:
 // bf16 activations; 3: fp32, cut into three terms of 8 significant bits)
 template <int TERMS>
 struct RawActs {
-    u32x4 v[TERMS == 1 ? 1 : 2];
+    static constexpr int kPieces = TERMS == 1 ? 1 : 2;
+    u32x4 v[kPieces];
+    __device__ void read(const char *lds, int tok, int ck, int sub) {
+#pragma unroll
+        for (int i = 0; i < kPieces; i++)
+            v[i] = *(const u32x4 *)(lds + tok * Rows<TERMS>::kRowBytes + (((ck * 4 + sub) * kPieces + i) ^ tok) * 16);
+    }
 };
 template <int TERMS>
 struct Acts {
     bf16x8 t[TERMS];
 };
-template <int TERMS>
-__device__ inline void load_acts(RawActs<TERMS> &a, const void *X, int64_t at, bool ok) {
-#pragma unroll
-    for (int i = 0; i < (TERMS == 1 ? 1 : 2); i++) {
-        a.v[i] = u32x4{0, 0, 0, 0};
-        if (ok) a.v[i] = *((const u32x4 *)((const char *)X + at * (TERMS == 1 ? 2 : 4)) + i);
-    }
-}
 template <int TERMS>
 __device__ inline Acts<TERMS> terms(const RawActs<TERMS> &a) {
     Acts<TERMS> r;
@@ -146,55 +176,45 @@ struct Scales {
     }
 };
 
-// The activations and scales of 128 rows (GC: 32-row chunks of a scale group).
-template <int TERMS, bool SBF, int NB, int GC>
-struct Side {
-    RawActs<TERMS> x[4];
-    typename Scales<SBF>::Raw s[4 / GC][NB];
-};
-
-// Blocks k0 .. k1 - 1 of a wave's NB column blocks.  The weights, which come
-// from HBM, are loaded kAhead blocks ahead, the activations and scales, which
-// mostly come from L2, one block ahead.
+// Blocks k0 .. k1 - 1 of a wave's NB column blocks (GC: 32-row chunks of a scale
+// group).  The weights, which come from HBM, are loaded kAhead blocks ahead, the
+// activations and scales, which mostly come from L2, one block ahead.
 constexpr int kAhead = 2;
 template <int TERMS, bool SBF, int NB, int GC>
-__device__ inline void run_blocks(const Q4One &p, int T, int tok, int sub, const u32x4 *const (&W)[NB],
+__device__ inline void run_blocks(const Q4One &p, const char *X, int nt, int lane, char *lds, const u32x4 *const (&W)[NB],
                                   const int (&col)[NB], int k0, int k1, f32x4 (&y)[NB]) {
-    using S = Side<TERMS, SBF, NB, GC>;
-    const int64_t xrow = (int64_t)tok * p.in + sub * 8;
-    const int ng = (p.in + GC * 32 - 1) / (GC * 32);
+    using Sc = typename Scales<SBF>::Raw;
+    const int ng = (p.in + GC * 32 - 1) / (GC * 32), tok = lane & 15, sub = lane >> 4;
     u32x4 w[kAhead][NB];
+    Rows<TERMS> rows;
+    Sc sc[2][4 / GC][NB];
     auto load_w = [&](u32x4 (&o)[NB], int kb) {
 #pragma unroll
         for (int i = 0; i < NB; i++) o[i] = W[i][(int64_t)(kb < k1 ? kb : k1 - 1) * 64];
     };
-    auto load_side = [&](S &b, int kb) {
-        kb = kb < k1 ? kb : k1 - 1;
-#pragma unroll
-        for (int ck = 0; ck < 4; ck++) {
-            const int r = kb * kRows + ck * 32;
-            load_acts<TERMS>(b.x[ck], p.X, xrow + r, tok < T && r + sub * 8 < p.in);
-        }
+    auto load_s = [&](Sc (&o)[4 / GC][NB], int kb) {
 #pragma unroll
         for (int g = 0; g < 4 / GC; g++) {
             // a group past the last row (its weights multiply zeros) takes the last scale
             const int at = kb * (4 / GC) + g;
 #pragma unroll
             for (int i = 0; i < NB; i++)
-                b.s[g][i] = Scales<SBF>::load(p.gscale, (int64_t)(at < ng ? at : ng - 1) * p.out + col[i]);
+                o[g][i] = Scales<SBF>::load(p.gscale, (int64_t)(at < ng ? at : ng - 1) * p.out + col[i]);
         }
     };
     bf16x8 off;
 #pragma unroll
     for (int e = 0; e < 8; e++) off[e] = (__bf16)-24.0f;
-    auto work = [&](const u32x4 (&wb)[NB], const S &b) {
+    auto work = [&](const u32x4 (&wb)[NB], const Sc (&sb)[4 / GC][NB]) {
 #pragma unroll
         for (int g = 0; g < 4 / GC; g++) {
             f32x4 acc[NB];
 #pragma unroll
             for (int c = 0; c < GC; c++) {
                 const int ck = g * GC + c;
-                const Acts<TERMS> x = terms<TERMS>(b.x[ck]);
+                RawActs<TERMS> raw;
+                raw.read(lds, tok, ck, sub);
+                const Acts<TERMS> x = terms<TERMS>(raw);
                 f32x4 z = {0, 0, 0, 0};
 #pragma unroll
                 for (int t = 0; t < TERMS; t++) z = mfma(off, x.t[t], z);
@@ -208,23 +228,30 @@ __device__ inline void run_blocks(const Q4One &p, int T, int tok, int sub, const
             }
 #pragma unroll
             for (int i = 0; i < NB; i++) {
-                const f32x4 s = Scales<SBF>::get(b.s[g][i]);
+                const f32x4 s = Scales<SBF>::get(sb[g][i]);
 #pragma unroll
                 for (int r = 0; r < 4; r++) y[i][r] = fmaf(s[r], acc[i][r], y[i][r]);
             }
         }
     };
-    S side[2];
 #pragma unroll
     for (int j = 0; j < kAhead; j++) load_w(w[j], k0 + j);
-    load_side(side[0], k0);
+    rows.load(X, nt, p.in, k0 * kRows, lane);
+    load_s(sc[0], k0);
     for (int kb = k0; kb < k1; kb += kAhead) {
 #pragma unroll
         for (int j = 0; j < kAhead; j++) {
             if (kb + j < k1) {
-                load_side(side[(j + 1) & 1], kb + j + 1);
+                const int next = kb + j + 1 < k1 ? kb + j + 1 : k1 - 1;
+                // (the fences keep the order of a wave's own accesses to its piece of
+                // shared memory, which needs no wait)
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                rows.store(lds, lane);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                rows.load(X, nt, p.in, next * kRows, lane);
+                load_s(sc[(j + 1) & 1], next);
                 __builtin_amdgcn_sched_barrier(0);
-                work(w[j], side[j & 1]);
+                work(w[j], sc[j & 1]);
                 load_w(w[j], kb + j + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -237,12 +264,17 @@ __device__ inline void run_blocks(const Q4One &p, int T, int tok, int sub, const
 // order of the waves.
 template <int TERMS, bool SBF, int NB>
 __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a) {
-    __shared__ float red[max_waves(TERMS, NB)][16][NB * kCols + 4];
+    extern __shared__ __attribute__((aligned(16))) char lds[];   // lds_bytes()
+    using Red = float[16][NB * kCols + 4];
+    Red *const red = (Red *)(lds + a.waves * Rows<TERMS>::kBytes);
     int pi = 0;
     while (pi + 1 < a.n && (int)blockIdx.x >= a.p[pi + 1].start) pi++;
     const Q4One p = a.p[pi];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tok0 = blockIdx.y * 16, tok = tok0 + (lane & 15), sub = lane >> 4;
+    const int tok0 = blockIdx.y * 16, sub = lane >> 4;
+    const int nt = a.T - tok0 < 16 ? a.T - tok0 : 16;
+    const char *X = (const char *)p.X + (int64_t)tok0 * p.in * Rows<TERMS>::ES;
+    char *xs = lds + wave * Rows<TERMS>::kBytes;
     const int ncb = (p.out + kCols - 1) / kCols;
     const int cb0 = ((int)blockIdx.x - p.start) * NB;
     const int per = (p.nkb + a.waves - 1) / a.waves;
@@ -260,14 +292,13 @@ __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a)
         y[b] = f32x4{0, 0, 0, 0};
     }
     if (k0 < k1) {
-        if (p.group_chunks == 1) run_blocks<TERMS, SBF, NB, 1>(p, a.T, tok, sub, W, col, k0, k1, y);
-        else if (p.group_chunks == 2) run_blocks<TERMS, SBF, NB, 2>(p, a.T, tok, sub, W, col, k0, k1, y);
-        else run_blocks<TERMS, SBF, NB, 4>(p, a.T, tok, sub, W, col, k0, k1, y);
+        if (p.group_chunks == 1) run_blocks<TERMS, SBF, NB, 1>(p, X, nt, lane, xs, W, col, k0, k1, y);
+        else if (p.group_chunks == 2) run_blocks<TERMS, SBF, NB, 2>(p, X, nt, lane, xs, W, col, k0, k1, y);
+        else run_blocks<TERMS, SBF, NB, 4>(p, X, nt, lane, xs, W, col, k0, k1, y);
     }
 #pragma unroll
     for (int b = 0; b < NB; b++) *(f32x4 *)&red[wave][lane & 15][b * kCols + sub * 4] = y[b];
     __syncthreads();
-    const int nt = a.T - tok0 < 16 ? a.T - tok0 : 16;
     for (int i = threadIdx.x; i < nt * NB * kCols; i += a.waves * 64) {
         const int t = i / (NB * kCols), c = i % (NB * kCols);
         float v = red[0][t][c];
@@ -279,6 +310,11 @@ __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a)
             else ((float *)p.Y)[o] = v;
         }
     }
+}
+
+template <int TERMS, int NB>
+int lds_bytes(int waves) {
+    return waves * (Rows<TERMS>::kBytes + 16 * (NB * kCols + 4) * 4);
 }
 
 }  // namespace qdev
@@ -298,8 +334,8 @@ bool sizes_ok(int64_t in, int64_t out) {
 
 template <int TERMS, bool SBF>
 void launch_nb(int nb, dim3 g, dim3 b, hipStream_t st, const qdev::Q4Args &a) {
-    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 1>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 2>), g, b, 0, st, a);
+    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 1>), g, b, (qdev::lds_bytes<TERMS, 1>(a.waves)), st, a);
+    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 2>), g, b, (qdev::lds_bytes<TERMS, 2>(a.waves)), st, a);
 }
 
 }  // namespace

@@ -17,6 +17,13 @@
 //
 // fp32 activations are cut into three bf16 terms of 8 significant bits each,
 // exactly, and multiplied term by term.
+//
+// What bounds it: one bf16 token of 4096 x 16384 takes 10.8 us, 3.3 TB/s of the 5.1 of a
+// copy (about 3 us are the launch's start and the first loads); three 2048 x 2048
+// 5.7 us, two thirds of it that latency.  More tokens read the activations
+// once a column block, through shared memory (16 bf16 tokens 13.5 us); fp32 ones pass
+// it as 12 KiB a block and wave and are cut there, which bounds 13 rows of 16384 x
+// 4096 at 29 us, 1.3 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <type_traits>
@@ -34,8 +41,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCols = 16, kRows = 128;          // a block of the packed matrix: 1 KiB
 constexpr int kBlockWords = kCols * kRows / 8;
-// waves of a workgroup: 16 where 128 registers a lane are enough
-constexpr int max_waves(int terms, int nb) { return terms == 1 && nb == 1 ? 16 : 8; }
+// waves of a workgroup, at most: 16 where 128 registers a lane are enough; with fp32
+// activations shared memory holds 12 (13 rows of 16384 x 4096: 29 us, 8 waves 32)
+constexpr int max_waves(int terms, int nb) { return nb == 1 ? (terms == 1 ? 16 : 12) : 8; }
 
 // Word w of lane l of a block: rows 32 w + 8 (l / 16) + e (e < 8), column
 // l % 16.  Rows e = 2 d and 2 d + 1 stand at bits 4 d + 3 and 4 d + 19 (mod 32), so
@@ -93,13 +101,17 @@ __device__ inline bf16x8 weights(uint32_t w) {
 // matrix instruction, whose lanes stand at 16 different tokens (loaded in that order,
 // every lane's 16 bytes cost the L1 cache an access of their own, which bound the
 // kernel: 13 rows of 16384 x 4096 in fp32 took 33.7 us, 16 in bf16 23.8).
+// fp32 ones are cut on the way, TERMS matrices of bf16, for the tokens that are
+// there; the places of other tokens hold anything, and spoil only results that are
+// not written.
 // The 16-byte pieces of a token's row are permuted by its number, so that
 // equal pieces of the 16 tokens fall in different banks.
 template <int TERMS>
 struct Rows {
-    static constexpr int ES = TERMS == 1 ? 2 : 4, kRowBytes = kRows * ES, kBytes = 16 * kRowBytes;
-    static constexpr int kPieces = kRowBytes / 16, kPer = 64 / kPieces, kLoads = 16 / kPer;   // kPer: tokens a load
+    static constexpr int ES = TERMS == 1 ? 2 : 4, kTerm = 16 * kRows * 2, kBytes = TERMS * kTerm;
+    static constexpr int kPieces = kRows * ES / 16, kPer = 64 / kPieces, kLoads = 16 / kPer;   // kPer: tokens a load
     u32x4 v[kLoads];
+    __device__ static char *place(char *lds, int tok, int piece) { return lds + tok * kRows * 2 + (piece ^ tok) * 16; }
     // rows r0 .. of the tokens at X (nt of them)
     __device__ void load(const char *X, int nt, int in, int r0, int lane) {
         const int t = lane / kPieces, piece = lane % kPieces;
@@ -112,53 +124,34 @@ struct Rows {
             if (ok && j * kPer + t < nt) v[j] = *(const u32x4 *)(p + (int64_t)j * kPer * in * ES + at);
         }
     }
-    __device__ void store(char *lds, int lane) const {
+    __device__ void store(char *lds, int nt, int lane) const {
         const int t = lane / kPieces, piece = lane % kPieces;
 #pragma unroll
-        for (int j = 0; j < kLoads; j++)
-            *(u32x4 *)(lds + (j * kPer + t) * kRowBytes + ((piece ^ (j * kPer + t)) * 16)) = v[j];
-    }
-};
-
-// 8 activations of a lane's token: as loaded, and as bf16 terms (TERMS 1:
-// bf16 activations; 3: fp32, cut into three terms of 8 significant bits)
-template <int TERMS>
-struct RawActs {
-    static constexpr int kPieces = TERMS == 1 ? 1 : 2;
-    u32x4 v[kPieces];
-    __device__ void read(const char *lds, int tok, int ck, int sub) {
+        for (int j = 0; j < kLoads; j++) {
+            if (j * kPer >= nt) continue;
+            if constexpr (TERMS == 1) {
+                *(u32x4 *)place(lds, j * kPer + t, piece) = v[j];
+            } else {
+                // 4 values, each cut into terms of 8 significant bits
+                uint32_t x[4] = {v[j][0], v[j][1], v[j][2], v[j][3]};
+                char *at = place(lds, j * kPer + t, piece >> 1) + (piece & 1) * 8;
 #pragma unroll
-        for (int i = 0; i < kPieces; i++)
-            v[i] = *(const u32x4 *)(lds + tok * Rows<TERMS>::kRowBytes + (((ck * 4 + sub) * kPieces + i) ^ tok) * 16);
-    }
-};
-template <int TERMS>
-struct Acts {
-    bf16x8 t[TERMS];
-};
-template <int TERMS>
-__device__ inline Acts<TERMS> terms(const RawActs<TERMS> &a) {
-    Acts<TERMS> r;
-    if constexpr (TERMS == 1) {
-        r.t[0] = __builtin_bit_cast(bf16x8, a.v[0]);
-    } else {
-        uint32_t v[8];
+                for (int i = 0; i < TERMS; i++) {
+                    *(u32x2 *)(at + i * kTerm) = u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x07060302u),   // upper halves
+                                                       __builtin_amdgcn_perm(x[3], x[2], 0x07060302u)};
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = a.v[i >> 2][i & 3];
-#pragma unroll
-        for (int t = 0; t < 3; t++) {
-            u32x4 o;
-#pragma unroll
-            for (int d = 0; d < 4; d++) o[d] = __builtin_amdgcn_perm(v[2 * d + 1], v[2 * d], 0x07060302u);   // upper halves
-            r.t[t] = __builtin_bit_cast(bf16x8, o);
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, v[i]) -
-                                                        __builtin_bit_cast(float, v[i] & 0xFFFF0000u));
+                    for (int e = 0; e < 4; e++)
+                        x[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x[e]) -
+                                                                __builtin_bit_cast(float, x[e] & 0xFFFF0000u));
+                }
+            }
         }
     }
-    return r;
-}
+    // 8 activations of a token, rows 32 ck + 8 sub .., of one term
+    __device__ static bf16x8 read(const char *lds, int term, int tok, int ck, int sub) {
+        return *(const bf16x8 *)place(const_cast<char *>(lds) + term * kTerm, tok, ck * 4 + sub);
+    }
+};
 
 // the 4 scales of a lane's columns: as loaded, and as fp32
 template <bool SBF>
@@ -212,18 +205,18 @@ __device__ inline void run_blocks(const Q4One &p, const char *X, int nt, int lan
 #pragma unroll
             for (int c = 0; c < GC; c++) {
                 const int ck = g * GC + c;
-                RawActs<TERMS> raw;
-                raw.read(lds, tok, ck, sub);
-                const Acts<TERMS> x = terms<TERMS>(raw);
+                bf16x8 x[TERMS];
+#pragma unroll
+                for (int t = 0; t < TERMS; t++) x[t] = Rows<TERMS>::read(lds, t, tok, ck, sub);
                 f32x4 z = {0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < TERMS; t++) z = mfma(off, x.t[t], z);
+                for (int t = 0; t < TERMS; t++) z = mfma(off, x[t], z);
 #pragma unroll
                 for (int i = 0; i < NB; i++) {
                     acc[i] = c ? acc[i] + z : z;
                     const bf16x8 q = weights(wb[i][ck]);
 #pragma unroll
-                    for (int t = 0; t < TERMS; t++) acc[i] = mfma(q, x.t[t], acc[i]);
+                    for (int t = 0; t < TERMS; t++) acc[i] = mfma(q, x[t], acc[i]);
                 }
             }
 #pragma unroll
@@ -246,7 +239,7 @@ __device__ inline void run_blocks(const Q4One &p, const char *X, int nt, int lan
                 // (the fences keep the order of a wave's own accesses to its piece of
                 // shared memory, which needs no wait)
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                rows.store(lds, lane);
+                rows.store(lds, nt, lane);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 rows.load(X, nt, p.in, next * kRows, lane);
                 load_s(sc[(j + 1) & 1], next);
@@ -400,11 +393,12 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
     qdev::Q4Args a{};
     // Shape of the launch.  From 1024 column blocks on (4 a compute unit) a
     // wave takes two, which share its activations, and 4 waves share the rows:
-    // 4096 x 16384, one token 10.6 us against 11.8 with single blocks, 16 tokens
-    // 14.1 against 20.7.  Fewer blocks take one each (4096 x 4096 5.3 us against
-    // 6.1), and enough waves that each has about 4 row blocks, which is all it
-    // needs to hide its loads (16384 x 2048: 16 waves 10.9 us, 8 13.1, 4 20.0;
-    // three 2048 x 2048: 4 waves 5.2, 8 5.5, 16 7.7).
+    // 4096 x 16384, one bf16 token 11.6 us against 13.9 with single blocks (8 waves
+    // 13.5, 2 16.9), 16 fp32 tokens 22.4 against 37.1.  Fewer blocks take one
+    // each (4096 x 4096 5.6 us against 7.8 with two, 16384 x 4096 12.4 against
+    // 23.9), and enough waves that each has about 4 row blocks, which is all it
+    // needs to hide its loads (4096 x 4096: 4 row blocks a wave 5.6 us, 8 6.8; three
+    // 2048 x 2048: 4 waves 5.7, 2 7.6).
     int64_t maxk = 1, ncb = 0;
     for (int i = 0; i < n; i++) {
         maxk = projs[i].in > maxk ? projs[i].in : maxk;

@@ -154,6 +154,19 @@ def test_recur_saturated_gates(act):
         c.check()
 
 
+@pytest.mark.parametrize("act,dy", [("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("lens", [[16, 32, 0, 128, 64, 16, 0, 240], [8, 8, 112, 1, 15, 144], [512], [500]])
+def test_recur_borders_on_and_off_the_blocks(lens, state, act, dy):
+    """Sequences that start or end with a block of 16 rows or a chunk, next to
+    ones that do not, with and without states to start from; up to 12 rows behind."""
+    log(f"recur borders {lens} state={state} {act}")
+    c = Case(512 if sum(lens) > 300 else 300, 72, act, lens, False, dy, seed=sum(lens), state=state)
+    c.fwd()
+    c.bwd()
+    c.check()
+
+
 @pytest.mark.parametrize("gate", [(-3.0, 3.0), (3.0, 6.0), (22.0, 25.0)])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("where", ["V", "K", "h0", "dY", "dhT"])

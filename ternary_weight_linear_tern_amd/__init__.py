@@ -1,5 +1,6 @@
 """Python binding of libtern, the MI355X forward and backward of the SR4
-ternary projection (C ABI in include/tern.h).
+ternary projection, with the recurrence, the 4-bit products and the
+orthogonalisation that stand around it in a layer (C ABI in include/tern.h).
 
 The functions below carry the C entry points' names and only marshal
 arguments: torch tensors (device memory) become raw pointers, the current HIP

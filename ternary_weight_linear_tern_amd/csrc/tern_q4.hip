@@ -26,6 +26,8 @@
 // 4096 at 29 us, 1.3 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/tern.h"
@@ -412,7 +414,6 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
     if (waves > nkb) waves = nkb;
     a.waves = (int)waves;
     a.T = (int)T;
-    int64_t wgs = 0;
     for (int i = 0; i < n; i++) {
         const tern_q4_proj_t &p = projs[i];
         if (p.out == 0) continue;
@@ -420,8 +421,13 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
         o.X = p.X; o.packed = p.packed; o.gscale = p.gscale; o.Y = p.Y;
         o.in = (int)p.in; o.out = (int)p.out; o.nkb = (int)cdiv(p.in, qdev::kRows);
         o.group_chunks = (int)(p.group / 32);
-        o.start = (int)wgs;
-        wgs += cdiv(cdiv(p.out, qdev::kCols), nb);
+    }
+    // the longest sums start first (each projection's results are its own)
+    std::stable_sort(a.p, a.p + a.n, [](const qdev::Q4One &x, const qdev::Q4One &y) { return x.nkb > y.nkb; });
+    int64_t wgs = 0;
+    for (int i = 0; i < a.n; i++) {
+        a.p[i].start = (int)wgs;
+        wgs += cdiv(cdiv(a.p[i].out, qdev::kCols), nb);
     }
     if (wgs == 0 || T == 0) return TERN_OK;
     const dim3 g((unsigned)wgs, (unsigned)cdiv(T, 16)), b((unsigned)(a.waves * 64));

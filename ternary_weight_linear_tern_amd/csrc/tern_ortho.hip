@@ -10,11 +10,25 @@
 // The products run on the fp16 matrix cores with fp32 sums.  fp16 and not
 // bf16: X, A and B have known ranges (the polynomial keeps every singular
 // value, and so every element of X, below 1.2025; |A| <= 1.45, |B| <= 2.9), so
-// scaled by powers of two they fit fp16, whose three more bits make the
-// result's error that of its own rounding to bf16 (measured on gradients of
-// full rank: 0.0020 rms against the 0.0017 of the rounding alone; with bf16
-// operands 0.010).
+// scaled by powers of two they fit fp16, whose three more bits count (bf16
+// operands: an error of 0.010 where fp16 ones leave 0.0012).
 //   X is held as 2^14 X, A as 2^14 A, B as 2^13 B.
+//
+// What is rounded, and what is not.  A rounding of X itself would be noise in
+// every direction, and a direction in which G has next to nothing grows 3.44
+// times a step: over five steps such noise reaches 0.02 of O for a G of rank 64
+// of 512, and 0.15 for rank one.  So X = H + L is held in two terms of fp16, 22
+// bits, and a X takes both; the products take H, whose rounding they pass on only
+// to the directions in which B is large, where X has stopped growing.  There
+// B L, the part left out, is most of the error.  Its largest part, that of B's
+// diagonal, is put back in the last two steps (before them it would take from
+// the weak directions what it gives to the strong ones), and so is in every step
+// what the rounding of B's diagonal loses.  With d = diag(B) in fp32, e = d less
+// its fp16 value:
+//   X <- (a + e) H + (a + d or a) L + B H
+// leaves, before O's rounding, 0.0007 of O for a flat spectrum, 0.0002 to 0.0009
+// for decaying and low-rank ones (emulated, 512 x 1024); O's rounding to bf16 is
+// 0.0017.
 // A and A^2 are symmetric: only the tiles on and above the diagonal are
 // computed, and each is written twice.  Every product is of the form P Q^T
 // with both operands contiguous along the sum: X is kept beside its transpose
@@ -44,11 +58,14 @@ constexpr float kEps = 1e-7f;
 constexpr float kXScale = 16384.0f;
 constexpr int kPad = 64;        // rows and columns of the working matrices: multiples of this, zeros
 constexpr int kParts = 256;     // partial sums of |G|^2
+constexpr float kLow = 2048.0f; // of X's low term, which is half a step of the high one at most
 
 struct OrthoOne {
     const void *G;
     void *O;
     h16 *X, *XT[2], *A, *B;   // [mp][np], [np][mp] twice, [mp][mp] twice
+    h16 *XL;                  // X's low term, 2^25 L, in the order of low_block()
+    float2 *diag;             // [mp]: a + e, a + d (or a)
     double *part;             // [kParts]
     int64_t rows, cols;       // of G and O
     int m, n, mp, np;         // of X: m <= n; padded
@@ -62,7 +79,26 @@ struct OrthoArgs {
     int g_bf16;
     int flip;                 // XT[flip] is current
     int last;                 // the last step writes O
+    int near;                 // one of the last two steps
 };
+
+// X's low term is read and written where X is computed, by the lane that holds the
+// element among the sums of a 32 x 32 block: it lies in that order, whatever the
+// tiles.  Blocks by rows, 1024 elements each: two pieces (g = 0, 1 and 2, 3) of 8 a
+// lane, element 4 (g & 1) + r of lane l being X's row 8 g + 4 (l / 32) + r and
+// column l % 32 of the block.
+__device__ inline h16 *low_block(const OrthoOne &p, int row, int col) {
+    return p.XL + ((int64_t)(row / 32) * (p.np / 32) + col / 32) * 1024 + (threadIdx.x & 63) * 8;
+}
+
+// A value whose fp16 rounding and remainder are both taken.  Left to itself the
+// compiler rounds twice, once within the operation that made the value and once
+// from its fp32 result, and where these fall on either side of a tie the two
+// terms do not belong together.
+__device__ inline float once(float x) {
+    asm("" : "+v"(x));
+    return x;
+}
 
 __device__ inline int problem_of(const OrthoArgs &a, int wg) {
     int pi = 0;
@@ -103,9 +139,9 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs a) {
     if (threadIdx.x == 0) p.part[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X and its transpose from G, 64 x 64 tiles, zeros in the padding
+// X, its transpose and its low term from G, 64 x 64 tiles, zeros in the padding
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
-    __shared__ h16 tile[64][68];
+    __shared__ h16 tile[64][68], low[64][68];
     const OrthoOne &p = a.p[problem_of(a, blockIdx.x)];
     // every wave adds up the partials (in the same order)
     const int lane = threadIdx.x & 63;
@@ -126,10 +162,15 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
         const int r = (threadIdx.x >> 4) + 16 * i;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (r0 + r < p.rows && c0 + c4 < p.cols) load4(p.G, a.g_bf16, (r0 + r) * p.cols + c0 + c4, v);
-        h16x4 o;
+        h16x4 o, l;
 #pragma unroll
-        for (int j = 0; j < 4; j++) o[j] = (h16)(v[j] * f);
+        for (int j = 0; j < 4; j++) {
+            const float x = once(v[j] * f);
+            o[j] = (h16)x;
+            l[j] = (h16)((x - (float)o[j]) * kLow);
+        }
         *(h16x4 *)&tile[r][c4] = o;
+        *(h16x4 *)&low[r][c4] = l;
     }
     __syncthreads();
     // the tile as it lies and transposed, into X and X^T (or the other way round)
@@ -148,6 +189,19 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
         *(h16x8 *)(same + (r0 + r) * lds + c0 + c8) = s;
         *(h16x8 *)(flip + (c0 + r) * ldf + r0 + c8) = q;
     }
+    // a block of the low term a wave
+    const int w = threadIdx.x >> 6, br = (w >> 1) * 32, bc = (w & 1) * 32, xc = bc + (lane & 31);
+    h16 *out = low_block(p, xi * 64 + br, xj * 64 + bc);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        h16x8 v;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int xr = br + 16 * h + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+            v[j] = p.tall ? low[xc][xr] : low[xr][xc];
+        }
+        *(h16x8 *)(out + 512 * h) = v;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -156,13 +210,13 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
 // ahead; the fragments of a stage are read into registers one stage ahead, so
 // the matrix cores run over the barrier (one a stage).
 //
-// What bounds it.  4096 x 16384: A 290 us, its polynomial 82, B X 540, five steps
-// 4.66 ms.  B X runs at 1.02 PFLOP/s (the vendor's plain product of that size 1.2):
-// the board is at its power cap (with zeros in all operands it takes 446 us), and
-// between the tiles the matrix cores wait for about 10 us while 128 KiB of the old X
-// are read and 256 KiB of the new one written.  Small matrices (six of 512 x 512 to
-// 512 x 2048, 155 us) are fifteen products of 5 to 13 us each, of which the
-// launch, the first loads and the results are 4 to 5.
+// What bounds it.  4096 x 16384: A 290 us, its polynomial 84, B X 577, five steps
+// 4.9 ms.  B X runs at 0.95 PFLOP/s (the vendor's plain product of that size 1.2):
+// the board is at its power cap, and between the tiles the matrix cores wait for
+// about 15 us while 256 KiB of the old X are read and 384 KiB of the new one written
+// (128 KiB each are the low term's, which costs 40 us of the 577).  Small matrices
+// (six of 512 x 512 to 512 x 2048, 169 us) are fifteen products of 5 to 15 us each, of
+// which the launch, the first loads and the results are 4 to 5.
 // ---------------------------------------------------------------------------
 
 enum { GRAM = 0, POLY = 1, APPLY = 2 };
@@ -351,6 +405,34 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
     constexpr uint32_t kNone = 0x7FFFFFF0u;
     constexpr int kAll = WT * WT / 8 / 64;                             // pieces a lane
     constexpr int NB = kAll % 8 == 0 ? 8 : kAll % 6 == 0 ? 6 : kAll;   // and how many at a time
+    // The low term and the diagonal's factors, of row of blocks i: on the way while
+    // the old matrix is read, all of a small tile's, of a large one's the first and then
+    // the next row's (read in turn, 4096 x 16384 takes 596 us a product, not 577).
+    h16x8 low[F][F][2];
+    float2 d[F][16];   // of rows 8 g + 4 lh + r, at 4 g + r
+    const __amdgpu_buffer_rsrc_t rdiag = rsrc(p.diag, (int64_t)p.mp * 8);
+    auto load_low = [&](int i) {
+        const int row = row0 + i * 32;
+#pragma unroll
+        for (int j = 0; j < F; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                low[i][j][h] = h16x8{};
+                if (row < p.mp && col0 + j * 32 < p.np)
+                    low[i][j][h] = *(const h16x8 *)(low_block(p, row, col0 + j * 32) + 512 * h);
+            }
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) {
+                const u32x4 v = load16(rdiag, (uint32_t)(row + 8 * g + 4 * lh + r) * 8);
+                d[i][4 * g + r] = __builtin_bit_cast(float2, u32x2{v[0], v[1]});
+                d[i][4 * g + r + 1] = __builtin_bit_cast(float2, u32x2{v[2], v[3]});
+            }
+    };
+    if (MODE == APPLY)
+#pragma unroll
+        for (int i = 0; i < (F > 2 ? 1 : F); i++) load_low(i);
     if (MODE != GRAM) {
         // the old matrix's term at [column][row] (A is symmetric)
         const h16 *old = (MODE == APPLY ? p.XT[a.flip] : p.A) + (int64_t)col0 * p.mp;
@@ -373,6 +455,8 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
 #pragma unroll
     for (int i = 0; i < F; i++) {
         char *at = T + lr * kT + (i * 32 + lh * 4) * 2;
+        const int row = row0 + i * 32;
+        if (MODE == APPLY && F > 2 && i + 1 < F) load_low(i + 1);
         h16x4 x[F][4];
         if (MODE != GRAM)
 #pragma unroll
@@ -388,14 +472,36 @@ __global__ __launch_bounds__(256) void ortho_gemm_kernel(OrthoArgs a) {
                 for (int r = 0; r < 4; r++) {
                     const float v = acc[i][j][g * 4 + r];
                     if (MODE == GRAM) o[r] = (h16)(v * (1.0f / 16384.0f));
-                    else if (MODE == POLY) o[r] = (h16)fmaf(0.5f * kB, (float)x[j][g][r], v * (kC / 32768.0f));
-                    else {
-                        const float y = fmaf(kA, (float)x[j][g][r], v * (1.0f / 8192.0f));
-                        o[r] = a.last ? __builtin_bit_cast(h16, (__bf16)(y * (1.0f / kXScale) * p.gain)) : (h16)y;
+                    else if (MODE == POLY) {
+                        const float b = once(fmaf(0.5f * kB, (float)x[j][g][r], v * (kC / 32768.0f)));   // 2^13 B
+                        o[r] = (h16)b;
+                        const int k = 8 * g + 4 * lh + r;
+                        if (ti == tj && wm == wn && i == j && k == lr && row + k < p.mp)
+                            p.diag[row + k] = float2{kA + (b - (float)o[r]) * (1.0f / 8192.0f),
+                                                     a.near ? kA + b * (1.0f / 8192.0f) : kA};
+                    } else {
+                        const int e = 4 * (g & 1) + r;
+                        const float2 c = d[i][4 * g + r];
+                        const float y = once(fmaf(
+                            c.x, (float)x[j][g][r],
+                            fmaf(c.y * (1.0f / kLow), (float)low[i][j][g >> 1][e], v * (1.0f / 8192.0f))));
+                        if (a.last) {
+                            o[r] = __builtin_bit_cast(h16, (__bf16)(y * (1.0f / kXScale) * p.gain));
+                        } else {
+                            o[r] = (h16)y;
+                            low[i][j][g >> 1][e] = (h16)((y - (float)o[r]) * kLow);
+                        }
                     }
                 }
                 *(h16x4 *)(at + j * 32 * kT + g * 16) = o;
             }
+        if (MODE == APPLY && !a.last)
+#pragma unroll
+            for (int j = 0; j < F; j++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    if (row < p.mp && col0 + j * 32 < p.np)
+                        *(h16x8 *)(low_block(p, row, col0 + j * 32) + 512 * h) = low[i][j][h];
     }
     const bool out = MODE == APPLY && a.last;   // into O, without the padding
     const int rows = out ? p.m : p.mp, cols = out ? p.n : qall;
@@ -459,7 +565,7 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct OrthoLayout {
     int64_t m, n, mp, np;
-    size_t x, xt0, xt1, a, b, part, total;   // byte offsets
+    size_t x, xt0, xt1, xl, a, b, diag, part, total;   // byte offsets
 };
 OrthoLayout layout(int64_t rows, int64_t cols) {
     OrthoLayout L{};
@@ -471,9 +577,11 @@ OrthoLayout layout(int64_t rows, int64_t cols) {
     L.x = 0;
     L.xt0 = mn;
     L.xt1 = 2 * mn;
-    L.a = 3 * mn;
-    L.b = 3 * mn + mm;
-    L.part = 3 * mn + 2 * mm;
+    L.xl = 3 * mn;
+    L.a = 4 * mn;
+    L.b = 4 * mn + mm;
+    L.diag = 4 * mn + 2 * mm;
+    L.part = L.diag + al256((size_t)L.mp * 8);
     L.total = L.m ? L.part + al256(ndev::kParts * 8) : 0;
     return L;
 }
@@ -603,8 +711,10 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
         p.X = (ndev::h16 *)(w + L.x);
         p.XT[0] = (ndev::h16 *)(w + L.xt0);
         p.XT[1] = (ndev::h16 *)(w + L.xt1);
+        p.XL = (ndev::h16 *)(w + L.xl);
         p.A = (ndev::h16 *)(w + L.a);
         p.B = (ndev::h16 *)(w + L.b);
+        p.diag = (float2 *)(w + L.diag);
         p.part = (double *)(w + L.part);
         p.rows = mats[i].rows; p.cols = mats[i].cols;
         p.m = (int)L.m; p.n = (int)L.n; p.mp = (int)L.mp; p.np = (int)L.np;
@@ -627,6 +737,7 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
     for (int s = 0; s < steps; s++) {
         a.flip = s & 1;
         a.last = s == steps - 1;
+        a.near = s >= steps - 2;
         launch_product<ndev::GRAM>(gram, a, st);
         launch_product<ndev::POLY>(poly, a, st);
         launch_product<ndev::APPLY>(apply, a, st);

@@ -4,9 +4,12 @@
 //   w_t = sigmoid(k_t)          h_t = h_{t-1} + w_t (v_t - h_{t-1})
 //   s_t = sigmoid(r_t)          y_t = s_t h_t
 //
-// per channel, over packed sequences.  The update is written with w and not
-// with the kept share 1 - w: a gate near 0 (a long memory) keeps its relative
-// accuracy.  All states, gradients and sums are fp32.
+// per channel, over packed sequences.  A step multiplies by the smaller of the
+// two gates, w and the kept share 1 - w = sigmoid(-k), from whichever end it is:
+// h + w (v - h) or v + (1 - w) (h - v).  So a gate near 0 (a long memory) keeps its
+// relative accuracy, and of a gate near 1 neither the little that is kept nor a
+// value much smaller than the state it replaces is lost.  All states, gradients
+// and sums are fp32.
 //
 // A step is an affine map of the state, h -> (1 - w) h + w v, and affine maps
 // compose to affine maps (A, B): h -> A h + B.  So the T tokens (the packed
@@ -121,8 +124,19 @@ __device__ inline void store_f(float *p, const float *f) {
 __device__ inline float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * -1.44269504088896340736f); }
 __device__ inline float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(x)); }
 
-// sigmoid(x) and sigmoid(-x), neither by a difference that would cancel where
-// the gate saturates
+// The smaller of sigmoid(x) and sigmoid(-x), negative (by its sign bit) where
+// that is sigmoid(x): neither is made by a difference, which would cancel where
+// the gate saturates.
+__device__ inline float smaller(float x) {
+    const float e = exp_neg(fabsf(x));
+    return __builtin_copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), x);
+}
+__device__ inline bool is_write(float g) { return __builtin_bit_cast(int, g) < 0; }
+// a step of the state, and the kept share of x, by the smaller gate
+__device__ inline float step(float g, float h, float v) { return fmaf(-g, v - h, is_write(g) ? h : v); }
+__device__ inline float keep(float g, float x) { return fmaf(g, x, is_write(g) ? x : 0.0f); }
+
+// sigmoid(x) and sigmoid(-x)
 __device__ inline void gates(float x, float &on, float &off) {
     const float e = exp_neg(fabsf(x)), i = __builtin_amdgcn_rcpf(1.0f + e), j = e * i;
     on = x < 0.0f ? j : i;
@@ -429,7 +443,7 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         float kf[N];
         E::unpack(k[j], kf);
 #pragma unroll
-        for (int i = 0; i < N; i++) w[j][i] = sigmoid(kf[i]);
+        for (int i = 0; i < N; i++) w[j][i] = smaller(kf[i]);
     }
     float A[N], B[N], h[N];
 #pragma unroll
@@ -441,8 +455,8 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             E::unpack(v[j], vf);
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                A[i] = fmaf(-w[j][i], A[i], A[i]);
-                B[i] = fmaf(w[j][i], vf[i] - B[i], B[i]);
+                A[i] = keep(w[j][i], A[i]);
+                B[i] = step(w[j][i], B[i], vf[i]);
             }
         };
         if (whole) {
@@ -481,7 +495,7 @@ __device__ inline void fwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         E::unpack(r[j], rf);
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            h[i] = fmaf(w[j][i], vf[i] - h[i], h[i]);
+            h[i] = step(w[j][i], h[i], vf[i]);
             o[i] = sigmoid(rf[i]) * h[i];
         }
         store_row<E>(a.Y, t0 + j, a.ldy, lb, o);
@@ -636,7 +650,7 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
 #pragma unroll
             for (int i = 0; i < N; i++) {
                 hb[j][i] = h[i];
-                h[i] = fmaf(sigmoid(kf[i]), vf[i] - h[i], h[i]);
+                h[i] = step(smaller(kf[i]), h[i], vf[i]);
             }
         }
     });
@@ -649,13 +663,13 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
         dy[j].get(d);
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            float w, keep, s, off;
-            gates(kf[i], w, keep);
+            float w, share, s, off;
+            gates(kf[i], w, share);
             gates(rf[i], s, off);
             const float u = d[i] * s, g = u + p[i], x = vf[i] - hb[j][i];
-            dr[i] = u * off * fmaf(w, x, hb[j][i]);
+            dr[i] = u * off * (kf[i] < 0.0f ? fmaf(w, x, hb[j][i]) : fmaf(-share, x, vf[i]));
             dv[i] = g * w;
-            dk[i] = dv[i] * x * keep;
+            dk[i] = dv[i] * x * share;
             p[i] = fmaf(-w, g, g);
         }
         store_row<E>(a.dK, t0 + j, a.ldd, lb, dk);
@@ -718,7 +732,7 @@ __global__ __launch_bounds__(256) void recur_step_kernel(const void *K, const vo
     load_f<N>(h_in + row * C + col, h);
 #pragma unroll
     for (int j = 0; j < N; j++) {
-        h[j] = fmaf(sigmoid(k[j]), v[j] - h[j], h[j]);
+        h[j] = step(smaller(k[j]), h[j], v[j]);
         y[j] = sigmoid(r[j]) * h[j];
     }
     store_f<N>(h_out + row * C + col, h);

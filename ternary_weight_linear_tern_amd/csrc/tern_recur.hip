@@ -24,7 +24,7 @@
 // K, V, R are read once and Y is written once: 32768 x 4096 bf16 in one sequence
 // 289 us, 3.7 TB/s of the 5.1 of a copy (with the pairs, the chain and the
 // output in three launches, which read K and V twice, 345 us); backward, with
-// fp32 dY, 560 us, 3.8 TB/s.  What bounds it is the time a chunk's registers are
+// fp32 dY, 580 us, 3.7 TB/s.  What bounds it is the time a chunk's registers are
 // held: the loads, about 3 us for the words of other chunks, the output.  Short
 // calls (2048 x 512: 12 us) are two launches and one such chunk's time.
 // The pairs in between are applied in order to the state found, the same
@@ -597,9 +597,9 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             dy[j].get(d);
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                const float w = sigmoid(kf[i]), g = fmaf(d[i], sigmoid(rf[i]), B[i]);
-                A[i] = fmaf(-w, A[i], A[i]);
-                B[i] = fmaf(-w, g, g);
+                const float w = smaller(kf[i]), g = fmaf(d[i], sigmoid(rf[i]), B[i]);
+                A[i] = keep(w, A[i]);
+                B[i] = keep(w, g);
             }
         };
         if (whole) {
@@ -670,7 +670,7 @@ __device__ inline void bwd_chunk(const RecurArgs &a, int cb, int col, int wave, 
             dr[i] = u * off * (kf[i] < 0.0f ? fmaf(w, x, hb[j][i]) : fmaf(-share, x, vf[i]));
             dv[i] = g * w;
             dk[i] = dv[i] * x * share;
-            p[i] = fmaf(-w, g, g);
+            p[i] = kf[i] < 0.0f ? fmaf(-w, g, g) : share * g;
         }
         store_row<E>(a.dK, t0 + j, a.ldd, lb, dk);
         store_row<E>(a.dV, t0 + j, a.ldd, lb, dv);
@@ -754,7 +754,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //             unit): 32768 x 4096 289 us; 4 waves 377, 16 waves 385, one channel
 //             309;
 //   backward  4 waves, one channel a lane (135 registers, 12 waves): 32768 x
-//             4096 560 us; 8 waves 686, two channels 714.
+//             4096 580 us (before the gates' exact shares 560; 8 waves 686, two channels 714).
 constexpr int kFwdWaves = 8, kBwdWaves = 4;
 constexpr int kFwdCols = 128, kBwdCols = 64;   // columns of a workgroup, bf16 (fp32: 64)
 struct RecurPlan {

@@ -76,3 +76,15 @@ def test_one_token_through_open_gates(gate, act):
         tl.tern_recur_step(d["K"], d["V"], d["R"], d["h0"], o["Y"], o["hT"])
         torch.cuda.synchronize()
         check(o, want, tol, ("Y", "hT"))
+
+
+@pytest.mark.parametrize("act,dy", ACTS)
+@pytest.mark.parametrize("what", ["late", "reset", "still"])
+@pytest.mark.parametrize("gate", gr.GATES)
+def test_gradients_through_open_gates(gate, what, act, dy):
+    """What is left of a gradient behind open gates: with 'late', tokens that have
+    none of their own receive only that."""
+    for lens in LENS:
+        log(f"recur gradients, gates {gate}, {what}, {act}, dY {dy}, lengths {lens}")
+        _, o, want, tol = run(lens, 136, gate, what, act, dy)
+        check(o, want, tol, gr.NAMES)

@@ -499,7 +499,9 @@ int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int
  *   row of X that holds a non-finite value spoils its own row of Y only.
  * tern_layer_q4_matvec -- the same for 1 to 8 projections that share T and the
  *   types (a layer's receptance, key and value on one token), in one launch.
- *   Inputs may be shared; no output may overlap an input or another output.
+ *   Inputs may be shared; no output may overlap an input or another output.  Each
+ *   Y equals tern_q4_matvec's bit for bit, whatever else the call holds, and a
+ *   token's row does not depend on the other tokens.
  * Errors: NULL, SHAPE, DTYPE, VALUE (group), ALIGN, ALIAS, HIP.
  */
 typedef struct tern_q4_proj {

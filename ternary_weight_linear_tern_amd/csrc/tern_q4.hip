@@ -18,12 +18,15 @@
 // fp32 activations are cut into three bf16 terms of 8 significant bits each,
 // exactly, and multiplied term by term.
 //
-// What bounds it: one bf16 token of 4096 x 16384 takes 10.8 us, 3.3 TB/s of the 5.1 of a
-// copy (about 3 us are the launch's start and the first loads); three 2048 x 2048
-// 5.7 us, two thirds of it that latency.  More tokens read the activations
-// once a column block, through shared memory (16 bf16 tokens 13.5 us); fp32 ones pass
-// it as 12 KiB a block and wave and are cut there, which bounds 13 rows of 16384 x
-// 4096 at 29 us, 1.3 TB/s.
+// What bounds it (times of a call in a recorded chain of eight, each with weights of its
+// own): one bf16 token of 4096 x 16384 takes 13.8 us, 2.7 TB/s of the 5.1 of a copy
+// (about 3 us are the launch's start and the first loads); three 2048 x 2048 6.4 us, two
+// thirds of it that latency.  The rows are split among the waves of one workgroup only,
+// so narrow matrices leave units idle: 8192 x 2048 (128 workgroups for 256 units) takes
+// 7.6 us, 16384 x 512 10.4.  More tokens read the activations once a column block, through
+// shared memory (16 bf16 tokens of 16384 x 4096 17.5 us); fp32 ones pass it as 12 KiB a
+// block and wave and are cut there, in every workgroup anew, which bounds one token of
+// 16384 x 4096 at 19 us and 13 at 27, 1.4 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,7 +47,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kCols = 16, kRows = 128;          // a block of the packed matrix: 1 KiB
 constexpr int kBlockWords = kCols * kRows / 8;
 // waves of a workgroup, at most: 16 where 128 registers a lane are enough; with fp32
-// activations shared memory holds 12 (13 rows of 16384 x 4096: 29 us, 8 waves 32)
+// activations shared memory holds 12
 constexpr int max_waves(int terms, int nb) { return nb == 1 ? (terms == 1 ? 16 : 12) : 8; }
 
 // Word w of lane l of a block: rows 32 w + 8 (l / 16) + e (e < 8), column
@@ -77,12 +80,37 @@ struct Q4One {
     const void *gscale;
     void *Y;
     int in, out, nkb, group_chunks;   // group_chunks: 32-row chunks of a group (1, 2, 4)
+    int runs, per, more;              // runs of row blocks: nkb = runs * per + more
+    int wave_runs;                    // runs a wave takes
+    int inv;                          // 2^16 / runs, rounded up
     int start;                        // first workgroup
+    // of the row blocks that are over, how many runs before run r take one more:
+    // floor(r more / runs), exact for up to 16 runs
+    __device__ int over(int r) const { return (int)((unsigned)(r * more * inv) >> 16); }
 };
 struct Q4Args {
     Q4One p[kMaxGroup];
     int n, T, waves, y_bf16;
+    int rows;                         // tokens of a workgroup, at most 16
 };
+
+// A projection's row blocks are cut into runs.  The sum of a run and the order in
+// which they are added are the projection's alone; which wave takes which runs is
+// the call's.  So the result is the same, bit for bit, whatever else the call holds.
+// Runs: about 4 row blocks each, what a wave needs to hide its loads (one bf16 token
+// of 4096 x 4096 6.3 us, runs of 8 7.9; 2600 x 2600 5.4 and 6.4; 5000 x 5000, with
+// more column blocks than units, 10.7 and 8.5), in fours, so that 4 waves share them
+// evenly, and no more than one a wave of the largest workgroup.  A projection whose
+// columns alone fill the chip (pair() below) needs only 4.  A wave that takes 4 runs
+// spends about 0.2 us on each: the six matrices of d = 2048 14.9 us (split for the
+// whole call, with bits that follow the company, 14.1).
+constexpr int kPairFrom = 1024;   // column blocks
+inline bool pair(int64_t column_blocks) { return column_blocks >= kPairFrom; }
+inline int64_t runs_of(int64_t nkb, int64_t ncb, int terms) {
+    int64_t runs = pair(ncb) || nkb < 16 ? 4 : (nkb + 15) / 16 * 4;
+    if (runs > max_waves(terms, 1)) runs = max_waves(terms, 1);
+    return runs < nkb ? runs : nkb;
+}
 
 __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -171,16 +199,30 @@ struct Scales {
     }
 };
 
-// Blocks k0 .. k1 - 1 of a wave's NB column blocks (GC: 32-row chunks of a scale
-// group).  The weights, which come from HBM, are loaded kAhead blocks ahead, the
+// Blocks k0 .. k1 - 1 of a wave's NB column blocks, whole runs from r0 on, of each of
+// which `done` takes the sums (GC: 32-row chunks of a scale group).  The weights, which come from HBM, are loaded kAhead blocks ahead, the
 // activations and scales, which mostly come from L2, one block ahead.
 constexpr int kAhead = 2;
-template <int TERMS, bool SBF, int NB, int GC>
+template <int TERMS, bool SBF, int NB, int GC, class Done>
 __device__ inline void run_blocks(const Q4One &p, const char *X, int nt, int lane, char *lds, const u32x4 *const (&W)[NB],
-                                  const int (&col)[NB], int k0, int k1, f32x4 (&y)[NB]) {
+                                  const int (&col)[NB], int r0, int k0, int k1, Done done) {
     using Sc = typename Scales<SBF>::Raw;
     const int ng = (p.in + GC * 32 - 1) / (GC * 32), tok = lane & 15, sub = lane >> 4;
     u32x4 w[kAhead][NB];
+    f32x4 y[NB];
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < NB; i++) y[i] = f32x4{0, 0, 0, 0};
+    };
+    clear();
+    // the row blocks left of the run: its share, and one more as the remainders add up
+    int run = r0, rest = r0 * p.more - p.over(r0) * p.runs, left;
+    auto begin = [&] {
+        rest += p.more;
+        left = p.per + (rest >= p.runs);
+        rest -= rest >= p.runs ? p.runs : 0;
+    };
+    begin();
     Rows<TERMS> rows;
     Sc sc[2][4 / GC][NB];
     auto load_w = [&](u32x4 (&o)[NB], int kb) {
@@ -249,19 +291,24 @@ __device__ inline void run_blocks(const Q4One &p, const char *X, int nt, int lan
                 work(w[j], sc[j & 1]);
                 load_w(w[j], kb + j + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
+                if (--left == 0) {
+                    done(run++, y);
+                    clear();
+                    begin();
+                }
             }
         }
     }
 }
 
 // One workgroup: NB column blocks, 16 tokens, all rows, the rows' blocks
-// dealt to the waves in runs; the waves' sums meet in shared memory in the
-// order of the waves.
+// dealt to the waves in runs, whose sums meet in shared memory and are added in
+// their order.
 template <int TERMS, bool SBF, int NB>
 __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];   // lds_bytes()
-    using Red = float[16][NB * kCols + 4];
-    Red *const red = (Red *)(lds + a.waves * Rows<TERMS>::kBytes);
+    constexpr int kLine = NB * kCols + 4;
+    float *const red = (float *)(lds + a.waves * Rows<TERMS>::kBytes);   // [run][token][kLine]
     int pi = 0;
     while (pi + 1 < a.n && (int)blockIdx.x >= a.p[pi + 1].start) pi++;
     const Q4One p = a.p[pi];
@@ -272,32 +319,35 @@ __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a)
     char *xs = lds + wave * Rows<TERMS>::kBytes;
     const int ncb = (p.out + kCols - 1) / kCols;
     const int cb0 = ((int)blockIdx.x - p.start) * NB;
-    const int per = (p.nkb + a.waves - 1) / a.waves;
-    const int k0 = wave * per, k1 = k0 + per < p.nkb ? k0 + per : p.nkb;
+    const int r0 = wave * p.wave_runs, r1 = r0 + p.wave_runs < p.runs ? r0 + p.wave_runs : p.runs;
+    const int k0 = r0 * p.per + p.over(r0), k1 = r1 * p.per + p.over(r1);
 
     const u32x4 *W[NB];
     int col[NB];   // first of the 4 columns a lane accumulates
-    f32x4 y[NB];
 #pragma unroll
     for (int b = 0; b < NB; b++) {
         const int cb = cb0 + b < ncb ? cb0 + b : ncb - 1;
         W[b] = (const u32x4 *)p.packed + ((int64_t)cb * p.nkb) * 64 + lane;
         const int c = cb * kCols + sub * 4;
         col[b] = c < p.out ? c : 0;   // the last block may be half full (out is a multiple of 8)
-        y[b] = f32x4{0, 0, 0, 0};
     }
-    if (k0 < k1) {
-        if (p.group_chunks == 1) run_blocks<TERMS, SBF, NB, 1>(p, X, nt, lane, xs, W, col, k0, k1, y);
-        else if (p.group_chunks == 2) run_blocks<TERMS, SBF, NB, 2>(p, X, nt, lane, xs, W, col, k0, k1, y);
-        else run_blocks<TERMS, SBF, NB, 4>(p, X, nt, lane, xs, W, col, k0, k1, y);
-    }
+    auto done = [&](int run, const f32x4 (&y)[NB]) {
+        float *to = red + (run * a.rows + (lane & 15)) * kLine + sub * 4;
+        if ((lane & 15) < a.rows)
 #pragma unroll
-    for (int b = 0; b < NB; b++) *(f32x4 *)&red[wave][lane & 15][b * kCols + sub * 4] = y[b];
+            for (int b = 0; b < NB; b++) *(f32x4 *)(to + b * kCols) = y[b];
+    };
+    if (r0 < r1) {
+        if (p.group_chunks == 1) run_blocks<TERMS, SBF, NB, 1>(p, X, nt, lane, xs, W, col, r0, k0, k1, done);
+        else if (p.group_chunks == 2) run_blocks<TERMS, SBF, NB, 2>(p, X, nt, lane, xs, W, col, r0, k0, k1, done);
+        else run_blocks<TERMS, SBF, NB, 4>(p, X, nt, lane, xs, W, col, r0, k0, k1, done);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < nt * NB * kCols; i += a.waves * 64) {
         const int t = i / (NB * kCols), c = i % (NB * kCols);
-        float v = red[0][t][c];
-        for (int w = 1; w < a.waves; w++) v += red[w][t][c];
+        const float *from = red + t * kLine + c;
+        float v = p.runs ? *from : 0.0f;
+        for (int r = 1; r < p.runs; r++) v += *(from += a.rows * kLine);
         const int oc = cb0 * kCols + c;
         if (oc < p.out) {
             const int64_t o = (int64_t)(tok0 + t) * p.out + oc;
@@ -308,8 +358,10 @@ __global__ __launch_bounds__(64 * max_waves(TERMS, NB)) void q4_kernel(Q4Args a)
 }
 
 template <int TERMS, int NB>
-int lds_bytes(int waves) {
-    return waves * (Rows<TERMS>::kBytes + 16 * (NB * kCols + 4) * 4);
+int lds_bytes(const Q4Args &a) {
+    int runs = 1;
+    for (int i = 0; i < a.n; i++) runs = std::max(runs, a.p[i].runs);
+    return a.waves * Rows<TERMS>::kBytes + runs * a.rows * (NB * kCols + 4) * 4;
 }
 
 }  // namespace qdev
@@ -329,8 +381,8 @@ bool sizes_ok(int64_t in, int64_t out) {
 
 template <int TERMS, bool SBF>
 void launch_nb(int nb, dim3 g, dim3 b, hipStream_t st, const qdev::Q4Args &a) {
-    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 1>), g, b, (qdev::lds_bytes<TERMS, 1>(a.waves)), st, a);
-    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 2>), g, b, (qdev::lds_bytes<TERMS, 2>(a.waves)), st, a);
+    if (nb == 1) hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 1>), g, b, (qdev::lds_bytes<TERMS, 1>(a)), st, a);
+    else hipLaunchKernelGGL((qdev::q4_kernel<TERMS, SBF, 2>), g, b, (qdev::lds_bytes<TERMS, 2>(a)), st, a);
 }
 
 }  // namespace
@@ -395,25 +447,21 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
     qdev::Q4Args a{};
     // Shape of the launch.  From 1024 column blocks on (4 a compute unit) a
     // wave takes two, which share its activations, and 4 waves share the rows:
-    // 4096 x 16384, one bf16 token 11.6 us against 13.9 with single blocks (8 waves
-    // 13.5, 2 16.9), 16 fp32 tokens 22.4 against 37.1.  Fewer blocks take one
-    // each (4096 x 4096 5.6 us against 7.8 with two, 16384 x 4096 12.4 against
-    // 23.9), and enough waves that each has about 4 row blocks, which is all it
-    // needs to hide its loads (4096 x 4096: 4 row blocks a wave 5.6 us, 8 6.8; three
-    // 2048 x 2048: 4 waves 5.7, 2 7.6).
-    int64_t maxk = 1, ncb = 0;
-    for (int i = 0; i < n; i++) {
-        maxk = projs[i].in > maxk ? projs[i].in : maxk;
-        ncb += cdiv(projs[i].out, qdev::kCols);
-    }
-    const int nb = ncb >= 1024 ? 2 : 1;
-    const int64_t nkb = cdiv(maxk, qdev::kRows);
-    const int64_t most = qdev::max_waves(act_dtype == TERN_F32 ? 3 : 1, nb);
-    int64_t waves = nb == 2 || nkb < 16 ? 4 : nkb / 4;
-    if (waves > most) waves = most;
-    if (waves > nkb) waves = nkb;
-    a.waves = (int)waves;
+    // 4096 x 16384, one bf16 token 13.8 us against 14.7 with single blocks, 16 fp32
+    // tokens 22.5 against 38.4, the six matrices of d = 2048 14.9 against 20.8.  Fewer
+    // blocks take one each (4096 x 4096 6.3 us against 8.4 with two, 16 tokens of
+    // 16384 x 4096 17.5 against 30.5), and as many waves as the longest sums have runs.
+    const int terms = act_dtype == TERN_F32 ? 3 : 1;
+    int64_t ncb = 0, waves = 1;
+    for (int i = 0; i < n; i++) ncb += cdiv(projs[i].out, qdev::kCols);
+    const int nb = qdev::pair(ncb) ? 2 : 1;
+    auto runs_of = [&](const tern_q4_proj_t &p) {
+        return qdev::runs_of(cdiv(p.in, qdev::kRows), cdiv(p.out, qdev::kCols), terms);
+    };
+    for (int i = 0; i < n; i++) waves = std::max(waves, runs_of(projs[i]));
+    a.waves = (int)(nb == 2 ? std::min<int64_t>(waves, 4) : waves);
     a.T = (int)T;
+    a.rows = (int)std::min<int64_t>(T, 16);
     for (int i = 0; i < n; i++) {
         const tern_q4_proj_t &p = projs[i];
         if (p.out == 0) continue;
@@ -421,6 +469,11 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
         o.X = p.X; o.packed = p.packed; o.gscale = p.gscale; o.Y = p.Y;
         o.in = (int)p.in; o.out = (int)p.out; o.nkb = (int)cdiv(p.in, qdev::kRows);
         o.group_chunks = (int)(p.group / 32);
+        o.runs = (int)runs_of(p);
+        o.per = o.runs ? o.nkb / o.runs : 0;
+        o.more = o.runs ? o.nkb % o.runs : 0;
+        o.inv = o.runs ? (65535 + o.runs) / o.runs : 0;
+        o.wave_runs = (int)cdiv(o.runs, a.waves);
     }
     // the longest sums start first (each projection's results are its own)
     std::stable_sort(a.p, a.p + a.n, [](const qdev::Q4One &x, const qdev::Q4One &y) { return x.nkb > y.nkb; });

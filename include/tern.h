@@ -495,7 +495,7 @@ int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int
  *   T          any, 16 rows share one pass over the weights (at most 1048560).
  *   Products of the integer codes with X are exact, sums are fp32, the scale
  *   multiplies each group's sum once; the order of the sums is fixed.  The
- *   sums hold terms up to 31 |X|: a group's must stay within fp32's range.  A
+ *   sums of 32 rows hold terms up to 31 |X|, which must stay within fp32's range.  A
  *   row of X that holds a non-finite value spoils its own row of Y only.
  * tern_layer_q4_matvec -- the same for 1 to 8 projections that share T and the
  *   types (a layer's receptance, key and value on one token), in one launch.

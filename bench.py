@@ -250,7 +250,8 @@ def layer_operators(w, projs, timed):
     q4 = []
     for p in projs:
         pk = tl.empty_q4_packed(p["n_in"], p["n_out"])
-        tl.tern_q4_pack(p["q"], pk)
+        # the projection as it is served: its ternary matrix, its scale in every group
+        tl.tern_q4_pack((p["q"].sign() * (p["q"].abs() >= p["theta"])).to(torch.int8), pk)
         q4.append(dict(n_in=p["n_in"], n_out=p["n_out"], group=128, packed=pk, X=p["X"][:1],
                        gscale=p["scale"].expand(-(-p["n_in"] // 128), -1).contiguous(),
                        Y=torch.empty((1, p["n_out"]), **bf)))

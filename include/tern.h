@@ -17,7 +17,7 @@
  * Around the projections stand the operators that a layer of them needs besides
  * (their own formulas, further below): the gated linear recurrence between the
  * receptance / key / value projections and the output projection
- * (tern_recur_*), products of a few rows with 4-bit weights for serving
+ * (tern_recur_*), products of a few rows with 4-bit weights
  * (tern_q4_*), and the orthogonalisation of an update (tern_orthogonalize).
  *
  * Conventions for every entry point:
@@ -474,11 +474,13 @@ int tern_recur_step(const void *K, const void *V, const void *R, int64_t ld, int
                     void *stream);
 
 /*
- * Products of a few rows with 4-bit weights and group scales: the form in
- * which a layer's matrices are served, one or a few tokens at a time.  The
- * codes are those of the SR4 accumulator (q clamped to +-7 fits), with one
- * scale per `group` consecutive input rows and output column:
+ * Products of a few rows with 4-bit weights and group scales, one or a few tokens
+ * at a time, with one scale per `group` consecutive input rows and output column:
  *   Y[t, c] = sum_r X[t, r] q[r, c] gscale[r / group, c].
+ * To serve a ternary projection, pack its ternary matrix (-1, 0 and 1 by the
+ * dead-zone rule) with the projection's scale in every row of gscale: Y is then
+ * tern_linear_fwd's, to the rounding of the sums.  Packing the accumulator itself
+ * gives X (q scale), which is not what the projection computes.
  *
  * tern_q4_packed_bytes -- bytes of the packed handle of an [in, out] matrix
  *   (-1 for sizes that are negative, too large or no multiples of 8).

@@ -717,7 +717,8 @@ def empty_q4_packed(n_in: int, n_out: int, device="cuda") -> torch.Tensor:
 
 
 def tern_q4_pack(q: torch.Tensor, packed: torch.Tensor, stream=None) -> None:
-    """q int8 [in, out] (clamped to [-8, 7]) -> 4-bit handle (see empty_q4_packed)."""
+    """q int8 [in, out] (clamped to [-8, 7]) -> 4-bit handle (see empty_q4_packed).
+    For a ternary projection q is its ternary matrix (-1, 0, 1), not the accumulator."""
     fn = "tern_q4_pack"
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise ValueError(f"{fn}: q must be a tensor [in, out]")

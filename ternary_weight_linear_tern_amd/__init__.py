@@ -540,8 +540,17 @@ def _shaped(fn, name, t, shape, dtypes) -> None:
         _need(fn, name, t, shape, dtypes)
 
 
+def _tensors(fn, **ts) -> None:
+    """Words the error for an argument that is no tensor."""
+    for name, t in ts.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a tensor")
+
+
 def _device_of(fn, t0, *ts) -> int:
     """Index of the one GPU every tensor (None: not given) lives on."""
+    if not all(t is None or isinstance(t, torch.Tensor) for t in ts):
+        raise TypeError(f"{fn}: an array must be a tensor or None")
     d = t0.get_device()
     for t in ts:
         if t is not None and t.get_device() != d:
@@ -603,7 +612,8 @@ def _recur_inputs(fn, K, V, R):
     shape, dt = K.shape, K.dtype
     if len(shape) != 2:
         raise ValueError(f"{fn}: K must be [T, C]")
-    if dt not in _ACT or V.shape != shape or R.shape != shape or V.dtype is not dt or R.dtype is not dt:
+    if not isinstance(V, torch.Tensor) or not isinstance(R, torch.Tensor) or dt not in _ACT or V.shape != shape \
+            or R.shape != shape or V.dtype is not dt or R.dtype is not dt:
         _need(fn, "K", K, shape, _ACT)
         _need(fn, "V", V, shape, (dt,))
         _need(fn, "R", R, shape, (dt,))
@@ -677,6 +687,8 @@ def tern_recur_step(K, V, R, h, Y, h_out=None, stream=None) -> None:
     if h_out is None:
         h_out = h
     dt, f32 = K.dtype, torch.float32
+    if not (isinstance(h, torch.Tensor) and isinstance(h_out, torch.Tensor) and isinstance(Y, torch.Tensor)):
+        _tensors(fn, h=h, h_out=h_out, Y=Y)
     if h.shape != shape or h.dtype is not f32 or h_out.shape != shape or h_out.dtype is not f32 \
             or Y.shape != shape or Y.dtype is not dt:
         _need(fn, "h", h, shape, _F32)
@@ -740,6 +752,8 @@ def tern_q4_matvec(X, packed, gscale, group: int, Y, stream=None) -> None:
     """Y [T, out] = X [T, in] . (q * scale of the group), with q as packed by
     tern_q4_pack and gscale [ceil(in / group), out] (fp32 or bf16)."""
     fn = "tern_q4_matvec"
+    if not isinstance(X, torch.Tensor) or not isinstance(Y, torch.Tensor):
+        _tensors(fn, X=X, Y=Y)
     if X.dim() != 2 or Y.dim() != 2:
         raise ValueError(f"{fn}: X must be [T, in] and Y [T, out]")
     T, n_in = X.shape
@@ -764,6 +778,11 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
         raise ValueError(f"{fn}: 1 to 8 projections, got {n}")
     first = projs[0]
     X0, s0, Y0 = first["X"], first["gscale"], first["Y"]
+    tensor = torch.Tensor
+    if not (isinstance(X0, tensor) and isinstance(s0, tensor) and isinstance(Y0, tensor)):
+        _tensors(fn, X=X0, gscale=s0, Y=Y0)
+    if X0.dim() != 2:
+        raise ValueError(f"{fn}: X must be [T, in]")
     T = X0.shape[0]
     act, sdt, ydt = X0.dtype, s0.dtype, Y0.dtype
     if act not in _ACT or sdt not in _ACT or ydt not in (torch.float32, act):
@@ -774,6 +793,8 @@ def tern_layer_q4_matvec(projs, stream=None) -> None:
     for d in projs:
         n_in, n_out, group = d["n_in"], d["n_out"], d["group"]
         X, s, Y, pk = d["X"], d["gscale"], d["Y"], d["packed"]
+        if not (isinstance(X, tensor) and isinstance(s, tensor) and isinstance(Y, tensor) and isinstance(pk, tensor)):
+            _tensors(fn, X=X, gscale=s, Y=Y, packed=pk)
         if X.shape != (T, n_in) or X.dtype is not act:
             _need(fn, "X", X, (T, n_in), (act,))
         groups = -(-n_in // group) if group > 0 else 0
@@ -820,7 +841,21 @@ def empty_ortho_workspace(shapes, device="cuda") -> torch.Tensor:
 
 def tern_orthogonalize(G, O, workspace, steps: int = 5, gain: float = 1.0, stream=None) -> None:
     """O (bf16) = gain * the Newton-Schulz orthogonalisation of G (fp32 or bf16)."""
-    tern_layer_orthogonalize([dict(G=G, O=O, gain=gain)], workspace, steps, stream)
+    fn = "tern_orthogonalize"
+    g, o = _ortho_matrix(fn, G, O, _ACT)
+    rows, cols = G.shape
+    dev = _device_of(fn, G, O, workspace)
+    _call(fn, dev, stream, g, _act_code(G), rows, cols, int(steps), float(gain), o, _addr(workspace),
+          _bytes_of(workspace))
+
+
+def _ortho_matrix(fn, G, O, dtypes):
+    """Addresses of a matrix and of its result."""
+    if not isinstance(G, torch.Tensor) or G.dim() != 2:
+        raise ValueError(f"{fn}: G must be a tensor [rows, cols]")
+    _shaped(fn, "G", G, G.shape, dtypes)
+    _shaped(fn, "O", O, G.shape, (torch.bfloat16,))
+    return _addr(G), _addr(O)
 
 
 def tern_layer_orthogonalize(mats, workspace, steps: int = 5, stream=None) -> None:
@@ -835,12 +870,9 @@ def tern_layer_orthogonalize(mats, workspace, steps: int = 5, stream=None) -> No
     used = []
     for a, d in zip(arr, mats):
         G, O = d["G"], d["O"]
-        if not isinstance(G, torch.Tensor) or G.dim() != 2:
-            raise ValueError(f"{fn}: G must be a tensor [rows, cols]")
-        _shaped(fn, "G", G, G.shape, _ACT if G is G0 else (G0.dtype,))
-        _shaped(fn, "O", O, G.shape, (torch.bfloat16,))
+        a.G, a.O = _ortho_matrix(fn, G, O, _ACT if G is G0 else (G0.dtype,))
         a.rows, a.cols = G.shape
-        a.G, a.O, a.gain = _addr(G), _addr(O), float(d.get("gain", 1.0))
+        a.gain = float(d.get("gain", 1.0))
         used += (G, O)
     dev = _device_of(fn, *used, workspace)
     _call(fn, dev, stream, arr, n, _act_code(G0), int(steps), _addr(workspace), _bytes_of(workspace))

@@ -544,7 +544,9 @@ int tern_layer_q4_matvec(const tern_q4_proj_t *projs, int32_t n, int64_t T, int3
  * to 0.001 of |O|_F for flat, decaying and low-rank spectra alike; more steps
  * add to it, for a flat spectrum (0.002 at eight) and where a direction in which
  * G has nothing has grown out of the roundings, as it does in fp32 (0.001 at
- * eight, 0.1 at twelve for rank one).  The order of every sum is fixed.  A
+ * eight, 0.1 at twelve for rank one).  Elements of X below 2^-49 are lost: a G
+ * with |G|_F below 1e-16, which the 1e-7 leaves next to nothing of, comes out
+ * inexact, and from some 1e-20 on as zeros.  The order of every sum is fixed.  A
  * non-finite G gives an unspecified O.
  * Calls that may run at the same time need a workspace each.
  *

@@ -90,3 +90,12 @@ def test_layer_of_mixed_spectra():
         e = float((m["O"].double() - E).norm() / E.norm())
         log(f"  {l}: {e:.5f}")
         assert e <= 2.0 ** -8, (l, e)
+
+
+@pytest.mark.parametrize("norm", [1e-13, 1e-10, 1e-7, 1e-3, 1e30, 1e38])
+def test_norms_far_from_one(norm):
+    """The 1e-7 beside |G|_F makes X small as G is; large norms are taken out before
+    X is rounded."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    G = torch.randn(264, 520, generator=g, device="cuda", dtype=torch.float64)
+    check((G * (norm / G.norm())).float(), 5, f"norm {norm}")

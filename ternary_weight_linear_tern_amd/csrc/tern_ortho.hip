@@ -212,8 +212,8 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoArgs a) {
 //
 // What bounds it.  4096 x 16384: A 290 us, its polynomial 84, B X 577, five steps
 // 4.9 ms.  B X runs at 0.95 PFLOP/s (the vendor's plain product of that size 1.2):
-// the board is at its power cap, and between the tiles the matrix cores wait for
-// about 15 us while 256 KiB of the old X are read and 384 KiB of the new one written
+// the board is at its power cap (with zeros in all operands it takes 485 us), and
+// between the tiles the matrix cores wait for about 15 us while 256 KiB of the old X are read and 384 KiB of the new one written
 // (128 KiB each are the low term's, which costs 40 us of the 577).  Small matrices
 // (six of 512 x 512 to 512 x 2048, 169 us) are fifteen products of 5 to 15 us each, of
 // which the launch, the first loads and the results are 4 to 5.

@@ -31,12 +31,37 @@ struct Cursor {
         }
         cur = lo;
     }
-    // to a later / an earlier token
+    // To a later / an earlier token: one sequence on, and from there in steps that
+    // double while they fall short and then halve.  A run of empty sequences takes
+    // reads as its logarithm; one by one, a wave that crosses millions would be
+    // waited for longer than the others wait.
     TERN_HD void forth(int64_t t) {
-        while (cur < S && at(cur + 1) <= t) cur++;
+        if (cur >= S || at(cur + 1) > t) return;
+        cur++;
+        bool up = true;
+        for (int64_t d = 1; d;) {
+            if (d <= S - cur && at(cur + d) <= t) {
+                cur += d;
+                d = up ? 2 * d : d >> 1;
+            } else {
+                up = false;
+                d >>= 1;
+            }
+        }
     }
     TERN_HD void back(int64_t t) {
-        while (cur >= 0 && at(cur) > t) cur--;
+        if (cur < 0 || at(cur) <= t) return;
+        cur--;
+        bool up = true;
+        for (int64_t d = 1; d;) {
+            if (d <= cur + 1 && at(cur - d + 1) > t) {
+                cur -= d;
+                d = up ? 2 * d : d >> 1;
+            } else {
+                up = false;
+                d >>= 1;
+            }
+        }
     }
 };
 

@@ -426,7 +426,9 @@ int tern_layer_bwd_dw(const tern_proj_t *projs, int32_t n, int64_t T, int32_t ac
  *   every pointer 16-byte aligned (offsets: 8-byte).  Outputs may be column
  *   slices of one matrix, but share no element with an input or another
  *   output (TERN_ERR_ALIAS).
- * All states, gradients and sums are fp32; Y, dK, dV and dR are rounded once
+ * All states, gradients and sums are fp32; a step multiplies by the smaller of
+ * w_t and 1 - w_t = sigmoid(-K_t), so that neither a gate that is nearly shut nor one
+ * that is nearly open loses what it lets through.  Y, dK, dV and dR are rounded once
  * (nearest even) to act_dtype.  The order of every sum is fixed: repeated
  * calls are bitwise identical.  A NaN or an infinity goes on to its
  * sequence's end as the formulas carry it, and never reaches another.

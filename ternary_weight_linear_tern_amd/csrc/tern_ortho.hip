@@ -615,7 +615,7 @@ constexpr Shape kShapes[] = {{128, 1, 14.0, 0.44, 1.10}, {96, 1, 9.0, 0.32, 0.65
 // single and of six matrices, 128 x 8192 to 4096 x 16384, the choice is within
 // 0.9 % of the best shape in the mean and 3 % but for four, all of the last product,
 // whose low term the figures do not know: 1000 x 12000 takes 60 us where 256 x 256
-// tiles take 52.  Without the last round 2048 x 2048 took the smallest tiles, 24 us
+// tiles take 52.  With full rounds only, 2048 x 2048 took the smallest tiles, 24 us
 // against 18.)
 int choose_shape(int mode, const OrthoArgs &a) {
     int best = 0;

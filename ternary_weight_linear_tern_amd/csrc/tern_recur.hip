@@ -22,7 +22,7 @@
 //   - it publishes its own closing state, and every wave walks its rows again
 //     in registers, from the state that enters them, and writes Y.
 // K, V, R are read once and Y is written once: 32768 x 4096 bf16 in one sequence
-// 305 us, 3.5 TB/s of the 5.1 of a copy; backward, with fp32 dY, 580 us, 3.7 TB/s.
+// 305 us, 3.5 TB/s of the 5.1 of a copy; backward, with fp32 dY, 590 us, 3.6 TB/s.
 // (With w as every step's factor, which loses what an open gate keeps, 289 and 560;
 // so, with the pairs, the chain and the output in three launches, which read K and V
 // twice, the forward took 345.)  What bounds it is the time a chunk's registers are
@@ -753,7 +753,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // chunks the chain passes through:
 //   forward   8 waves, two channels a lane (118 registers, 16 waves a compute
 //             unit): 32768 x 4096 305 us;
-//   backward  4 waves, one channel a lane (135 registers, 12 waves): 580 us.
+//   backward  4 waves, one channel a lane (135 registers, 12 waves): 590 us.
 // With w as every step's factor these were 289 and 560, and the others: forward with 4
 // waves 377, 16 waves 385, one channel 309; backward with 8 waves 686, two channels 714.
 // All are of this one size: smaller calls (2048 x 512: 64 workgroups for 256 units) take

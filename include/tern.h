@@ -18,12 +18,15 @@
  * (their own formulas, further below): the gated linear recurrence between the
  * receptance / key / value projections and the output projection
  * (tern_recur_*), products of a few rows with 4-bit weights
- * (tern_q4_*), and the orthogonalisation of an update (tern_orthogonalize).
+ * (tern_q4_*), and the orthogonalisation of an update (tern_orthogonalize); in
+ * front of them the layer norm (tern_norm_*), and behind the head's logits the log
+ * probabilities of tokens (tern_logprob) and the distillation loss (tern_distill).
  *
  * Conventions for every entry point:
  *   - All array pointers are DEVICE pointers owned by the caller: contiguous
- *     (tern_recur_*: contiguous rows), row-major, 16-byte aligned.  The library allocates nothing, frees
- *     nothing, keeps no state between calls and never synchronises.
+ *     (tern_recur_*, tern_norm_*, tern_logprob, tern_distill: contiguous rows), row-major, 16-byte
+ *     aligned where nothing else is said.  The library allocates nothing, frees nothing,
+ *     keeps no state between calls and never synchronises.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).  All
  *     work is enqueued on it in order; results are ready when the caller's
  *     next synchronisation on that stream returns.
@@ -64,7 +67,8 @@ extern "C" {
 #define TERN_ERR_ALIAS     -7  /* an output overlaps an input or another output */
 #define TERN_ERR_HIP       -8  /* the HIP runtime refused a launch */
 #define TERN_ERR_VALUE     -9  /* a scalar argument outside its range (optimizer step, learning rate,
-                                * group of 4-bit scales, Newton-Schulz steps) */
+                                * group of 4-bit scales, Newton-Schulz steps, eps, temperature,
+                                * number of alternatives) */
 #define TERN_ERR_SCRATCH  -10  /* the sizes need more than the library's static scratch */
 
 /* Number of uint32 words of a packed ternary handle for an [in, out] matrix
@@ -568,6 +572,128 @@ int tern_orthogonalize(const void *G, int32_t g_dtype, int64_t rows, int64_t col
 size_t tern_layer_orthogonalize_workspace_bytes(const tern_ortho_t *mats, int32_t n);
 int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtype, int32_t steps,
                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm of the rows of [T, C], with the residual add that stands in front of
+ * it in a layer:
+ *   S = X + A,   mu = mean_c S,   r = 1 / sqrt(mean_c (S - mu)^2 + eps),
+ *   Y = (S - mu) r w + b.
+ * T, C >= 0; C and every row stride multiples of 8, strides >= C.  Row strides
+ * are in elements; any of the matrices may be a column slice of a wider one.
+ *
+ * tern_norm_fwd
+ *   X        [T, C] of x_dtype (TERN_F32 or TERN_BF16), row stride ldx.
+ *   A, S     A [T, C] of a_dtype (either type), stride lda, is added to X;
+ *            S [T, C] of x_dtype, stride lds, receives the sum, rounded once, and
+ *            the norm is that of S as stored, so that the backward, which reads S,
+ *            sees the same numbers.  S may be X (the stream is then updated in
+ *            place).  Both NULL: the norm of X.
+ *   w, b     fp32 [C], or NULL (ones, zeros).
+ *   eps      above 0 and finite (TERN_ERR_VALUE).
+ *   Y        [T, C] of y_dtype (either type), stride ldy, rounded once.
+ *   stats    fp32 [T, 2], 8-byte aligned: mu and r of each row, which the backward
+ *            reads; or NULL.
+ *
+ * tern_norm_bwd -- from dY, with xh = (S - mu) r and g = dY w:
+ *   dX = dS + r (g - mean_c g - xh mean_c (g xh)),
+ *   dw[c] = sum_t dY xh,   db[c] = sum_t dY.
+ *   S        what the forward normed (its S, or its X where it had no A), of
+ *            s_dtype; stats as the forward wrote them; w as given to it.
+ *   dY       [T, C] of dy_dtype (either type), stride lddy.
+ *   dS       [T, C] of dx_dtype, stride ldds: the gradient that reaches S besides
+ *            the norm (that of the residual stream); or NULL (zeros).
+ *   dX       [T, C] of dx_dtype (TERN_F32, or TERN_BF16 where S is bf16), stride
+ *            lddx, rounded once: the gradient of S, that is of X and of A alike.
+ *            dX may be dS (updated in place).
+ *   dw, db   fp32 [C], each may be NULL.
+ *   workspace  at least tern_norm_bwd_workspace_bytes(T, C) bytes where dw or db is
+ *            asked for.  Calls that may run at the same time need one each.
+ * Statistics and sums are fp32 (mu first, then the squares of the differences);
+ * the order of every sum is fixed: repeated calls are bitwise identical.  A row
+ * with a non-finite value spoils its own rows of the outputs, and its columns of dw, db.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
+ */
+size_t tern_norm_bwd_workspace_bytes(int64_t T, int64_t C);
+int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, int64_t lda,
+                  int32_t a_dtype, const float *w, const float *b, float eps, int64_t T, int64_t C,
+                  void *S, int64_t lds, void *Y, int64_t ldy, int32_t y_dtype, float *stats,
+                  void *stream);
+int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stats, const float *w,
+                  const void *dY, int64_t lddy, int32_t dy_dtype, const void *dS, int64_t ldds,
+                  int64_t T, int64_t C, void *dX, int64_t lddx, int32_t dx_dtype, float *dw,
+                  float *db, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * What a row of the head's logits says of tokens: with z = scale Z,
+ *   lse = log sum_v exp z_v,   logp = z[token] - lse,
+ *   entropy = -sum_v p_v log p_v  (p = exp(z - lse); a p of 0 adds nothing),
+ *   and the k most probable tokens, with their log probabilities.
+ * The log probabilities of given tokens (bits per byte, top-1), a generation loop's
+ * alternatives, and, with scale = 1 / tau, what a teacher hands to tern_distill.
+ *
+ *   Z        [T, V] of z_dtype (TERN_F32 or TERN_BF16), row stride ld (elements, a
+ *            multiple of 8, >= V).  V from 1 to 2^20, any number.  T >= 0.
+ *   scale    1 / temperature, above 0 and finite (TERN_ERR_VALUE).
+ *   tokens   int64 [T]; logp[t] is 0 for a token outside [0, V) (padding).  tokens
+ *            and logp are both given or both NULL.
+ *   entropy, lse   fp32 [T], or NULL.
+ *   k        0 to 64 and not above V (TERN_ERR_VALUE).
+ *   top_ids, top_logp   int64 and fp32 [T, k], by falling Z, ties by rising index (NULL
+ *            where k is 0).
+ *   workspace  at least tern_logprob_workspace_bytes(T, V, k) bytes (NULL when that is
+ *            0).  Calls that may run at the same time need one each.
+ * Int64 arrays are 8-byte aligned, fp32 arrays of this call and of tern_distill 4-byte.
+ * A logit of -inf is a token that is not allowed: p = 0, log p = -inf.  In a row
+ * where nothing is allowed lse and every log probability are -inf, the entropy 0.
+ * A row that holds a NaN or +inf gets NaN, and top_ids in [0, V); other rows are
+ * not touched by it.  Sums are fp32 in a fixed order: repeated calls are bitwise identical.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
+ */
+#define TERN_TOP_MAX 64
+size_t tern_logprob_workspace_bytes(int64_t T, int64_t V, int32_t k);
+int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_t T, int64_t V,
+                 const int64_t *tokens, float *logp, float *entropy, float *lse, int32_t k,
+                 int64_t *top_ids, float *top_logp, void *workspace, size_t workspace_bytes,
+                 void *stream);
+
+/*
+ * Distillation from a teacher's most probable tokens, mixed with the cross entropy
+ * of given targets (page "heal_gpu.rs": alpha CE + (1 - alpha) KL against the
+ * teacher's top k).  Per row of the student's logits Z,
+ *   p_j = exp(teacher_logp_j) / sum_i exp(teacher_logp_i)   over the teacher's entries,
+ *   q = softmax(Z / tau),   KL = sum_j p_j (log p_j - log q[id_j]),
+ *   CE = -log softmax(Z)[target],
+ *   loss = alpha CE + (1 - alpha) tau^2 KL,
+ *   dZ = dloss (alpha (softmax(Z) - 1_target) + (1 - alpha) tau (q - p)).
+ * Loss and gradient come from one call that reads Z once where a row fits a
+ * workgroup; a caller that knows dloss only later calls twice.
+ *
+ *   Z, ld, z_dtype, T, V  as for tern_logprob.
+ *   targets  int64 [T], or NULL: a target outside [0, V), as NULL, has no CE (0, and no
+ *            gradient; the KL keeps its factor).
+ *   K, teacher_ids, teacher_logp   0 to 64 entries (TERN_ERR_VALUE) a row: int64 and fp32
+ *            [T, K], as tern_logprob with scale = 1 / tau writes them.  Entries with an
+ *            id outside [0, V) or a logp of -inf are none; a token that is named twice
+ *            has the sum of both.  A row without entries has no KL.
+ *   alpha    0 to 1 (a part whose factor is 0 is left out, whatever it would be);
+ *   tau      above 0 and finite (TERN_ERR_VALUE).
+ *   loss     fp32 [T], or NULL.
+ *   dloss    fp32 [T], the gradient that reaches loss, or NULL (ones).  Where it is
+ *            0, as where neither part exists, the row of dZ is 0 whatever Z holds.
+ *   dZ       [T, V] of z_dtype, row stride lddz, rounded once; may be Z (then with
+ *            lddz = ld); or NULL.  Columns from V on are left as they are.
+ *   workspace  at least tern_distill_workspace_bytes(T, V) bytes (NULL when that is 0).
+ *            Calls that may run at the same time need one each.
+ * A logit of -inf has q = 0; a teacher's token with q = 0 makes the loss +inf.  A row
+ * of nothing but -inf has q = 0 everywhere.  A row that holds a NaN or +inf gets NaN.
+ * Sums are fp32 in a fixed order: repeated calls are bitwise identical.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
+ */
+size_t tern_distill_workspace_bytes(int64_t T, int64_t V);
+int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t V,
+                 const int64_t *targets, int32_t K, const int64_t *teacher_ids,
+                 const float *teacher_logp, float alpha, float tau, const float *dloss, float *loss,
+                 void *dZ, int64_t lddz, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Graphs of library calls.  The page's trainer launches every glue kernel and

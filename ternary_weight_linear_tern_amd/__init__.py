@@ -73,6 +73,17 @@ SIGNATURES = {
     "tern_orthogonalize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, ctypes.c_float, _vp, _vp, _sz, _vp]),
     "tern_layer_orthogonalize_workspace_bytes": (_sz, [_vp, _i32]),
     "tern_layer_orthogonalize": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "tern_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "tern_norm_fwd": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _i64, _i64, _vp, _i64,
+                                     _vp, _i64, _i32, _vp, _vp]),
+    "tern_norm_bwd": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _i32,
+                                     _vp, _vp, _vp, _sz, _vp]),
+    "tern_logprob_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "tern_logprob": (ctypes.c_int, [_vp, _i64, _i32, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "tern_distill_workspace_bytes": (_sz, [_i64, _i64]),
+    "tern_distill": (ctypes.c_int, [_vp, _i64, _i32, _i64, _i64, _vp, _i32, _vp, _vp, ctypes.c_float, ctypes.c_float,
+                                    _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "tern_graph_begin": (ctypes.c_int, [_vp]),
     "tern_graph_end": (ctypes.c_int, [_vp, ctypes.POINTER(_vp)]),
     "tern_graph_launch": (ctypes.c_int, [_vp, _vp]),
@@ -142,6 +153,7 @@ def _check(fn: str, rc: int):
 
 _F32 = (torch.float32,)
 _ACT = (torch.bfloat16, torch.float32)
+_I64 = (torch.int64,)
 
 
 def _need(fn: str, name: str, t, shape, dtypes) -> None:
@@ -876,6 +888,153 @@ def tern_layer_orthogonalize(mats, workspace, steps: int = 5, stream=None) -> No
         used += (G, O)
     dev = _device_of(fn, *used, workspace)
     _call(fn, dev, stream, arr, n, _act_code(G0), int(steps), _addr(workspace), _bytes_of(workspace))
+
+
+def tern_norm_bwd_workspace_bytes(T: int, C: int) -> int:
+    return int(lib().tern_norm_bwd_workspace_bytes(int(T), int(C)))
+
+
+def empty_norm_stats(T: int, device="cuda") -> torch.Tensor:
+    """Row statistics of tern_norm_fwd for tern_norm_bwd: mean and 1 / deviation."""
+    return torch.empty((T, 2), dtype=torch.float32, device=device)
+
+
+def empty_norm_workspace(T: int, C: int, device="cuda") -> torch.Tensor:
+    """Workspace of tern_norm_bwd where it computes dw or db."""
+    return torch.empty((max(tern_norm_bwd_workspace_bytes(T, C), 16),), dtype=torch.uint8, device=device)
+
+
+def _matrix(fn, name, t, shape, dtypes) -> tuple:
+    """Address, row stride and type code of a matrix whose rows are contiguous."""
+    _shaped(fn, name, t, shape, dtypes)
+    # (the stride of rows without elements means nothing)
+    return t.data_ptr(), _row_stride(fn, name, t) if shape[1] else 0, TERN_BF16 if t.dtype is torch.bfloat16 else TERN_F32
+
+
+def _vector(fn, name, t, shape, dtypes=_F32):
+    """Address of a contiguous array (None: not given)."""
+    if t is None:
+        return None
+    _shaped(fn, name, t, shape, dtypes)
+    return _addr(t)
+
+
+def _rows_of(fn, name, t) -> tuple:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{fn}: {name} must have two dimensions")
+    return t.shape
+
+
+def tern_norm_fwd(X, Y, w=None, b=None, A=None, S=None, stats=None, eps: float = 1e-5, stream=None) -> None:
+    """Y = layer norm of S = X + A (of X without A), times w, plus b.  S, given
+    with A, receives the sum (it may be X: in place); stats [T, 2] the rows'
+    mean and 1 / deviation for tern_norm_bwd."""
+    fn = "tern_norm_fwd"
+    shape = T, C = _rows_of(fn, "X", X)
+    x, ldx, xd = _matrix(fn, "X", X, shape, _ACT)
+    y, ldy, yd = _matrix(fn, "Y", Y, shape, _ACT)
+    a, lda, ad, s, lds = None, 0, 0, None, 0
+    if A is not None or S is not None:
+        if A is None or S is None:
+            raise ValueError(f"{fn}: A and S are given together")
+        a, lda, ad = _matrix(fn, "A", A, shape, _ACT)
+        s, lds, _ = _matrix(fn, "S", S, shape, (X.dtype,))
+    wp, bp = _vector(fn, "w", w, (C,)), _vector(fn, "b", b, (C,))
+    st = _vector(fn, "stats", stats, (T, 2))
+    dev = _device_of(fn, X, Y, w, b, A, S, stats)
+    _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, float(eps), T, C, s, lds, y, ldy, yd, st)
+
+
+def tern_norm_bwd(S, stats, dY, dX, workspace=None, w=None, dS=None, dw=None, db=None, stream=None) -> None:
+    """Gradients of tern_norm_fwd: dX (= the gradient of X and of A) from dY and
+    dS, the gradient that reaches S besides the norm (None: zeros; dX may be dS);
+    dw and db [C] where given, which need the workspace (empty_norm_workspace)."""
+    fn = "tern_norm_bwd"
+    shape = T, C = _rows_of(fn, "S", S)
+    s, lds, sd = _matrix(fn, "S", S, shape, _ACT)
+    dy, lddy, dyd = _matrix(fn, "dY", dY, shape, _ACT)
+    dx, lddx, dxd = _matrix(fn, "dX", dX, shape, (torch.float32, S.dtype))
+    ds, ldds = None, 0
+    if dS is not None:
+        ds, ldds, _ = _matrix(fn, "dS", dS, shape, (dX.dtype,))
+    _shaped(fn, "stats", stats, (T, 2), _F32)
+    args = (s, lds, sd, _addr(stats), _vector(fn, "w", w, (C,)), dy, lddy, dyd, ds, ldds, T, C, dx, lddx, dxd,
+            _vector(fn, "dw", dw, (C,)), _vector(fn, "db", db, (C,)))
+    dev = _device_of(fn, S, stats, dY, dX, workspace, w, dS, dw, db)
+    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
+
+
+def tern_logprob_workspace_bytes(T: int, V: int, k: int = 0) -> int:
+    return int(lib().tern_logprob_workspace_bytes(int(T), int(V), int(k)))
+
+
+def empty_logprob_workspace(T: int, V: int, k: int = 0, device="cuda") -> torch.Tensor:
+    """Workspace of tern_logprob, either type of logits."""
+    return torch.empty((max(tern_logprob_workspace_bytes(T, V, k), 16),), dtype=torch.uint8, device=device)
+
+
+def _logits(fn, name, t, shape, dtypes) -> tuple:
+    """As _matrix, for rows of any length: what a single row's stride would be."""
+    p, ld, dt = _matrix(fn, name, t, shape, dtypes)
+    return p, (ld if shape[0] > 1 else -(-shape[1] // 8) * 8), dt
+
+
+def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None,
+                 scale: float = 1.0, stream=None) -> None:
+    """Of each row of logits Z [T, V], times scale: logp [T] of the given tokens
+    (int64 [T]; 0 for one outside [0, V)), the entropy [T], the log-sum-exp lse
+    [T], and the k most probable tokens, top_ids (int64) and top_logp [T, k], ties
+    by rising index.  Rows start on 16 bytes: for a V that is no multiple of 8,
+    Z is a column slice of a wider matrix."""
+    fn = "tern_logprob"
+    shape = T, V = _rows_of(fn, "Z", Z)
+    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT)
+    k = 0
+    if top_ids is not None or top_logp is not None:
+        if top_ids is None or top_logp is None:
+            raise ValueError(f"{fn}: top_ids and top_logp are given together")
+        k = _rows_of(fn, "top_ids", top_ids)[1]
+    args = (z, ld, zd, float(scale), T, V, _vector(fn, "tokens", tokens, (T,), _I64), _vector(fn, "logp", logp, (T,)),
+            _vector(fn, "entropy", entropy, (T,)), _vector(fn, "lse", lse, (T,)), k,
+            _vector(fn, "top_ids", top_ids, (T, k), _I64), _vector(fn, "top_logp", top_logp, (T, k)))
+    dev = _device_of(fn, Z, workspace, tokens, logp, entropy, lse, top_ids, top_logp)
+    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
+
+
+def tern_distill_workspace_bytes(T: int, V: int) -> int:
+    return int(lib().tern_distill_workspace_bytes(int(T), int(V)))
+
+
+def empty_distill_workspace(T: int, V: int, device="cuda") -> torch.Tensor:
+    """Workspace of tern_distill, either type of logits."""
+    return torch.empty((max(tern_distill_workspace_bytes(T, V), 16),), dtype=torch.uint8, device=device)
+
+
+def tern_distill(Z, workspace=None, targets=None, teacher_ids=None, teacher_logp=None, alpha: float = 0.0,
+                 tau: float = 1.0, loss=None, dloss=None, dZ=None, stream=None) -> None:
+    """loss [T] = alpha CE(targets) + (1 - alpha) tau^2 KL(teacher || softmax(Z / tau)) of
+    each row of logits Z [T, V], and where dZ is given its gradient times dloss [T]
+    (None: ones); dZ may be Z.  The teacher's entries teacher_ids (int64) and
+    teacher_logp [T, K] are what tern_logprob with scale = 1 / tau writes; their
+    probabilities are made to sum to one."""
+    fn = "tern_distill"
+    shape = T, V = _rows_of(fn, "Z", Z)
+    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT)
+    dz, lddz = None, 0
+    if dZ is not None:
+        dz, lddz, _ = _logits(fn, "dZ", dZ, shape, (Z.dtype,))
+    K = 0
+    if teacher_ids is not None or teacher_logp is not None:
+        if teacher_ids is None or teacher_logp is None:
+            raise ValueError(f"{fn}: teacher_ids and teacher_logp are given together")
+        K = _rows_of(fn, "teacher_ids", teacher_ids)[1]
+    args = (z, ld, zd, T, V, _vector(fn, "targets", targets, (T,), _I64), K,
+            _vector(fn, "teacher_ids", teacher_ids, (T, K), _I64), _vector(fn, "teacher_logp", teacher_logp, (T, K)),
+            float(alpha), float(tau), _vector(fn, "dloss", dloss, (T,)), _vector(fn, "loss", loss, (T,)), dz, lddz)
+    dev = _device_of(fn, Z, workspace, targets, teacher_ids, teacher_logp, loss, dloss, dZ)
+    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
 
 
 def tern_graph_begin(stream) -> None:

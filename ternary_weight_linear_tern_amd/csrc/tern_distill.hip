@@ -1,0 +1,325 @@
+// tern_distill.hip -- the distillation loss of rows of logits against a
+// teacher's top alternatives, mixed with the cross entropy of given targets, and
+// its gradient (C ABI and formulas in include/tern.h).
+//
+// A row of logits is held in registers (tern_softmax.h): its largest element,
+// then s1 = sum exp(Z - m) and st = sum exp((Z - m) / tau), then the gradient
+//   dloss (alpha exp(Z - m) / s1 + (1 - alpha) tau exp((Z - m) / tau) / st)
+// from the same registers, so that Z is read once and dZ written once.  The few
+// elements that have a target or a teacher's probability to lose are written again,
+// whole, by the wave that wrote them before.  Where one softmax serves both parts
+// (tau = 1, or only one part) each element takes one exponential a pass, else two.
+//
+// Rows that are cut (few rows, or longer than a workgroup's registers) take two
+// launches: the segments' sums, and the logits of the named tokens, which dZ may
+// overwrite; then the gradient, which reads the segments again.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "tern_softmax.h"
+
+namespace tern {
+namespace kdev {
+
+using namespace rows;
+
+constexpr int kEntries = TERN_TOP_MAX + 1;   // the teacher's, and the target
+
+struct DistillArgs {
+    const void *Z;
+    int64_t ld, lddz, T;
+    int V, K, S;
+    int seg;
+    const int64_t *targets, *ids;
+    const float *lp, *dloss;
+    float alpha, tau;
+    float c1, ct;             // log2 e, log2 e / tau
+    bool ce, kl;              // which parts the call has
+    float *loss;
+    void *dZ;
+    float4 *part;             // [T][S]: largest logit, s1, st of a segment
+    float *named;             // [T][65]: logits of the teacher's tokens and of the target
+};
+
+// The tokens a row names.
+struct Names {
+    int id[kEntries];         // -1: none; the last is the target
+    float z[kEntries];        // their logits
+    float less[kEntries];     // what the gradient loses there, before dloss
+    float p[kEntries], logp[kEntries];   // the teacher's
+    bool kl, ce;
+};
+
+// By the first wave of a row.  `z` is the row (its logits are read where `cut` is not
+// set: in a row that is cut they come from the workspace).
+template <int DT>
+__device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z, Names &e, int lane, bool cut) {
+    int64_t id = -1;
+    float lp = -kInf;
+    if (a.kl && lane < a.K) {
+        id = a.ids[t * a.K + lane];
+        lp = a.lp[t * a.K + lane];
+        if (id < 0 || id >= a.V || lp == -kInf) id = -1, lp = -kInf;
+    }
+    int64_t y = a.ce ? a.targets[t] : -1;
+    if (y < 0 || y >= a.V) y = -1;
+    float zid = 0.0f, zy = 0.0f;
+    if (cut) {
+        if (id >= 0) zid = a.named[t * kEntries + lane];
+        if (y >= 0) zy = a.named[t * kEntries + kEntries - 1];
+    } else {
+        if (id >= 0) zid = at<DT>(z, id);
+        if (y >= 0) zy = at<DT>(z, y);
+    }
+    const bool kl = __ballot(id >= 0) != 0;
+    const float lm = wave_all<Max>(lp);
+    float p = id < 0 ? 0.0f : exp2_((lp - lm) * a.c1);
+    const float ps = wave_all<Add>(p);
+    p = id < 0 ? 0.0f : p / ps;
+    // a token that is named twice loses the sum, wherever it stands; the order of the sum is the entries'
+    const int me = (int)id, target = (int)y;
+    float mine = 0.0f, its = 0.0f;
+    for (int j = 0; j < a.K; j++) {
+        const int o = __builtin_amdgcn_readlane(me, j);
+        const float q = as_f(__builtin_amdgcn_readlane(as_u(p), j));
+        mine += o == me ? q : 0.0f;
+        its += o == target ? q : 0.0f;
+    }
+    const float f = (1.0f - a.alpha) * a.tau;
+    e.id[lane] = me;
+    e.z[lane] = zid;
+    e.p[lane] = p;
+    e.logp[lane] = id < 0 ? 0.0f : lp - lm - logf(ps);
+    e.less[lane] = kl ? fmaf(f, mine, me == target ? a.alpha : 0.0f) : 0.0f;
+    if (lane == 0) {
+        e.id[kEntries - 1] = target;
+        e.z[kEntries - 1] = zy;
+        e.less[kEntries - 1] = fmaf(kl ? f : 0.0f, its, a.alpha);
+        e.kl = kl;
+        e.ce = target >= 0;
+    }
+}
+
+// sums of exponentials: of Z - m (s1) and of (Z - m) / tau (st); where one serves both
+// parts, it is st that is taken with the exponent's factor c
+template <int DT, int W, int NV>
+__device__ inline void sums_of(Raw8<DT> (&x)[NV], int n, float m0, float c, float c1, bool two, float &s1,
+                               float &st) {
+    s1 = 0.0f, st = 0.0f;
+    each8<DT, W, NV>(x, n, [&](int, const float *f) {
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) d[j] = f[j] - m0;   // no product of a large logit, which could overflow
+#pragma unroll
+        for (int j = 0; j < 8; j++) st += exp2_(d[j] * c);
+        if (two)
+#pragma unroll
+            for (int j = 0; j < 8; j++) s1 += exp2_(d[j] * c1);
+    });
+}
+
+struct Sums {
+    float m0, s1, st;
+};
+
+// the loss of a row, by its first wave
+__device__ inline void write_loss(const DistillArgs &a, int64_t t, const Names &e, const Sums &s, int lane) {
+    float k = 0.0f;
+    const float p = e.p[lane];
+    if (e.id[lane] >= 0 && p != 0.0f)
+        k = s.st == 0.0f ? kInf : p * (e.logp[lane] - (e.z[lane] - s.m0) / a.tau + logf(s.st));
+    k = wave_all<Add>(k);
+    if (lane != 0) return;
+    float loss = 0.0f;
+    if (e.ce) loss += a.alpha * (s.s1 == 0.0f ? kInf : logf(s.s1) - (e.z[kEntries - 1] - s.m0));
+    if (e.kl) loss += (1.0f - a.alpha) * a.tau * a.tau * k;
+    a.loss[t] = loss;
+}
+
+// the gradient of a segment's n elements, of which `first` is the row's index of the first
+template <int DT, int W, int NV>
+__device__ inline void write_grad(const DistillArgs &a, int64_t t, Raw8<DT> (&x)[NV], int first, int n,
+                                  const Names &e, const Sums &s, float c, bool two, int tid) {
+    constexpr int ST = W * 512, ES = esize<DT>();
+    const float w = a.dloss ? a.dloss[t] : 1.0f;
+    char *dz = (char *)a.dZ + (t * a.lddz + first) * ES;
+    const bool zero = w == 0.0f || !(e.kl || e.ce);
+    float f1 = e.ce && s.s1 != 0.0f ? w * a.alpha / s.s1 : 0.0f;
+    float ft = e.kl && s.st != 0.0f ? w * (1.0f - a.alpha) * a.tau / s.st : 0.0f;
+    if (!two) ft += f1;
+    const int full = n & ~7, l = fresh(tid);
+    const uint32_t off = (uint32_t)l * (8 * ES);
+    float last[8] = {};   // of the stride with the last, partial eight
+    each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+        float d[8], g[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) d[j] = f[j] - s.m0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) g[j] = ft * exp2_(d[j] * c);
+        if (two)
+#pragma unroll
+            for (int j = 0; j < 8; j++) g[j] = fmaf(f1, exp2_(d[j] * a.c1), g[j]);
+        if (zero)
+#pragma unroll
+            for (int j = 0; j < 8; j++) g[j] = 0.0f;
+        if (l * 8 < full - i * ST) store8<DT>(dz + i * ST * ES + off, pack8<DT>(g));
+        if (i == full / ST)
+#pragma unroll
+            for (int j = 0; j < 7; j++) last[j] = g[j];
+    });
+    if (n & 7 && l == full % ST / 8)
+#pragma unroll
+        for (int j = 0; j < 7; j++)
+            if (full + j < n) store1<DT>(dz + (int64_t)full * ES + j * ES, last[j]);
+    if (zero) return;
+    // the named tokens, by the wave that has just written them
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+        const int j = r == 0 ? lane : kEntries - 1;
+        const int v = e.id[j] - first;
+        if ((r == 1 && lane != 0) || e.id[j] < 0 || v < 0 || v >= n || (v / 512) % W != wave) continue;
+        const float d = e.z[j] - s.m0;
+        float g = ft * exp2_(d * c);
+        if (two) g = fmaf(f1, exp2_(d * a.c1), g);
+        store1<DT>(dz + (int64_t)v * ES, fmaf(-w, e.less[j], g));
+    }
+}
+
+// PHASE 0: whole rows.  1: a segment's sums and the named logits.  2: the row's sums from
+// its segments', loss and gradient.
+template <int DT, int W, int NV, int PHASE>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(DistillArgs a) {
+    constexpr int R = W == 1 ? 4 : 1;   // rows of a workgroup
+    __shared__ Names names[R];
+    __shared__ float sh[3][W];
+    const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x, lane = tid & 63;
+    Names &e = names[slot];
+    // one exponential an element, or two
+    const bool two = a.ce && a.kl && a.tau != 1.0f;
+    const float c = a.kl ? a.ct : a.c1;
+    const int64_t items = a.T * a.S;
+    for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
+        const int64_t t = PHASE == 0 ? item : item / a.S;
+        const int s = PHASE == 0 ? 0 : (int)(item - t * a.S), first = s * a.seg, n = min(a.seg, a.V - first);
+        const char *row = (const char *)a.Z + t * a.ld * esize<DT>();
+        Raw8<DT> x[NV];
+        load_row<DT, W, NV>(row + (int64_t)first * esize<DT>(), n, tid, x);
+        if (PHASE == 1) {
+            // logits of the named tokens of this segment
+            if (tid < 64) {
+                const int64_t id = a.kl && lane < a.K ? a.ids[t * a.K + lane] : -1;
+                if (id >= first && id < first + n) a.named[t * kEntries + lane] = at<DT>(row, id);
+                const int64_t y = a.ce && lane == 0 ? a.targets[t] : -1;
+                if (y >= first && y < first + n) a.named[t * kEntries + kEntries - 1] = at<DT>(row, y);
+            }
+        } else if (tid < 64) {
+            read_names<DT>(a, t, row, e, lane, PHASE == 2);
+        }
+        Sums q;
+        if (PHASE != 2) {
+            const float m = row_all<Max, W>(lane_max<DT, W, NV>(x, n), sh[0], tid);
+            q.m0 = m == -kInf ? 0.0f : m;
+            sums_of<DT, W, NV>(x, n, q.m0, c, a.c1, two, q.s1, q.st);
+            row_sums<W>(q.s1, q.st, &sh[1], tid);
+            if (PHASE == 1 && tid == 0) a.part[item] = float4{m, q.s1, q.st, 0.0f};
+        } else {
+            const float4 r = lane < a.S ? a.part[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
+            const float m = wave_all<Max>(r.x);
+            q.m0 = m == -kInf ? 0.0f : m;
+            q.s1 = two ? wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)) : 0.0f;
+            q.st = wave_all<Add>(r.z * exp2_((r.x - q.m0) * c));
+        }
+        if (!two) q.s1 = q.st;
+        if (PHASE != 1) {
+            meet<W>();   // the names are there
+            if (a.loss && s == 0 && tid < 64) write_loss(a, t, e, q, lane);
+            if (a.dZ) write_grad<DT, W, NV>(a, t, x, first, n, e, q, c, two, tid);
+        }
+        meet<W>();
+    }
+}
+
+}  // namespace kdev
+
+namespace {
+
+using kdev::DistillArgs;
+
+int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP; }
+
+size_t workspace_of(const RowPlan &p, int64_t T) {
+    return p.S == 1 ? 0 : (size_t)T * ((size_t)p.S * 16 + kdev::kEntries * 4);
+}
+
+template <int32_t DT, int PHASE>
+struct Launch {
+    DistillArgs a;
+    hipStream_t st;
+    template <int W, int NV>
+    void operator()() const {
+        constexpr int R = W == 1 ? 4 : 1;
+        const dim3 g((unsigned)std::min<int64_t>(cdiv_(a.T * a.S, R), 1 << 21)), b(W == 1 ? 256 : 64 * W);
+        hipLaunchKernelGGL((kdev::distill_kernel<DT, W, NV, PHASE>), g, b, 0, st, a);
+    }
+};
+
+template <int32_t DT>
+void run(const DistillArgs &a, const RowPlan &p, hipStream_t st) {
+    if (a.S == 1) {
+        with_plan<DT>(p, Launch<DT, 0>{a, st});
+    } else {
+        with_plan<DT>(p, Launch<DT, 1>{a, st});
+        with_plan<DT>(p, Launch<DT, 2>{a, st});
+    }
+}
+
+}  // namespace
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" {
+
+size_t tern_distill_workspace_bytes(int64_t T, int64_t V) {
+    if (!row_sizes_ok(T, V)) return 0;
+    return std::max(workspace_of(plan_rows(TERN_F32, T, V), T), workspace_of(plan_rows(TERN_BF16, T, V), T));
+}
+
+int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t V, const int64_t *targets, int32_t K,
+                 const int64_t *teacher_ids, const float *teacher_logp, float alpha, float tau, const float *dloss,
+                 float *loss, void *dZ, int64_t lddz, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!row_sizes_ok(T, V) || !row_stride_ok(ld, V) || (dZ && !row_stride_ok(lddz, V))) return TERN_ERR_SHAPE;
+    if (z_dtype != TERN_F32 && z_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+    if (K < 0 || K > TERN_TOP_MAX || !(alpha >= 0.0f && alpha <= 1.0f) || !(tau > 0.0f) || !factor_ok(1.0 / tau) ||
+        !std::isfinite(tau * tau))
+        return TERN_ERR_VALUE;
+    if (T == 0 || (!loss && !dZ)) return TERN_OK;
+    if (!Z || (K > 0 && (!teacher_ids || !teacher_logp))) return TERN_ERR_NULL;
+    const RowPlan p = plan_rows(z_dtype, T, V);
+    const size_t wsb = workspace_of(p, T);
+    if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
+    if (off_by(Z, 16) || off_by(dZ, 16) || off_by(targets, 8) || off_by(teacher_ids, 8) || off_by(teacher_logp, 4) ||
+        off_by(dloss, 4) || off_by(loss, 4) || off_by(workspace, 16))
+        return TERN_ERR_ALIGN;
+    const size_t es = z_dtype == TERN_BF16 ? 2 : 4;
+    // every element of Z is read before its place in dZ is written, so dZ may be Z
+    const bool in_place = dZ == Z && lddz == ld;
+    const Mat outs[] = {{dZ, T, V, lddz, es}, vec(loss, T, 4), vec(workspace, (int64_t)wsb, 1)};
+    const Mat ins[] = {vec(targets, T, 8), vec(teacher_ids, T * K, 8), vec(teacher_logp, T * K, 4), vec(dloss, T, 4),
+                       {in_place ? nullptr : Z, T, V, ld, es}};
+    if (any_overlap(outs, 3, ins, 5)) return TERN_ERR_ALIAS;
+    DistillArgs a{Z, ld, lddz, T, (int)V, K, p.S, (int)p.seg, targets, teacher_ids, teacher_logp, dloss, alpha, tau,
+                  (float)rows::kLog2e, (float)(rows::kLog2e / tau), alpha > 0.0f && targets, alpha < 1.0f && K > 0, loss,
+                  dZ, (float4 *)workspace, nullptr};
+    if (p.S > 1) a.named = (float *)(a.part + T * p.S);
+    hipStream_t st = (hipStream_t)stream;
+    if (z_dtype == TERN_BF16) run<TERN_BF16>(a, p, st);
+    else run<TERN_F32>(a, p, st);
+    return launched();
+}
+
+}  // extern "C"

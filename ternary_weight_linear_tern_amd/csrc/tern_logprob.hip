@@ -1,0 +1,351 @@
+// tern_logprob.hip -- log probabilities of given tokens, entropy and top
+// alternatives of rows of logits (C ABI and formulas in include/tern.h).
+//
+// With m the row's largest logit and d = (Z - m) scale <= 0,
+//   s = sum e^d,  u = sum e^d d:  logp = d[token] - log s,  entropy = log s - u / s.
+// The exponentials are powers of two (d is carried in units of log 2).
+//
+// The k largest: 256 groups of lanes (64 where one wave has the row) know their
+// own largest element.  The k-th largest of those is a bound that at least k
+// elements reach, and hardly more do; a bisection over its bits by one wave finds
+// it.  The elements that reach it go to a list in shared memory, and each one's
+// place is the number of greater keys there.  Rows whose list would overflow (ties,
+// rows in which fewer than k tokens are allowed) are taken one alternative after
+// the other.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tern_softmax.h"
+
+namespace tern {
+namespace hdev {
+
+using namespace rows;
+
+struct LogprobArgs {
+    const void *Z;
+    int64_t ld, T;
+    int V, k, S;
+    int seg;
+    float scale, c;            // c = scale log2 e
+    const int64_t *tokens;
+    float *logp, *entropy, *lse;
+    int64_t *top_ids;
+    float *top_logp;
+    float4 *part;              // [T][S]: largest logit, s, u of a segment
+    uint64_t *keys;            // [T][S][k]: its alternatives, 0 behind the last
+};
+
+template <int W>
+struct Pick {
+    static constexpr int kGroups = W >= 4 ? 256 : 64, kRoom = W >= 4 ? 1024 : 256;
+    uint64_t key[kRoom];
+    uint64_t round[2][W];
+    uint32_t group[kGroups];
+    uint32_t bound;
+    int count;
+};
+
+struct MaxU {
+    __device__ static uint32_t of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+};
+struct MinU {
+    __device__ static uint32_t of(uint32_t a, uint32_t b) { return a < b ? a : b; }
+};
+template <class Op>
+__device__ inline uint32_t wave_all_u(uint32_t x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x = Op::of(x, (uint32_t)__shfl_xor((int)x, d));
+    return x;
+}
+__device__ inline uint64_t wave_max64(uint64_t x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint64_t y = __shfl_xor((unsigned long long)x, d);
+        x = y > x ? y : x;
+    }
+    return x;
+}
+
+// A bound that at least k of the groups' largest reach (0 where there are not k
+// groups), by one wave.
+template <int G>
+__device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
+    uint32_t g[G / 64];
+#pragma unroll
+    for (int i = 0; i < G / 64; i++) g[i] = group[i * 64 + lane];
+    uint32_t most = g[0], least = g[0];
+#pragma unroll
+    for (int i = 1; i < G / 64; i++) most = max(most, g[i]), least = min(least, g[i]);
+    most = wave_all_u<MaxU>(most);
+    if (k == 1) return most;
+    if (k > G) return 0;
+    auto reach = [&](uint32_t t) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < G / 64; i++) c += __builtin_popcountll(__ballot(g[i] >= t));
+        return c;
+    };
+    if (reach(most) >= k) return most;
+    // at least k reach lo, fewer than k reach hi; a few more than k will do
+    uint32_t lo = wave_all_u<MinU>(least), hi = most;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int c = reach(mid);
+        if (c >= k) {
+            lo = mid;
+            if (c <= k + k / 4 + 2) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
+// The k largest of the n elements from z on (k <= n), which x holds, `first` the index
+// of the first: put(place, key) for each.
+template <int DT, int W, int NV, class Put>
+__device__ inline void top_keys(const char *z, Raw8<DT> (&x)[NV], int n, uint32_t first, int k, float mine, Pick<W> &p, int tid,
+                                Put put) {
+    constexpr int G = Pick<W>::kGroups, PER = W * 64 / G, ST = W * 512;
+    float m = mine;
+    if constexpr (PER >= 2) m = fmaxf(m, dpp<0xB1>(m));
+    if constexpr (PER >= 4) m = fmaxf(m, dpp<0x4E>(m));
+    if (tid % PER == 0) p.group[tid / PER] = ordered(m);
+    if (tid == 0) p.count = 0;
+    meet<W>();
+    if (tid < 64) {
+        const uint32_t b = bound_of<G>(p.group, k, tid);
+        if (tid == 0) p.bound = b;
+    }
+    meet<W>();
+    const float bound = from_ordered(p.bound);   // of 0: NaN, below which nothing is
+    if (__ballot(!(mine < bound))) {
+        const int lane = fresh(tid);
+        each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+            if (max8(f) < bound) return;
+            const int v = i * ST + lane * 8;
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (!(f[j] < bound) && v + j < n) {
+                    const int at = atomicAdd(&p.count, 1);
+                    if (at < Pick<W>::kRoom) p.key[at] = key_of(f[j], first + v + j);
+                }
+        });
+    }
+    meet<W>();
+    const int count = p.count;
+    if (count >= k && count <= Pick<W>::kRoom) {
+        for (int q = tid; q < count; q += W * 64) {
+            const uint64_t key = p.key[q];
+            int place = 0;
+            for (int i = 0; i < count; i++) place += p.key[i] > key;
+            if (place < k) put(place, key);
+        }
+        return;
+    }
+    // one after the other: each lane keeps its largest key below the last one taken
+    // (of the row in memory, which the caches hold: a rare way needs no registers)
+    uint64_t last = ~(uint64_t)0, best = 0;
+    for (int r = 0; r < k; r++) {
+        if (best == last || r == 0) {
+            best = 0;
+            for (int v = tid; v < n; v += W * 64) {
+                const uint64_t key = key_of(at<DT>(z, v), first + v);
+                if (key < last && key > best) best = key;
+            }
+        }
+        uint64_t top = wave_max64(best);
+        if constexpr (W > 1) {
+            if ((tid & 63) == 0) p.round[r & 1][tid >> 6] = top;
+            __syncthreads();
+            for (int i = 0; i < W; i++) top = max(top, p.round[r & 1][i]);
+        }
+        last = top;
+        if (tid == 0) put(r, top);
+    }
+}
+
+// what a row's sums say
+struct RowEnd {
+    float m0, s, logs, scale;
+    __device__ float log_p(float z) const { return s == 0.0f ? -kInf : (z - m0) * scale - logs; }
+};
+__device__ inline RowEnd finish_row(const LogprobArgs &a, int64_t t, float m0, float s, float u, int tid) {
+    RowEnd r{m0, s, logf(s), a.scale};
+    if (tid == 0) {
+        if (a.lse) a.lse[t] = fmaf(m0, a.scale, r.logs);
+        if (a.entropy) a.entropy[t] = s == 0.0f ? 0.0f : r.logs - u / s * kLn2;
+    }
+    return r;
+}
+
+template <int DT>
+__device__ inline void token_of(const LogprobArgs &a, int64_t t, const RowEnd &r, int tid) {
+    if (!a.tokens || tid != 0) return;
+    const int64_t y = a.tokens[t];
+    a.logp[t] = y >= 0 && y < a.V ? r.log_p(at<DT>((const char *)a.Z + t * a.ld * esize<DT>(), y)) : 0.0f;
+}
+
+template <int DT, int W, int NV>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(LogprobArgs a) {
+    constexpr int R = W == 1 ? 4 : 1;   // rows of a workgroup
+    __shared__ Pick<W> picks[R];
+    __shared__ float sh[3][W];
+    const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x;
+    Pick<W> &pick = picks[slot];
+    const int64_t items = a.T * a.S;
+    for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
+        const int64_t t = a.S == 1 ? item : item / a.S;
+        const int s = (int)(item - t * a.S), first = s * a.seg, n = min(a.seg, a.V - first);
+        const char *z = (const char *)a.Z + (t * a.ld + first) * esize<DT>();
+        Raw8<DT> x[NV];
+        load_row<DT, W, NV>(z, n, tid, x);
+        const float mine = lane_max<DT, W, NV>(x, n);
+        const float m = row_all<Max, W>(mine, sh[0], tid), m0 = m == -kInf ? 0.0f : m;
+        float sum = 0.0f, u = 0.0f;
+        each8<DT, W, NV>(x, n, [&](int, const float *f) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                // from the largest on: no product of a large logit, which could overflow
+                const float d = (f[j] - m0) * a.c, e = exp2_(d);
+                sum += e;
+                u = fmaf(e, fmaxf(d, -200.0f), u);   // (-inf: e is 0)
+            }
+        });
+        row_sums<W>(sum, u, &sh[1], tid);
+        if (a.S == 1) {
+            const RowEnd r = finish_row(a, t, m0, sum, u, tid);
+            token_of<DT>(a, t, r, tid);
+            if (a.k)
+                top_keys<DT, W, NV>(z, x, n, 0, a.k, mine, pick, tid, [&](int place, uint64_t key) {
+                    a.top_ids[t * a.k + place] = index_of(key);
+                    a.top_logp[t * a.k + place] = r.log_p(value_of(key));
+                });
+        } else {
+            if (tid == 0) a.part[item] = float4{m, sum, u, 0.0f};
+            if (a.k) {
+                uint64_t *out = a.keys + item * a.k;
+                const int k = min(a.k, n);
+                for (int i = k + tid; i < a.k; i += W * 64) out[i] = 0;
+                top_keys<DT, W, NV>(z, x, n, first, k, mine, pick, tid, [&](int place, uint64_t key) { out[place] = key; });
+            }
+        }
+        meet<W>();
+    }
+}
+
+// Rows that were cut: the segments' sums meet, and their alternatives.  Each
+// segment's keys fall, so that with r = ceil(k / S) the smallest of their r-th is
+// reached by k at least.
+template <int DT>
+__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
+    __shared__ uint64_t list[kMaxSegments * TERN_TOP_MAX];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        float4 q = lane < a.S ? a.part[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
+        const float m = wave_all<Max>(q.x), m0 = m == -kInf ? 0.0f : m;
+        const float d = (q.x - m0) * a.c, f = exp2_(d);
+        const float s = wave_all<Add>(f * q.y), u = wave_all<Add>(f * fmaf(q.y, fmaxf(d, -200.0f), q.z));
+        const RowEnd r = finish_row(a, t, m0, s, u, tid);
+        token_of<DT>(a, t, r, tid);
+        if (!a.k) continue;
+        const uint64_t *keys = a.keys + t * a.S * a.k;
+        const int rank = (a.k + a.S - 1) / a.S - 1;
+        uint64_t bound = lane < a.S ? keys[lane * a.k + rank] : ~(uint64_t)0;
+#pragma unroll
+        for (int i = 1; i < 64; i *= 2) bound = min(bound, (uint64_t)__shfl_xor((unsigned long long)bound, i));
+        if (tid == 0) count = 0;
+        __syncthreads();
+        for (int i = tid; i < a.S * a.k; i += 256) {
+            const uint64_t key = keys[i];
+            if (key >= bound && key) list[atomicAdd(&count, 1)] = key;
+        }
+        __syncthreads();
+        const int n = count;
+        for (int i = tid; i < n; i += 256) {
+            const uint64_t key = list[i];
+            int place = 0;
+            for (int j = 0; j < n; j++) place += list[j] > key;
+            if (place < a.k) {
+                a.top_ids[t * a.k + place] = index_of(key);
+                a.top_logp[t * a.k + place] = r.log_p(value_of(key));
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace hdev
+
+namespace {
+
+using hdev::LogprobArgs;
+
+int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP; }
+
+size_t workspace_of(const RowPlan &p, int64_t T, int32_t k) {
+    return p.S == 1 ? 0 : (size_t)T * (size_t)p.S * (16 + 8 * (size_t)k);
+}
+
+template <int32_t DT>
+struct Launch {
+    LogprobArgs a;
+    hipStream_t st;
+    template <int W, int NV>
+    void operator()() const {
+        constexpr int R = W == 1 ? 4 : 1;
+        const dim3 g((unsigned)std::min<int64_t>(cdiv_(a.T * a.S, R), 1 << 21)), b(W == 1 ? 256 : 64 * W);
+        hipLaunchKernelGGL((hdev::logprob_kernel<DT, W, NV>), g, b, 0, st, a);
+    }
+};
+
+template <int32_t DT>
+void run(const LogprobArgs &a, const RowPlan &p, hipStream_t st) {
+    with_plan<DT>(p, Launch<DT>{a, st});
+    if (a.S > 1)
+        hipLaunchKernelGGL(hdev::logprob_join_kernel<DT>, dim3((unsigned)std::min<int64_t>(a.T, 1 << 21)), dim3(256), 0,
+                           st, a);
+}
+
+}  // namespace
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" {
+
+size_t tern_logprob_workspace_bytes(int64_t T, int64_t V, int32_t k) {
+    if (!row_sizes_ok(T, V) || k < 0 || k > TERN_TOP_MAX) return 0;
+    return std::max(workspace_of(plan_rows(TERN_F32, T, V), T, k), workspace_of(plan_rows(TERN_BF16, T, V), T, k));
+}
+
+int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_t T, int64_t V, const int64_t *tokens,
+                 float *logp, float *entropy, float *lse, int32_t k, int64_t *top_ids, float *top_logp,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!row_sizes_ok(T, V) || !row_stride_ok(ld, V)) return TERN_ERR_SHAPE;
+    if (z_dtype != TERN_F32 && z_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+    if (!factor_ok(scale) || k < 0 || k > TERN_TOP_MAX || k > V) return TERN_ERR_VALUE;
+    if (T == 0) return TERN_OK;
+    if (!Z || !tokens != !logp || (k > 0 && (!top_ids || !top_logp))) return TERN_ERR_NULL;
+    const RowPlan p = plan_rows(z_dtype, T, V);
+    const size_t wsb = workspace_of(p, T, k);
+    if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
+    if (off_by(Z, 16) || off_by(tokens, 8) || off_by(top_ids, 8) || off_by(logp, 4) || off_by(entropy, 4) ||
+        off_by(lse, 4) || off_by(top_logp, 4) || off_by(workspace, 16))
+        return TERN_ERR_ALIGN;
+    const Mat outs[] = {vec(logp, T, 4), vec(entropy, T, 4), vec(lse, T, 4), vec(top_ids, T * k, 8),
+                        vec(top_logp, T * k, 4), vec(workspace, (int64_t)wsb, 1)};
+    const Mat ins[] = {{Z, T, V, ld, (size_t)(z_dtype == TERN_BF16 ? 2 : 4)}, vec(tokens, T, 8)};
+    if (any_overlap(outs, 6, ins, 2)) return TERN_ERR_ALIAS;
+    LogprobArgs a{Z, ld, T, (int)V, k, p.S, (int)p.seg, scale, (float)(scale * rows::kLog2e), tokens, logp, entropy, lse,
+                  top_ids, top_logp, (float4 *)workspace, nullptr};
+    if (p.S > 1) a.keys = (uint64_t *)(a.part + T * p.S);
+    hipStream_t st = (hipStream_t)stream;
+    if (z_dtype == TERN_BF16) run<TERN_BF16>(a, p, st);
+    else run<TERN_F32>(a, p, st);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,239 @@
+// tern_softmax.h -- rows of logits held in registers, shared by the log
+// probabilities (tern_logprob.hip) and the distillation loss (tern_distill.hip).
+//
+// A row, or a segment of one, is read once: W waves take it in strides of W * 512
+// elements, eight neighbours a lane, and NV such eights stay in a lane's
+// registers as they came.  Its largest element is then known before the first
+// exponential, so a sum needs no rescaling, and what comes after the sums (the
+// top alternatives, the gradient) reads registers again and not memory.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/tern.h"
+#include "tern_mat.h"
+#include "tern_plan.h"
+#include "tern_rows.h"
+
+namespace tern {
+namespace rows {
+
+constexpr float kInf = __builtin_inff();
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// (v_max3: fmaxf of loaded bits makes two instructions, one to quiet NaNs)
+__device__ inline float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// The lanes of a row meet: those of a workgroup, or of the one wave that has it.
+template <int W>
+__device__ inline void meet() {
+    if constexpr (W > 1) {
+        __syncthreads();
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Eight elements that are not there.
+template <int DT>
+__device__ inline Raw8<DT> none8() {
+    constexpr uint32_t w = DT == TERN_BF16 ? 0xFF80FF80u : 0xFF800000u;
+    Raw8<DT> r;
+#pragma unroll
+    for (int i = 0; i < Raw8<DT>::N; i++) r.v[i] = u32x4{w, w, w, w};
+    return r;
+}
+
+// A lane's number that the compiler takes for new: it would compute what depends
+// on it for all rows ahead of the loop over them, and spill that.
+__device__ inline int fresh(int tid) {
+    asm volatile("" : "+v"(tid));
+    return tid;
+}
+
+// The n elements from z on into registers, -inf behind them.
+template <int DT, int W, int NV>
+__device__ inline void load_row(const char *z, int n, int tid, Raw8<DT> (&x)[NV]) {
+    constexpr int ST = W * 512, ES = esize<DT>();
+    const int full = n & ~7;
+    const uint32_t lane = (uint32_t)tid * (8 * ES);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        x[i] = none8<DT>();
+        if (tid * 8 < full - i * ST) x[i] = load8<DT>(z + i * ST * ES + lane);
+    }
+    if (n & 7 && tid == full % ST / 8) {   // the lane that has the last, partial eight
+        const char *p = z + (int64_t)full * ES;
+        Raw8<DT> t = none8<DT>();
+#pragma unroll
+        for (int j = 0; j < 7; j++) {
+            if (full + j >= n) continue;
+            if constexpr (DT == TERN_BF16) {
+                const uint32_t e = ((const uint16_t *)p)[j], keep = j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                t.v[0][j >> 1] = (t.v[0][j >> 1] & keep) | e << (j & 1 ? 16 : 0);
+            } else {
+                t.v[j >> 2][j & 3] = ((const uint32_t *)p)[j];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (i == full / ST) x[i] = t;
+    }
+}
+
+__device__ inline float max8(const float *f) {
+    return max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+}
+
+// A pass over the registers: f(i, eight elements) of each stride that the row
+// reaches.  An eight is opaque to the compiler at its turn, and nothing moves
+// across turns: it would keep the unpacked elements of one pass for the next, and
+// unpack all of them first, at twice the registers.
+template <int DT, int W, int NV, class F>
+__device__ inline void each8(Raw8<DT> (&x)[NV], int n, F f) {
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+        if (i * W * 512 < n) {
+#pragma unroll
+            for (int j = 0; j < Raw8<DT>::N; j++) asm volatile("" : "+v"(x[i].v[j]));
+            float e[8];
+            unpack8<DT>(x[i], e);
+            f(i, e);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+// A lane's largest element (NaN loses against a number).
+template <int DT, int W, int NV>
+__device__ inline float lane_max(Raw8<DT> (&x)[NV], int n) {
+    float m = -kInf;
+    each8<DT, W, NV>(x, n, [&](int, const float *f) {
+        m = max3(max3(m, f[0], f[1]), max3(f[2], f[3], f[4]), max3(f[5], f[6], f[7]));
+    });
+    return m;
+}
+
+// Reductions over the W waves of a row; sh holds W floats, which are free
+// again after the next meeting.
+template <class Op, int W>
+__device__ inline float row_all(float x, float *sh, int tid) {
+    x = wave_all<Op>(x);
+    if constexpr (W > 1) {
+        if ((tid & 63) == 0) sh[tid >> 6] = x;
+        __syncthreads();
+        x = sh[0];
+#pragma unroll
+        for (int i = 1; i < W; i++) x = Op::of(x, sh[i]);
+    }
+    return x;
+}
+template <int W>
+__device__ inline void row_sums(float &a, float &b, float (*sh)[W], int tid) {
+    a = wave_all<Add>(a);
+    b = wave_all<Add>(b);
+    if constexpr (W > 1) {
+        if ((tid & 63) == 0) sh[0][tid >> 6] = a, sh[1][tid >> 6] = b;
+        __syncthreads();
+        a = sh[0][0], b = sh[1][0];
+#pragma unroll
+        for (int i = 1; i < W; i++) a += sh[0][i], b += sh[1][i];
+    }
+}
+
+// Bits that order as the values do, -0 as +0, NaN outermost.
+__device__ inline uint32_t ordered(float f) {
+    const uint32_t b = as_u(f + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ inline float from_ordered(uint32_t o) { return as_f(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
+// The value, then the lower index: no two elements of a row have one key.
+__device__ inline uint64_t key_of(float f, uint32_t i) { return (uint64_t)ordered(f) << 32 | (0xFFFFFFFFu - i); }
+__device__ inline int index_of(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
+__device__ inline float value_of(uint64_t key) { return from_ordered((uint32_t)(key >> 32)); }
+
+template <int DT>
+__device__ inline float at(const char *z, int64_t v) { return load1<DT>(z + v * esize<DT>()); }
+
+}  // namespace rows
+
+// ---------------------------------------------------------------------------
+// How the rows are dealt out (host).
+// ---------------------------------------------------------------------------
+
+// Eights a lane holds at most: 64 registers.
+constexpr int held(int32_t dt) { return dt == TERN_BF16 ? 16 : 8; }
+constexpr int kMaxSegments = 64;
+
+struct RowPlan {
+    int S, W, NV;    // segments of a row; waves of a segment and eights of a lane
+    int64_t seg;     // elements of a segment (the last may have fewer)
+};
+
+inline int64_t cdiv_(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Whole rows where there are enough of them (one launch, and a gradient that
+// need not read its row again); few long rows are cut, so that some 512
+// workgroups share them.
+inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V) {
+    const int nv = held(dt);
+    RowPlan p{};
+    int64_t S = cdiv_(V, (int64_t)16 * 512 * nv);
+    if (T < 128) S = std::max(S, std::min(cdiv_(512, std::max<int64_t>(T, 1)), cdiv_(V, 4096)));
+    S = std::min<int64_t>(S, kMaxSegments);
+    p.seg = cdiv_(cdiv_(V, S), 8) * 8;
+    p.S = (int)cdiv_(V, p.seg);
+    // waves: what the registers take, and more where the rows leave the chip empty
+    p.W = 1;
+    for (int w : {4, 8, 16})
+        if ((int64_t)p.W * 512 * nv < p.seg) p.W = w;
+    for (int w : {4, 16})
+        if (w > p.W && T * p.S * p.W < 2048 && (int64_t)p.W * 512 < p.seg) p.W = w;
+    p.NV = nv;
+    for (int v : {4, 1})
+        if ((int64_t)p.W * 512 * v >= p.seg) p.NV = v;
+    return p;
+}
+
+// f<W, NV>() of the kernel that a plan asks for.
+template <int32_t DT, class F>
+void with_plan(const RowPlan &p, F f) {
+    constexpr int H = held(DT);
+    const bool big = p.NV > 4;
+    switch (p.W) {
+    case 1:
+        if (big) f.template operator()<1, H>();
+        else if (p.NV > 1) f.template operator()<1, 4>();
+        else f.template operator()<1, 1>();
+        break;
+    case 4:
+        if (big) f.template operator()<4, H>();
+        else f.template operator()<4, 4>();
+        break;
+    case 8:
+        f.template operator()<8, H>();
+        break;
+    default:
+        if (big) f.template operator()<16, H>();
+        else f.template operator()<16, 4>();
+    }
+}
+
+inline bool row_sizes_ok(int64_t T, int64_t V) { return T >= 0 && T <= kMaxT && V >= 1 && V <= kMaxInOut; }
+inline bool row_stride_ok(int64_t ld, int64_t V) { return ld >= V && ld % 8 == 0 && ld <= kMaxInOut * 8; }
+// a factor of the logits and its product with log2 e, above 0 and finite
+inline bool factor_ok(double x) { return x > 0.0 && x * rows::kLog2e <= 3.4e38; }
+inline bool off_by(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) != 0; }
+inline Mat vec(const void *p, int64_t n, size_t es) { return {p, 1, n, n, es}; }
+
+}  // namespace tern

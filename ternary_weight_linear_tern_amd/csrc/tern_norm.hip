@@ -22,15 +22,13 @@ namespace ndev {
 
 using namespace rows;
 
-constexpr int kNone = 2;   // type code of an array that is not there
-
 struct FwdArgs {
     const void *X, *A;
     const float *w, *b;
     void *S, *Y;
     float *stats;
     int64_t ldx, lda, lds, ldy, T;
-    int C;
+    int C, W, a_dtype;
     float eps;
 };
 
@@ -41,8 +39,8 @@ struct BwdArgs {
     float *dw, *db;
     float *part;             // [groups][2][C]: dw and db of the groups' rows
     int64_t lds, lddy, ldds, lddx, T;
-    int64_t groups, per;     // row groups and rows of a group
-    int C;
+    int64_t groups;          // row groups, a workgroup each
+    int C, W;
 };
 
 template <int DT>
@@ -62,29 +60,148 @@ __device__ inline void coef8(const float *p, int c, float fill, float *f) {
     }
 }
 
+// An eight of A, which has a type of its own: told by a uniform branch.
+struct RawA {
+    Raw8<TERN_F32> r;
+    __device__ void load(const void *A, int dt, int64_t row, int64_t ld, int c) {
+        if (dt == TERN_BF16) r.v[0] = load8<TERN_BF16>((const char *)A + (row * ld + c) * 2).v[0];
+        else r = load8<TERN_F32>((const char *)A + (row * ld + c) * 4);
+    }
+    __device__ void add_to(int dt, float *x) const {
+        float f[8];
+        if (dt == TERN_BF16) unpack8<TERN_BF16>(Raw8<TERN_BF16>{{r.v[0]}}, f);
+        else unpack8<TERN_F32>(r, f);
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] += f[j];
+    }
+};
+
+// How a workgroup takes rows of up to 16 * 512 * CV columns: W waves a row, eight
+// neighbours a lane, CV times; R rows at once.
+struct Lanes {
+    int W, R, slot, tid, wave;   // this lane's row among the R, its number and its wave in the row
+    __device__ explicit Lanes(int waves) : W(waves) {
+        const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        R = (int)blockDim.x / (64 * W);
+        slot = w / W;
+        wave = w - slot * W;
+        tid = wave * 64 + (int)(threadIdx.x & 63);
+    }
+    __device__ int col(int v) const { return (v * W * 64 + tid) * 8; }
+    // columns of wave w of a row
+    template <int CV>
+    __device__ float columns(int w, int C) const {
+        int n = 0;
+#pragma unroll
+        for (int v = 0; v < CV; v++) n += min(max(C - (v * W + w) * 512, 0), 512);
+        return (float)n;
+    }
+};
+constexpr int kMaxWaves = 16;
+constexpr int kTogether = 8;   // waves of a backward workgroup that has several rows
+
+// Rows in registers.  A workgroup goes on to further rows, with w and b in
+// registers and, where they leave room (CV 1), the next rows' loads under way.  Each
+// wave takes the mean of its columns and the squares around that; the waves'
+// meet by n_i (mu_i - mu)^2: one barrier for R rows.
+template <int XD, int YD, int CV>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a) {
+    __shared__ float2 sh[2][kMaxWaves];
+    const Lanes l(a.W);
+    float w[CV][8], b[CV][8];
+#pragma unroll
+    for (int v = 0; v < CV; v++)
+        if (l.col(v) < a.C) {
+            coef8(a.w, l.col(v), 1.0f, w[v]);
+            coef8(a.b, l.col(v), 0.0f, b[v]);
+        }
+    Raw8<XD> nx[CV];
+    RawA na[CV];
+    auto fetch = [&](int64_t t) {
+        if (t >= a.T) return;
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (l.col(v) < a.C) {
+                nx[v] = load8<XD>((const char *)a.X + (t * a.ldx + l.col(v)) * esize<XD>());
+                if (a.A) na[v].load(a.A, a.a_dtype, t, a.lda, l.col(v));
+            }
+    };
+    const int64_t step = (int64_t)gridDim.x * l.R;
+    const float n = l.columns<CV>(l.wave, a.C);
+    if (CV == 1) fetch((int64_t)blockIdx.x * l.R + l.slot);
+    int turn = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * l.R; t0 < a.T; t0 += step, turn ^= 1) {
+        const int64_t t = t0 + l.slot;
+        const bool here = t < a.T;
+        if (CV > 1) fetch(t);
+        float x[CV][8], sum = 0.0f, sq = 0.0f;
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (here && l.col(v) < a.C) {
+                unpack8<XD>(nx[v], x[v]);
+                if (a.A) {
+                    na[v].add_to(a.a_dtype, x[v]);
+                    const Raw8<XD> s = pack8<XD>(x[v]);   // the norm is that of S as stored
+                    store8<XD>((char *)a.S + (t * a.lds + l.col(v)) * esize<XD>(), s);
+                    unpack8<XD>(s, x[v]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) sum += x[v][j];
+            }
+        if (CV == 1) fetch(t + step);
+        float mu = wave_all<Add>(sum) / fmaxf(n, 1.0f);
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (here && l.col(v) < a.C)
+#pragma unroll
+                for (int j = 0; j < 8; j++) sq = fmaf(x[v][j] - mu, x[v][j] - mu, sq);
+        sq = wave_all<Add>(sq);
+        if (l.W > 1) {
+            const float2 *of = &sh[turn][l.slot * l.W];
+            if ((threadIdx.x & 63) == 0) sh[turn][l.slot * l.W + l.wave] = float2{mu, sq};
+            __syncthreads();
+            float m = 0.0f;
+            for (int i = 0; i < l.W; i++) m = fmaf(l.columns<CV>(i, a.C), of[i].x, m);
+            mu = m / (float)a.C;
+            sq = 0.0f;
+            for (int i = 0; i < l.W; i++) {
+                const float d = of[i].x - mu;
+                sq += fmaf(l.columns<CV>(i, a.C) * d, d, of[i].y);
+            }
+        }
+        const float r = 1.0f / sqrtf(sq / (float)a.C + a.eps);
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (here && l.col(v) < a.C) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) x[v][j] = fmaf((x[v][j] - mu) * r, w[v][j], b[v][j]);
+                store8<YD>((char *)a.Y + (t * a.ldy + l.col(v)) * esize<YD>(), pack8<YD>(x[v]));
+            }
+        if (a.stats && here && l.tid == 0) *(float2 *)(a.stats + 2 * t) = float2{mu, r};
+    }
+}
+
 // Rows of any length: a workgroup a row, which it reads three times.
-template <int XD, int AD, int YD>
+template <int XD, int YD>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(FwdArgs a) {
     __shared__ float sh[2][4];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         float sum = 0.0f, sq = 0.0f;
-        const void *src = a.X;
-        int64_t ld = a.ldx;
         for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
             float x[8];
             get8<XD>(a.X, t, a.ldx, c, x);
-            if constexpr (AD != kNone) {
-                float y[8];
-                get8<AD>(a.A, t, a.lda, c, y);
-#pragma unroll
-                for (int j = 0; j < 8; j++) x[j] += y[j];
+            if (a.A) {
+                RawA y;
+                y.load(a.A, a.a_dtype, t, a.lda, c);
+                y.add_to(a.a_dtype, x);
                 put8<XD>(a.S, t, a.lds, c, x);
                 unpack8<XD>(pack8<XD>(x), x);
             }
 #pragma unroll
             for (int j = 0; j < 8; j++) sum += x[j];
         }
-        if constexpr (AD != kNone) src = a.S, ld = a.lds;   // each lane reads what it wrote
+        const void *src = a.A ? a.S : a.X;   // each lane reads what it wrote
+        const int64_t ld = a.A ? a.lds : a.ldx;
         const float mu = group_all<Add, 4>(sum, sh[0]) / (float)a.C;
         for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
             float x[8];
@@ -104,6 +221,111 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(FwdArgs a) {
         }
         if (a.stats && threadIdx.x == 0) *(float2 *)(a.stats + 2 * t) = float2{mu, r};
         __syncthreads();
+    }
+}
+
+// The backward of rows in registers, as the forward's: S and dY are read once, for
+// dX and for the sums of dw and db, which a lane keeps for its columns over all
+// rows of its workgroup.
+template <int SD, int DY, int DX, int CV>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a) {
+    __shared__ float2 sh[2][kMaxWaves];
+    __shared__ float4 meet[kTogether * 128];   // [R][C / 4] where there are several rows
+    const Lanes l(a.W);
+    float w[CV][8], dw[CV][8] = {}, db[CV][8] = {};
+#pragma unroll
+    for (int v = 0; v < CV; v++)
+        if (l.col(v) < a.C) coef8(a.w, l.col(v), 1.0f, w[v]);
+    Raw8<SD> nx[CV];
+    Raw8<DY> ny[CV];
+    Raw8<DX> nd[CV];
+    float2 ns{};
+    auto fetch = [&](int64_t t) {
+        if (t >= a.T) return;
+        ns = *(const float2 *)(a.stats + 2 * t);
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (l.col(v) < a.C) {
+                nx[v] = load8<SD>((const char *)a.S + (t * a.lds + l.col(v)) * esize<SD>());
+                ny[v] = load8<DY>((const char *)a.dY + (t * a.lddy + l.col(v)) * esize<DY>());
+                if (a.dS) nd[v] = load8<DX>((const char *)a.dS + (t * a.ldds + l.col(v)) * esize<DX>());
+            }
+    };
+    const int64_t step = a.groups * l.R;
+    if (CV == 1) fetch((int64_t)blockIdx.x * l.R + l.slot);
+    int turn = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * l.R; t0 < a.T; t0 += step, turn ^= 1) {
+        const int64_t t = t0 + l.slot;
+        const bool here = t < a.T;
+        if (CV > 1) fetch(t);
+        float xh[CV][8], g[CV][8], s1 = 0.0f, s2 = 0.0f;
+        const float mu = ns.x, r = ns.y;
+        Raw8<DX> d[CV];
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (here && l.col(v) < a.C) {
+                unpack8<SD>(nx[v], xh[v]);
+                unpack8<DY>(ny[v], g[v]);
+                d[v] = nd[v];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    xh[v][j] = (xh[v][j] - mu) * r;
+                    dw[v][j] = fmaf(g[v][j], xh[v][j], dw[v][j]);
+                    db[v][j] += g[v][j];
+                    g[v][j] *= w[v][j];
+                    s1 += g[v][j];
+                    s2 = fmaf(g[v][j], xh[v][j], s2);
+                }
+            }
+        if (CV == 1) fetch(t + step);
+        s1 = wave_all<Add>(s1);
+        s2 = wave_all<Add>(s2);
+        if (l.W > 1) {
+            const float2 *of = &sh[turn][l.slot * l.W];
+            if ((threadIdx.x & 63) == 0) sh[turn][l.slot * l.W + l.wave] = float2{s1, s2};
+            __syncthreads();
+            s1 = s2 = 0.0f;
+            for (int i = 0; i < l.W; i++) s1 += of[i].x, s2 += of[i].y;
+        }
+        const float m1 = s1 / (float)a.C, m2 = s2 / (float)a.C;
+#pragma unroll
+        for (int v = 0; v < CV; v++)
+            if (here && l.col(v) < a.C) {
+                float o[8] = {};
+                if (a.dS) unpack8<DX>(d[v], o);
+#pragma unroll
+                for (int j = 0; j < 8; j++) o[j] = fmaf(r, fmaf(-xh[v][j], m2, g[v][j] - m1), o[j]);
+                store8<DX>((char *)a.dX + (t * a.lddx + l.col(v)) * esize<DX>(), pack8<DX>(o));
+            }
+    }
+    if (!a.part) return;
+    // the workgroup's sums: the R rows' in order
+#pragma unroll
+    for (int which = 0; which < 2; which++) {
+        float *out = a.part + ((int64_t)blockIdx.x * 2 + which) * a.C;
+        if (l.R == 1) {
+#pragma unroll
+            for (int v = 0; v < CV; v++)
+                if (l.col(v) < a.C) store8<TERN_F32>(out + l.col(v), pack8<TERN_F32>(which ? db[v] : dw[v]));
+        } else if (CV == 1) {
+            const int n4 = a.C / 4;   // at most W * 128
+            __syncthreads();
+            if (l.col(0) < a.C)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float *f = which ? &db[0][4 * h] : &dw[0][4 * h];
+                    meet[l.slot * n4 + l.tid * 2 + h] = float4{f[0], f[1], f[2], f[3]};
+                }
+            __syncthreads();
+            for (int i = threadIdx.x; i < n4; i += blockDim.x) {
+                float4 q = meet[i];
+                for (int k = 1; k < l.R; k++) {
+                    const float4 o = meet[k * n4 + i];
+                    q.x += o.x, q.y += o.y, q.z += o.z, q.w += o.w;
+                }
+                *(float4 *)(out + i * 4) = q;
+            }
+        }
     }
 }
 
@@ -149,8 +371,7 @@ __global__ __launch_bounds__(64) void norm_dw_kernel(BwdArgs a) {
     if (c >= a.C) return;
     for (int64_t g = blockIdx.y; g < a.groups; g += gridDim.y) {
         float dw = 0.0f, db = 0.0f;
-        const int64_t t1 = min((g + 1) * a.per, a.T);
-        for (int64_t t = g * a.per; t < t1; t++) {
+        for (int64_t t = g; t < a.T; t += a.groups) {
             const float2 st = *(const float2 *)(a.stats + 2 * t);
             const float x = load1<SD>((const char *)a.S + (t * a.lds + c) * esize<SD>());
             const float d = load1<DY>((const char *)a.dY + (t * a.lddy + c) * esize<DY>());
@@ -162,17 +383,23 @@ __global__ __launch_bounds__(64) void norm_dw_kernel(BwdArgs a) {
     }
 }
 
-// The groups' sums, in order.
-__global__ __launch_bounds__(64) void norm_dw_sum_kernel(const float *part, int64_t groups, int C, float *dw, float *db) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= C) return;
-    double s = 0.0, u = 0.0;
-    for (int64_t g = 0; g < groups; g++) {
-        s += part[(g * 2) * C + c];
-        u += part[(g * 2 + 1) * C + c];
+// The groups' sums: 32 columns a workgroup, of [2][C]; eight strands of groups, each in
+// order, then the strands.
+__global__ __launch_bounds__(256) void norm_dw_sum_kernel(const float *part, int groups, int C, float *dw, float *db) {
+    __shared__ double sh[8][32];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    double s = 0.0;
+    if (c < 2 * C) {
+#pragma unroll 8
+        for (int g = y; g < groups; g += 8) s += part[(int64_t)g * 2 * C + c];
     }
-    if (dw) dw[c] = (float)s;
-    if (db) db[c] = (float)u;
+    sh[y][x] = s;
+    __syncthreads();
+    if (y != 0 || c >= 2 * C) return;
+#pragma unroll
+    for (int i = 1; i < 8; i++) s += sh[i][x];
+    float *out = c < C ? dw : db;
+    if (out) out[c < C ? c : c - C] = (float)s;
 }
 
 }  // namespace ndev
@@ -191,14 +418,23 @@ int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP
 bool sizes_ok(int64_t T, int64_t C) { return T >= 0 && T <= kMaxT && C >= 0 && C <= kMaxInOut && C % 8 == 0; }
 bool stride_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0 && ld <= kMaxInOut * 8; }
 
-struct BwdPlan {
-    int64_t groups, per;   // row groups of the weight's gradient, rows of one
+// Waves of a row and eights of a lane; waves 0: rows too long for registers.
+struct RowShape {
+    int W, CV;
 };
-BwdPlan plan_bwd(int64_t T) {
-    BwdPlan p;
-    p.per = std::max<int64_t>(8, cdiv(T, 512));
-    p.groups = cdiv(T, p.per);
-    return p;
+RowShape shape_of(int64_t C) {
+    const int64_t most = ndev::kMaxWaves * 512;
+    if (C <= most) return {(int)cdiv(C, 512), 1};
+    if (C <= 2 * most) return {(int)cdiv(C, 1024), 2};
+    return {0, 0};
+}
+// rows of a workgroup of about `waves` waves
+int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std::max(s.W, 1)); }
+
+// Row groups of the backward, a workgroup each.
+int64_t groups_of(int64_t T, int64_t C) {
+    const RowShape s = shape_of(C);
+    return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(T, rows_at_once(s, ndev::kTogether))));
 }
 
 // f with a type code as a compile-time constant
@@ -207,7 +443,6 @@ void with_type(int32_t dt, F f) {
     if (dt == TERN_BF16) f(std::integral_constant<int, TERN_BF16>{});
     else f(std::integral_constant<int, TERN_F32>{});
 }
-
 }  // namespace
 }  // namespace tern
 
@@ -217,7 +452,7 @@ extern "C" {
 
 size_t tern_norm_bwd_workspace_bytes(int64_t T, int64_t C) {
     if (!sizes_ok(T, C)) return 0;
-    return (size_t)plan_bwd(T).groups * (size_t)C * 8;
+    return (size_t)groups_of(T, C) * (size_t)C * 8;
 }
 
 int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, int64_t lda, int32_t a_dtype,
@@ -239,18 +474,21 @@ int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, in
     const Mat ins[] = {{A, T, C, lda, A ? esize(a_dtype) : 0}, {w, 1, C, C, 4}, {b, 1, C, C, 4},
                        {in_place ? nullptr : X, T, C, ldx, xs}};
     if (any_overlap(outs, 3, ins, 4)) return TERN_ERR_ALIAS;
-    FwdArgs a{X, A, w, b, S, Y, stats, ldx, lda, lds, ldy, T, (int)C, eps};
+    const RowShape shape = shape_of(C);
+    FwdArgs a{X, A, w, b, S, Y, stats, ldx, lda, lds, ldy, T, (int)C, shape.W, a_dtype, eps};
     hipStream_t st = (hipStream_t)stream;
-    const dim3 grid((unsigned)std::min<int64_t>(T, 65536));
     with_type(x_dtype, [&](auto xd) {
         with_type(y_dtype, [&](auto yd) {
             constexpr int XD = decltype(xd)::value, YD = decltype(yd)::value;
-            if (!A) hipLaunchKernelGGL((ndev::norm_fwd_kernel<XD, ndev::kNone, YD>), grid, dim3(256), 0, st, a);
-            else
-                with_type(a_dtype, [&](auto ad) {
-                    constexpr int AD = decltype(ad)::value;
-                    hipLaunchKernelGGL((ndev::norm_fwd_kernel<XD, AD, YD>), grid, dim3(256), 0, st, a);
-                });
+            if (shape.W == 0) {
+                hipLaunchKernelGGL((ndev::norm_fwd_kernel<XD, YD>), dim3((unsigned)std::min<int64_t>(T, 65536)),
+                                   dim3(256), 0, st, a);
+                return;
+            }
+            const int R = rows_at_once(shape, 4);
+            const dim3 g((unsigned)std::min<int64_t>(cdiv(T, R), 2048)), bl(64 * shape.W * R);
+            if (shape.CV == 1) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1>), g, bl, 0, st, a);
+            else hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 2>), g, bl, 0, st, a);
         });
     });
     return launched();
@@ -268,8 +506,8 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
     if (C == 0) return TERN_OK;
     if (T > 0 && (!S || !stats || !dY || !dX)) return TERN_ERR_NULL;
     const bool weights = dw || db;
-    const BwdPlan p = plan_bwd(T);
-    const size_t wsb = weights ? (size_t)p.groups * (size_t)C * 8 : 0;
+    const int64_t groups = groups_of(T, C);
+    const size_t wsb = weights ? (size_t)groups * (size_t)C * 8 : 0;
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (misaligned(S) || misaligned(w) || misaligned(dY) || misaligned(dS) || misaligned(dX) || misaligned(dw) ||
         misaligned(db) || misaligned(workspace) || ((uintptr_t)stats & 7u))
@@ -283,25 +521,37 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
                        {dY, T, C, lddy, esize(dy_dtype)}, {in_place ? nullptr : dS, T, C, ldds, xs}};
     if (any_overlap(outs, 4, ins, 5)) return TERN_ERR_ALIAS;
     if (T == 0 && !weights) return TERN_OK;
-    BwdArgs a{S, dY, dS, stats, w, dX, dw, db, (float *)workspace, lds, lddy, ldds, lddx, T, p.groups, p.per, (int)C};
+    const RowShape shape = shape_of(C);
+    BwdArgs a{S, dY, dS, stats, w, dX, dw, db, weights ? (float *)workspace : nullptr, lds, lddy, ldds, lddx, T, groups,
+              (int)C, shape.W};
     hipStream_t st = (hipStream_t)stream;
     const unsigned cols = (unsigned)cdiv(C, 64);
     if (T > 0) {
-        const dim3 grid((unsigned)std::min<int64_t>(T, 65536)), gw(cols, (unsigned)std::min<int64_t>(p.groups, 65535));
         with_type(s_dtype, [&](auto sd) {
             with_type(dy_dtype, [&](auto yd) {
                 constexpr int SD = decltype(sd)::value, DY = decltype(yd)::value;
                 with_type(dx_dtype, [&](auto xd) {
                     constexpr int DX = decltype(xd)::value;
-                    if constexpr (DX == TERN_F32 || SD == TERN_BF16)
-                        hipLaunchKernelGGL((ndev::norm_dx_kernel<SD, DY, DX>), grid, dim3(256), 0, st, a);
+                    if constexpr (DX == TERN_F32 || SD == TERN_BF16) {
+                        if (shape.W == 0) {
+                            hipLaunchKernelGGL((ndev::norm_dx_kernel<SD, DY, DX>),
+                                               dim3((unsigned)std::min<int64_t>(T, 65536)), dim3(256), 0, st, a);
+                            return;
+                        }
+                        const dim3 g((unsigned)groups), bl(64 * shape.W * rows_at_once(shape, ndev::kTogether));
+                        if (shape.CV == 1)
+                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1>), g, bl, 0, st, a);
+                        else hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 2>), g, bl, 0, st, a);
+                    }
                 });
-                if (weights) hipLaunchKernelGGL((ndev::norm_dw_kernel<SD, DY>), gw, dim3(64), 0, st, a);
+                if (weights && shape.W == 0)
+                    hipLaunchKernelGGL((ndev::norm_dw_kernel<SD, DY>), dim3(cols, (unsigned)groups), dim3(64), 0, st, a);
             });
         });
     }
     if (weights)
-        hipLaunchKernelGGL(ndev::norm_dw_sum_kernel, dim3(cols), dim3(64), 0, st, a.part, p.groups, a.C, dw, db);
+        hipLaunchKernelGGL(ndev::norm_dw_sum_kernel, dim3((unsigned)cdiv(2 * C, 32)), dim3(256), 0, st, a.part,
+                           T > 0 ? (int)groups : 0, a.C, dw, db);
     return launched();
 }
 

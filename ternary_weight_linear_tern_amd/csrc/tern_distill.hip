@@ -8,7 +8,8 @@
 // from the same registers, so that Z is read once and dZ written once.  The few
 // elements that have a target or a teacher's probability to lose are written again,
 // whole, by the wave that wrote them before.  Where one softmax serves both parts
-// (tau = 1, or only one part) each element takes one exponential a pass, else two.
+// (tau = 1, or only one part) each element takes one exponential a pass; where tau is
+// 2, exp(Z - m) is the square of the other; else two.
 //
 // Rows that are cut (few rows, or longer than a workgroup's registers) take two
 // launches: the segments' sums, and the logits of the named tokens, which dZ may
@@ -102,22 +103,48 @@ __device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z
     }
 }
 
-// sums of exponentials: of Z - m (s1) and of (Z - m) / tau (st); where one serves both
-// parts, it is st that is taken with the exponent's factor c
+// How many exponentials an element takes: one softmax, two of which one is the square
+// of the other, or two.
+enum Kind { kOne, kSquare, kTwo };
+
+// A row's exponents: of (Z - m) / tau, or of the one softmax there is, and of Z - m.
+struct Exponents {
+    Exponent t, one;
+    float m0;
+    bool far;
+    __device__ Exponents(float m, float ct, float c1, Kind kind) : t(m, ct), one(m, c1), m0(m) {
+        far = t.far || (kind == kTwo && one.far);
+    }
+};
+
+// A lane's sums of exponentials: of Z - m (s1) and of (Z - m) / tau (st); where there is
+// one softmax, st is its.
 template <int DT, int W, int NV>
-__device__ inline void sums_of(Raw8<DT> (&x)[NV], int n, float m0, float c, float c1, bool two, float &s1,
-                               float &st) {
+__device__ inline void sums_of(const char *z, const Raw8<DT> (&x)[NV], int n, const Exponents &e, Kind kind, int tid,
+                               float &s1, float &st) {
     s1 = 0.0f, st = 0.0f;
-    each8<DT, W, NV>(x, n, [&](int, const float *f) {
-        float d[8];
+    if (!e.far) {
+        each8<DT, W, NV>(x, n, [&](int, const float *f) {
+            float p[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) d[j] = f[j] - m0;   // no product of a large logit, which could overflow
+            for (int j = 0; j < 8; j++) st += p[j] = exp2_(e.t.of(f[j]));
+            if (kind == kSquare)
 #pragma unroll
-        for (int j = 0; j < 8; j++) st += exp2_(d[j] * c);
-        if (two)
+                for (int j = 0; j < 8; j++) s1 = fmaf(p[j], p[j], s1);
+            if (kind == kTwo)
 #pragma unroll
-            for (int j = 0; j < 8; j++) s1 += exp2_(d[j] * c1);
-    });
+                for (int j = 0; j < 8; j++) s1 += exp2_(e.one.of(f[j]));
+        });
+        // the exponents were `off` too large
+        s1 *= exp2_(kind == kSquare ? -2.0f * e.t.off : -e.one.off);
+        st *= exp2_(-e.t.off);
+    } else {
+        for (int v = fresh(tid); v < n; v += W * 64) {
+            const float d = at<DT>(z, v) - e.m0;
+            st += exp2_(d * e.t.c);
+            s1 += exp2_(d * e.one.c);
+        }
+    }
 }
 
 struct Sums {
@@ -140,40 +167,60 @@ __device__ inline void write_loss(const DistillArgs &a, int64_t t, const Names &
 
 // the gradient of a segment's n elements, of which `first` is the row's index of the first
 template <int DT, int W, int NV>
-__device__ inline void write_grad(const DistillArgs &a, int64_t t, Raw8<DT> (&x)[NV], int first, int n,
-                                  const Names &e, const Sums &s, float c, bool two, int tid) {
+__device__ inline void write_grad(const DistillArgs &a, int64_t t, const char *z, const Raw8<DT> (&x)[NV], int first,
+                                  int n, const Names &e, const Sums &s, float c, Kind kind, int tid) {
     constexpr int ST = W * 512, ES = esize<DT>();
     const float w = a.dloss ? a.dloss[t] : 1.0f;
     char *dz = (char *)a.dZ + (t * a.lddz + first) * ES;
     const bool zero = w == 0.0f || !(e.kl || e.ce);
     float f1 = e.ce && s.s1 != 0.0f ? w * a.alpha / s.s1 : 0.0f;
     float ft = e.kl && s.st != 0.0f ? w * (1.0f - a.alpha) * a.tau / s.st : 0.0f;
-    if (!two) ft += f1;
+    if (kind == kOne) ft += f1;
     const int full = n & ~7, l = fresh(tid);
-    const uint32_t off = (uint32_t)l * (8 * ES);
-    float last[8] = {};   // of the stride with the last, partial eight
-    each8<DT, W, NV>(x, n, [&](int i, const float *f) {
-        float d[8], g[8];
+    const Exponents x2(s.m0, c, a.c1, kind);
+    if (zero || x2.far) {
+        // element by element, in the places of the pass below (a row of zeros takes nothing from Z)
+        for (int v0 = l * 8; v0 < n; v0 += ST)
+            for (int v = v0; v < min(v0 + 8, n); v++) {
+                float g = 0.0f;
+                if (!zero) {
+                    const float d = at<DT>(z, v) - s.m0;
+                    g = ft * exp2_(d * c);
+                    if (kind != kOne) g = fmaf(f1, exp2_(d * a.c1), g);
+                }
+                store1<DT>(dz + (int64_t)v * ES, g);
+            }
+        if (zero) return;
+    } else {
+        // the factors take off what the exponents are too large by
+        const float ht = ft * exp2_(-x2.t.off);
+        const float h1 = f1 * exp2_(kind == kSquare ? -2.0f * x2.t.off : -x2.one.off);
+        const uint32_t off = (uint32_t)l * (8 * ES);
+        float last[8] = {};   // of the stride with the last, partial eight
+        each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+            float g[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) d[j] = f[j] - s.m0;
+            for (int j = 0; j < 8; j++) g[j] = exp2_(x2.t.of(f[j]));
+            if (kind == kSquare) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) g[j] = ft * exp2_(d[j] * c);
-        if (two)
+                for (int j = 0; j < 8; j++) g[j] *= fmaf(h1, g[j], ht);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; j++) g[j] = fmaf(f1, exp2_(d[j] * a.c1), g[j]);
-        if (zero)
+                for (int j = 0; j < 8; j++) g[j] *= ht;
+                if (kind == kTwo)
 #pragma unroll
-            for (int j = 0; j < 8; j++) g[j] = 0.0f;
-        if (l * 8 < full - i * ST) store8<DT>(dz + i * ST * ES + off, pack8<DT>(g));
-        if (i == full / ST)
+                    for (int j = 0; j < 8; j++) g[j] = fmaf(h1, exp2_(x2.one.of(f[j])), g[j]);
+            }
+            if (l * 8 < full - i * ST) store8<DT>(dz + i * ST * ES + off, pack8<DT>(g));
+            if (i == full / ST)
 #pragma unroll
-            for (int j = 0; j < 7; j++) last[j] = g[j];
-    });
-    if (n & 7 && l == full % ST / 8)
+                for (int j = 0; j < 7; j++) last[j] = g[j];
+        });
+        if (n & 7 && l == full % ST / 8)
 #pragma unroll
-        for (int j = 0; j < 7; j++)
-            if (full + j < n) store1<DT>(dz + (int64_t)full * ES + j * ES, last[j]);
-    if (zero) return;
+            for (int j = 0; j < 7; j++)
+                if (full + j < n) store1<DT>(dz + (int64_t)full * ES + j * ES, last[j]);
+    }
     // the named tokens, by the wave that has just written them
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     const int lane = tid & 63, wave = tid >> 6;
@@ -184,7 +231,7 @@ __device__ inline void write_grad(const DistillArgs &a, int64_t t, Raw8<DT> (&x)
         if ((r == 1 && lane != 0) || e.id[j] < 0 || v < 0 || v >= n || (v / 512) % W != wave) continue;
         const float d = e.z[j] - s.m0;
         float g = ft * exp2_(d * c);
-        if (two) g = fmaf(f1, exp2_(d * a.c1), g);
+        if (kind != kOne) g = fmaf(f1, exp2_(d * a.c1), g);
         store1<DT>(dz + (int64_t)v * ES, fmaf(-w, e.less[j], g));
     }
 }
@@ -198,16 +245,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
     __shared__ float sh[3][W];
     const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x, lane = tid & 63;
     Names &e = names[slot];
-    // one exponential an element, or two
-    const bool two = a.ce && a.kl && a.tau != 1.0f;
+    const Kind kind = !(a.ce && a.kl) || a.tau == 1.0f ? kOne : a.tau == 2.0f ? kSquare : kTwo;
     const float c = a.kl ? a.ct : a.c1;
     const int64_t items = a.T * a.S;
     for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
         const int64_t t = PHASE == 0 ? item : item / a.S;
         const int s = PHASE == 0 ? 0 : (int)(item - t * a.S), first = s * a.seg, n = min(a.seg, a.V - first);
         const char *row = (const char *)a.Z + t * a.ld * esize<DT>();
+        const char *z = row + (int64_t)first * esize<DT>();
         Raw8<DT> x[NV];
-        load_row<DT, W, NV>(row + (int64_t)first * esize<DT>(), n, tid, x);
+        load_row<DT, W, NV>(z, n, tid, x);
         if (PHASE == 1) {
             // logits of the named tokens of this segment
             if (tid < 64) {
@@ -223,21 +270,21 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
         if (PHASE != 2) {
             const float m = row_all<Max, W>(lane_max<DT, W, NV>(x, n), sh[0], tid);
             q.m0 = m == -kInf ? 0.0f : m;
-            sums_of<DT, W, NV>(x, n, q.m0, c, a.c1, two, q.s1, q.st);
+            sums_of<DT, W, NV>(z, x, n, Exponents(q.m0, c, a.c1, kind), kind, tid, q.s1, q.st);
             row_sums<W>(q.s1, q.st, &sh[1], tid);
             if (PHASE == 1 && tid == 0) a.part[item] = float4{m, q.s1, q.st, 0.0f};
         } else {
             const float4 r = lane < a.S ? a.part[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
             const float m = wave_all<Max>(r.x);
             q.m0 = m == -kInf ? 0.0f : m;
-            q.s1 = two ? wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)) : 0.0f;
+            q.s1 = kind != kOne ? wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)) : 0.0f;
             q.st = wave_all<Add>(r.z * exp2_((r.x - q.m0) * c));
         }
-        if (!two) q.s1 = q.st;
+        if (kind == kOne) q.s1 = q.st;
         if (PHASE != 1) {
             meet<W>();   // the names are there
             if (a.loss && s == 0 && tid < 64) write_loss(a, t, e, q, lane);
-            if (a.dZ) write_grad<DT, W, NV>(a, t, x, first, n, e, q, c, two, tid);
+            if (a.dZ) write_grad<DT, W, NV>(a, t, z, x, first, n, e, q, c, kind, tid);
         }
         meet<W>();
     }
@@ -286,7 +333,7 @@ extern "C" {
 
 size_t tern_distill_workspace_bytes(int64_t T, int64_t V) {
     if (!row_sizes_ok(T, V)) return 0;
-    return std::max(workspace_of(plan_rows(TERN_F32, T, V), T), workspace_of(plan_rows(TERN_BF16, T, V), T));
+    return std::max(workspace_of(plan_rows(TERN_F32, T, V, 16, false), T), workspace_of(plan_rows(TERN_BF16, T, V, 16, false), T));
 }
 
 int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t V, const int64_t *targets, int32_t K,
@@ -299,7 +346,7 @@ int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t 
         return TERN_ERR_VALUE;
     if (T == 0 || (!loss && !dZ)) return TERN_OK;
     if (!Z || (K > 0 && (!teacher_ids || !teacher_logp))) return TERN_ERR_NULL;
-    const RowPlan p = plan_rows(z_dtype, T, V);
+    const RowPlan p = plan_rows(z_dtype, T, V, 16, false);
     const size_t wsb = workspace_of(p, T);
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (off_by(Z, 16) || off_by(dZ, 16) || off_by(targets, 8) || off_by(teacher_ids, 8) || off_by(teacher_logp, 4) ||

@@ -8,10 +8,14 @@
 // The k largest: 256 groups of lanes (64 where one wave has the row) know their
 // own largest element.  The k-th largest of those is a bound that at least k
 // elements reach, and hardly more do; a bisection over its bits by one wave finds
-// it.  The elements that reach it go to a list in shared memory, and each one's
-// place is the number of greater keys there.  Rows whose list would overflow (ties,
-// rows in which fewer than k tokens are allowed) are taken one alternative after
-// the other.
+// it.  The eights that hold an element which reaches it go to a list in shared
+// memory, their elements that do to another, and each one's place is the
+// number of greater keys there.  Rows whose lists would overflow (ties, rows in
+// which fewer than k tokens are allowed) are taken one alternative after the other.
+//
+// A row longer than a workgroup's registers is taken in segments, one after the
+// other (the sums rescaled, the alternatives so far a bound for the next); where
+// the rows are few, by workgroups that a second launch joins.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,24 +30,27 @@ struct LogprobArgs {
     const void *Z;
     int64_t ld, T;
     int V, k, S;
-    int seg;
+    int part, seg;             // elements of a workgroup's part of a row, of a segment of it
     float scale, c;            // c = scale log2 e
     const int64_t *tokens;
     float *logp, *entropy, *lse;
     int64_t *top_ids;
     float *top_logp;
-    float4 *part;              // [T][S]: largest logit, s, u of a segment
+    float4 *sums;              // [T][S]: largest logit, s, u of a part
     uint64_t *keys;            // [T][S][k]: its alternatives, 0 behind the last
 };
 
-template <int W>
+template <int DT, int W>
 struct Pick {
-    static constexpr int kGroups = W >= 4 ? 256 : 64, kRoom = W >= 4 ? 1024 : 256;
-    uint64_t key[kRoom];
+    static constexpr int kGroups = W >= 4 ? 256 : 64, kKeys = W >= 4 ? 1024 : 256, kEights = W >= 4 ? 512 : 128;
+    uint64_t top[TERN_TOP_MAX];    // the largest so far, falling
+    uint64_t key[kKeys];
+    Raw8<DT> eight[kEights];
+    int from[kEights];             // index of an eight's first element in its segment
     uint64_t round[2][W];
     uint32_t group[kGroups];
     uint32_t bound;
-    int count;
+    int keys, eights;
 };
 
 struct MaxU {
@@ -102,50 +109,66 @@ __device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
     return lo;
 }
 
-// The k largest of the n elements from z on (k <= n), which x holds, `first` the index
-// of the first: put(place, key) for each.
-template <int DT, int W, int NV, class Put>
-__device__ inline void top_keys(const char *z, Raw8<DT> (&x)[NV], int n, uint32_t first, int k, float mine, Pick<W> &p, int tid,
-                                Put put) {
-    constexpr int G = Pick<W>::kGroups, PER = W * 64 / G, ST = W * 512;
+// The k largest (fewer where there are not so many) of the segment in x, n elements
+// of which `first` is the first's index, and of the `had` that p.top holds already:
+// to p.top.  Says how many there are, or -1 where a list would overflow.
+template <int DT, int W, int NV>
+__device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t first, int k, int had, float mine,
+                                     Pick<DT, W> &p, int tid) {
+    using P = Pick<DT, W>;
+    constexpr int G = P::kGroups, PER = W * 64 / G, ST = W * 512;
+    tid = fresh(tid);
     float m = mine;
     if constexpr (PER >= 2) m = fmaxf(m, dpp<0xB1>(m));
     if constexpr (PER >= 4) m = fmaxf(m, dpp<0x4E>(m));
     if (tid % PER == 0) p.group[tid / PER] = ordered(m);
-    if (tid == 0) p.count = 0;
+    if (tid == 0) p.keys = had, p.eights = 0;
+    for (int i = tid; i < had; i += W * 64) p.key[i] = p.top[i];
     meet<W>();
     if (tid < 64) {
-        const uint32_t b = bound_of<G>(p.group, k, tid);
+        uint32_t b = bound_of<G>(p.group, k, tid);
+        if (had == k) b = max(b, (uint32_t)(p.top[k - 1] >> 32));
         if (tid == 0) p.bound = b;
     }
     meet<W>();
     const float bound = from_ordered(p.bound);   // of 0: NaN, below which nothing is
     if (__ballot(!(mine < bound))) {
-        const int lane = fresh(tid);
         each8<DT, W, NV>(x, n, [&](int i, const float *f) {
             if (max8(f) < bound) return;
-            const int v = i * ST + lane * 8;
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                if (!(f[j] < bound) && v + j < n) {
-                    const int at = atomicAdd(&p.count, 1);
-                    if (at < Pick<W>::kRoom) p.key[at] = key_of(f[j], first + v + j);
-                }
+            const int at = atomicAdd(&p.eights, 1);
+            if (at < P::kEights) p.eight[at] = x[i], p.from[at] = i * ST + tid * 8;
         });
     }
     meet<W>();
-    const int count = p.count;
-    if (count >= k && count <= Pick<W>::kRoom) {
-        for (int q = tid; q < count; q += W * 64) {
-            const uint64_t key = p.key[q];
-            int place = 0;
-            for (int i = 0; i < count; i++) place += p.key[i] > key;
-            if (place < k) put(place, key);
+    const int eights = p.eights;
+    if (eights > P::kEights) return -1;
+    for (int q = tid; q < eights * 8; q += W * 64) {
+        const int v = p.from[q >> 3] + (q & 7);
+        const float f = at<DT>((const char *)&p.eight[q >> 3], q & 7);
+        if (!(f < bound) && v < n) {
+            const int at = atomicAdd(&p.keys, 1);
+            if (at < P::kKeys) p.key[at] = key_of(f, first + v);
         }
-        return;
     }
-    // one after the other: each lane keeps its largest key below the last one taken
-    // (of the row in memory, which the caches hold: a rare way needs no registers)
+    meet<W>();
+    const int keys = p.keys, want = min(k, had + n);
+    if (keys > P::kKeys || keys < want) return -1;
+    for (int q = tid; q < keys; q += W * 64) {
+        const uint64_t key = p.key[q];
+        int place = 0;
+#pragma unroll 8
+        for (int i = 0; i < keys; i++) place += p.key[i] > key;
+        if (place < k) p.top[place] = key;
+    }
+    meet<W>();
+    return want;
+}
+
+// The same of n elements in memory, one after the other: each lane keeps its largest
+// below the last one taken.
+template <int DT, int W>
+__device__ inline void top_by_turns(const char *z, int n, uint32_t first, int k, Pick<DT, W> &p, int tid) {
+    tid = fresh(tid);
     uint64_t last = ~(uint64_t)0, best = 0;
     for (int r = 0; r < k; r++) {
         if (best == last || r == 0) {
@@ -162,8 +185,9 @@ __device__ inline void top_keys(const char *z, Raw8<DT> (&x)[NV], int n, uint32_
             for (int i = 0; i < W; i++) top = max(top, p.round[r & 1][i]);
         }
         last = top;
-        if (tid == 0) put(r, top);
+        if (tid == 0) p.top[r] = top;
     }
+    meet<W>();
 }
 
 // what a row's sums say
@@ -187,56 +211,87 @@ __device__ inline void token_of(const LogprobArgs &a, int64_t t, const RowEnd &r
     a.logp[t] = y >= 0 && y < a.V ? r.log_p(at<DT>((const char *)a.Z + t * a.ld * esize<DT>(), y)) : 0.0f;
 }
 
+// s = sum e, u = sum e d over a lane's elements, m0 the segment's largest
+template <int DT, int W, int NV>
+__device__ inline void lane_sums(const char *z, const Raw8<DT> (&x)[NV], int n, float m0, const Exponent &e, int tid, float &s,
+                                 float &u) {
+    s = u = 0.0f;
+    auto add = [&](float d) {
+        const float p = exp2_(d);
+        s += p;
+        u = fmaf(p, fmaxf(d, -200.0f), u);   // (-inf: p is 0)
+    };
+    if (!e.far) {
+        each8<DT, W, NV>(x, n, [&](int, const float *f) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) add(e.of(f[j]));
+        });
+    } else {
+        for (int v = fresh(tid); v < n; v += W * 64) add((at<DT>(z, v) - m0) * e.c);
+    }
+}
+
 template <int DT, int W, int NV>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(LogprobArgs a) {
     constexpr int R = W == 1 ? 4 : 1;   // rows of a workgroup
-    __shared__ Pick<W> picks[R];
+    __shared__ Pick<DT, W> picks[R];
     __shared__ float sh[3][W];
     const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x;
-    Pick<W> &pick = picks[slot];
+    Pick<DT, W> &pick = picks[slot];
     const int64_t items = a.T * a.S;
     for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
         const int64_t t = a.S == 1 ? item : item / a.S;
-        const int s = (int)(item - t * a.S), first = s * a.seg, n = min(a.seg, a.V - first);
-        const char *z = (const char *)a.Z + (t * a.ld + first) * esize<DT>();
-        Raw8<DT> x[NV];
-        load_row<DT, W, NV>(z, n, tid, x);
-        const float mine = lane_max<DT, W, NV>(x, n);
-        const float m = row_all<Max, W>(mine, sh[0], tid), m0 = m == -kInf ? 0.0f : m;
-        float sum = 0.0f, u = 0.0f;
-        each8<DT, W, NV>(x, n, [&](int, const float *f) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                // from the largest on: no product of a large logit, which could overflow
-                const float d = (f[j] - m0) * a.c, e = exp2_(d);
-                sum += e;
-                u = fmaf(e, fmaxf(d, -200.0f), u);   // (-inf: e is 0)
+        const int begin = (int)(item - t * a.S) * a.part, end = min(begin + a.part, a.V);
+        const char *row = (const char *)a.Z + t * a.ld * esize<DT>();
+        float M = -kInf, s = 0.0f, u = 0.0f;   // of the segments so far
+        int had = 0;
+        for (int first = begin; first < end; first += a.seg) {
+            const int n = min(a.seg, end - first);
+            const char *z = row + (int64_t)first * esize<DT>();
+            Raw8<DT> x[NV];
+            load_row<DT, W, NV>(z, n, tid, x);
+            const float mine = lane_max<DT, W, NV>(x, n);
+            const float m = row_all<Max, W>(mine, sh[0], tid), m0 = m == -kInf ? 0.0f : m;
+            const Exponent e(m0, a.c);
+            float s1, u1;
+            lane_sums<DT, W, NV>(z, x, n, m0, e, tid, s1, u1);
+            row_sums<W>(s1, u1, &sh[1], tid);
+            if (!e.far) {   // the exponents were e.off too large
+                const float f = exp2_(-e.off);
+                u1 = fmaf(-e.off, s1, u1) * f;
+                s1 *= f;
             }
-        });
-        row_sums<W>(sum, u, &sh[1], tid);
+            // to the larger of the two largest
+            const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both;
+            const float d0 = (M - b0) * a.c, d1 = (m - b0) * a.c, f0 = exp2_(d0), f1 = exp2_(d1);
+            u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
+            s = f0 * s + f1 * s1;
+            M = both;
+            if (a.k && had >= 0) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);
+            meet<W>();
+        }
+        if (had < 0) {
+            top_by_turns<DT, W>(row + (int64_t)begin * esize<DT>(), end - begin, begin, min(a.k, end - begin), pick, tid);
+            had = min(a.k, end - begin);
+        }
+        const int l = fresh(tid);
         if (a.S == 1) {
-            const RowEnd r = finish_row(a, t, m0, sum, u, tid);
-            token_of<DT>(a, t, r, tid);
-            if (a.k)
-                top_keys<DT, W, NV>(z, x, n, 0, a.k, mine, pick, tid, [&](int place, uint64_t key) {
-                    a.top_ids[t * a.k + place] = index_of(key);
-                    a.top_logp[t * a.k + place] = r.log_p(value_of(key));
-                });
-        } else {
-            if (tid == 0) a.part[item] = float4{m, sum, u, 0.0f};
-            if (a.k) {
-                uint64_t *out = a.keys + item * a.k;
-                const int k = min(a.k, n);
-                for (int i = k + tid; i < a.k; i += W * 64) out[i] = 0;
-                top_keys<DT, W, NV>(z, x, n, first, k, mine, pick, tid, [&](int place, uint64_t key) { out[place] = key; });
+            const RowEnd r = finish_row(a, t, M == -kInf ? 0.0f : M, s, u, l);
+            token_of<DT>(a, t, r, l);
+            if (l < a.k) {
+                a.top_ids[t * a.k + l] = index_of(pick.top[l]);
+                a.top_logp[t * a.k + l] = r.log_p(value_of(pick.top[l]));
             }
+        } else {
+            if (l == 0) a.sums[item] = float4{M, s, u, 0.0f};
+            if (l < a.k) a.keys[item * a.k + l] = l < had ? pick.top[l] : 0;
         }
         meet<W>();
     }
 }
 
-// Rows that were cut: the segments' sums meet, and their alternatives.  Each
-// segment's keys fall, so that with r = ceil(k / S) the smallest of their r-th is
+// Rows that were cut: the parts' sums meet, and their alternatives.  Each
+// part's keys fall, so that with r = ceil(k / S) the smallest of their r-th is
 // reached by k at least.
 template <int DT>
 __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
@@ -244,7 +299,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float4 q = lane < a.S ? a.part[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
+        float4 q = lane < a.S ? a.sums[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
         const float m = wave_all<Max>(q.x), m0 = m == -kInf ? 0.0f : m;
         const float d = (q.x - m0) * a.c, f = exp2_(d);
         const float s = wave_all<Add>(f * q.y), u = wave_all<Add>(f * fmaf(q.y, fmaxf(d, -200.0f), q.z));
@@ -267,6 +322,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
         for (int i = tid; i < n; i += 256) {
             const uint64_t key = list[i];
             int place = 0;
+#pragma unroll 8
             for (int j = 0; j < n; j++) place += list[j] > key;
             if (place < a.k) {
                 a.top_ids[t * a.k + place] = index_of(key);
@@ -284,6 +340,11 @@ namespace {
 using hdev::LogprobArgs;
 
 int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP; }
+
+// Segments of four waves, so that four workgroups share a compute unit and one loads
+// while others compute.  (4096 rows of 131072 bf16, 64 alternatives: 252 us with 4
+// waves, 287 with 8, 361 with 16.)
+RowPlan plan_parts(int32_t dt, int64_t T, int64_t V) { return plan_rows(dt, T, V, 4, true); }
 
 size_t workspace_of(const RowPlan &p, int64_t T, int32_t k) {
     return p.S == 1 ? 0 : (size_t)T * (size_t)p.S * (16 + 8 * (size_t)k);
@@ -318,7 +379,7 @@ extern "C" {
 
 size_t tern_logprob_workspace_bytes(int64_t T, int64_t V, int32_t k) {
     if (!row_sizes_ok(T, V) || k < 0 || k > TERN_TOP_MAX) return 0;
-    return std::max(workspace_of(plan_rows(TERN_F32, T, V), T, k), workspace_of(plan_rows(TERN_BF16, T, V), T, k));
+    return std::max(workspace_of(plan_parts(TERN_F32, T, V), T, k), workspace_of(plan_parts(TERN_BF16, T, V), T, k));
 }
 
 int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_t T, int64_t V, const int64_t *tokens,
@@ -329,7 +390,7 @@ int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_
     if (!factor_ok(scale) || k < 0 || k > TERN_TOP_MAX || k > V) return TERN_ERR_VALUE;
     if (T == 0) return TERN_OK;
     if (!Z || !tokens != !logp || (k > 0 && (!top_ids || !top_logp))) return TERN_ERR_NULL;
-    const RowPlan p = plan_rows(z_dtype, T, V);
+    const RowPlan p = plan_parts(z_dtype, T, V);
     const size_t wsb = workspace_of(p, T, k);
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (off_by(Z, 16) || off_by(tokens, 8) || off_by(top_ids, 8) || off_by(logp, 4) || off_by(entropy, 4) ||
@@ -339,9 +400,9 @@ int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_
                         vec(top_logp, T * k, 4), vec(workspace, (int64_t)wsb, 1)};
     const Mat ins[] = {{Z, T, V, ld, (size_t)(z_dtype == TERN_BF16 ? 2 : 4)}, vec(tokens, T, 8)};
     if (any_overlap(outs, 6, ins, 2)) return TERN_ERR_ALIAS;
-    LogprobArgs a{Z, ld, T, (int)V, k, p.S, (int)p.seg, scale, (float)(scale * rows::kLog2e), tokens, logp, entropy, lse,
+    LogprobArgs a{Z, ld, T, (int)V, k, p.S, (int)p.part, (int)p.seg, scale, (float)(scale * rows::kLog2e), tokens, logp, entropy, lse,
                   top_ids, top_logp, (float4 *)workspace, nullptr};
-    if (p.S > 1) a.keys = (uint64_t *)(a.part + T * p.S);
+    if (p.S > 1) a.keys = (uint64_t *)(a.sums + T * p.S);
     hipStream_t st = (hipStream_t)stream;
     if (z_dtype == TERN_BF16) run<TERN_BF16>(a, p, st);
     else run<TERN_F32>(a, p, st);

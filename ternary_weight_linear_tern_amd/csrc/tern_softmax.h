@@ -66,8 +66,14 @@ __device__ inline int fresh(int tid) {
 template <int DT, int W, int NV>
 __device__ inline void load_row(const char *z, int n, int tid, Raw8<DT> (&x)[NV]) {
     constexpr int ST = W * 512, ES = esize<DT>();
+    tid = fresh(tid);
     const int full = n & ~7;
     const uint32_t lane = (uint32_t)tid * (8 * ES);
+    if (n == NV * ST) {   // every lane has all its eights
+#pragma unroll
+        for (int i = 0; i < NV; i++) x[i] = load8<DT>(z + i * ST * ES + lane);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         x[i] = none8<DT>();
@@ -96,27 +102,43 @@ __device__ inline float max8(const float *f) {
     return max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
 }
 
-// A pass over the registers: f(i, eight elements) of each stride that the row
-// reaches.  An eight is opaque to the compiler at its turn, and nothing moves
-// across turns: it would keep the unpacked elements of one pass for the next, and
-// unpack all of them first, at twice the registers.
-template <int DT, int W, int NV, class F>
-__device__ inline void each8(Raw8<DT> (&x)[NV], int n, F f) {
+// unpack8 that the compiler does not see through: it would keep the unpacked
+// elements, or the exponentials, of one pass over the registers for the next, at
+// twice the registers.  (The registers themselves are not made opaque: passes under
+// a condition would then leave two versions of them.)
+template <int DT>
+__device__ inline void unpack8_again(const Raw8<DT> &r, float *f) {
 #pragma unroll
-    for (int i = 0; i < NV; i++)
-        if (i * W * 512 < n) {
-#pragma unroll
-            for (int j = 0; j < Raw8<DT>::N; j++) asm volatile("" : "+v"(x[i].v[j]));
-            float e[8];
-            unpack8<DT>(x[i], e);
-            f(i, e);
-            __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < 8; i++) {
+        if constexpr (DT == TERN_BF16) {
+            const uint32_t w = r.v[0][i >> 1];
+            if (i & 1) asm volatile("v_and_b32 %0, 0xffff0000, %1" : "=v"(f[i]) : "v"(w));
+            else asm volatile("v_lshlrev_b32 %0, 16, %1" : "=v"(f[i]) : "v"(w));
+        } else {
+            const uint32_t w = r.v[i >> 2][i & 3];
+            asm volatile("v_mov_b32 %0, %1" : "=v"(f[i]) : "v"(w));
         }
+    }
+}
+
+// A pass over the registers: f(i, eight elements) of each stride that the row
+// reaches; nothing moves across turns, or all would be unpacked first.
+template <int DT, int W, int NV, class F>
+__device__ inline void each8(const Raw8<DT> (&x)[NV], int n, F f) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        if (i * W * 512 < n) {
+            float e[8];
+            unpack8_again<DT>(x[i], e);
+            f(i, e);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // A lane's largest element (NaN loses against a number).
 template <int DT, int W, int NV>
-__device__ inline float lane_max(Raw8<DT> (&x)[NV], int n) {
+__device__ inline float lane_max(const Raw8<DT> (&x)[NV], int n) {
     float m = -kInf;
     each8<DT, W, NV>(x, n, [&](int, const float *f) {
         m = max3(max3(m, f[0], f[1]), max3(f[2], f[3], f[4]), max3(f[5], f[6], f[7]));
@@ -162,6 +184,19 @@ __device__ inline uint64_t key_of(float f, uint32_t i) { return (uint64_t)ordere
 __device__ inline int index_of(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 __device__ inline float value_of(uint64_t key) { return from_ordered((uint32_t)(key >> 32)); }
 
+// The exponents of a row, in units of log 2: (z - m0) c by one fused multiply-add,
+// from m0 c as rounded, which is `off` less than it should be.  Where m0 c is so large
+// that this would matter, or overflow, `far` says that the row takes its differences
+// first, element by element.
+struct Exponent {
+    float c, mc, off;
+    bool far;
+    __device__ Exponent(float m0, float factor) : c(factor), mc(m0 * factor), off(fmaf(m0, factor, -mc)) {
+        far = !(fabsf(mc) < 1048576.0f);
+    }
+    __device__ float of(float z) const { return fmaf(z, c, -mc); }
+};
+
 template <int DT>
 __device__ inline float at(const char *z, int64_t v) { return load1<DT>(z + v * esize<DT>()); }
 
@@ -176,23 +211,25 @@ constexpr int held(int32_t dt) { return dt == TERN_BF16 ? 16 : 8; }
 constexpr int kMaxSegments = 64;
 
 struct RowPlan {
-    int S, W, NV;    // segments of a row; waves of a segment and eights of a lane
-    int64_t seg;     // elements of a segment (the last may have fewer)
+    int S, W, NV;        // parts of a row, a workgroup (or wave) each; its waves, and eights of a lane
+    int64_t part, seg;   // elements of a part, and of the segments that it takes in turn
 };
 
 inline int64_t cdiv_(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Whole rows where there are enough of them (one launch, and a gradient that
-// need not read its row again); few long rows are cut, so that some 512
-// workgroups share them.
-inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V) {
+// Whole rows where there are enough of them; few long rows are cut, so that some
+// 512 workgroups share them.  `most`: waves of a workgroup; in_turn: a part may take
+// several segments, else it is one.
+inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V, int most, bool in_turn) {
     const int nv = held(dt);
     RowPlan p{};
-    int64_t S = cdiv_(V, (int64_t)16 * 512 * nv);
+    const int64_t fits = (int64_t)most * 512 * nv;
+    int64_t S = in_turn ? 1 : cdiv_(V, fits);
     if (T < 128) S = std::max(S, std::min(cdiv_(512, std::max<int64_t>(T, 1)), cdiv_(V, 4096)));
     S = std::min<int64_t>(S, kMaxSegments);
-    p.seg = cdiv_(cdiv_(V, S), 8) * 8;
-    p.S = (int)cdiv_(V, p.seg);
+    p.part = cdiv_(cdiv_(V, S), 8) * 8;
+    p.S = (int)cdiv_(V, p.part);
+    p.seg = cdiv_(cdiv_(p.part, cdiv_(p.part, fits)), 8) * 8;
     // waves: what the registers take, and more where the rows leave the chip empty
     p.W = 1;
     for (int w : {4, 8, 16})

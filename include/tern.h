@@ -686,7 +686,8 @@ int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_
  *            Calls that may run at the same time need one each.
  * A logit of -inf has q = 0; a teacher's token with q = 0 makes the loss +inf.  A row
  * of nothing but -inf has q = 0 everywhere.  A row that holds a NaN or +inf gets NaN.
- * Sums are fp32 in a fixed order: repeated calls are bitwise identical.
+ * Sums are fp32 in a fixed order: repeated calls are bitwise identical (a call
+ * without dZ may sum in another order than one with).
  * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
  */
 size_t tern_distill_workspace_bytes(int64_t T, int64_t V);

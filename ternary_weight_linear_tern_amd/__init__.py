@@ -904,27 +904,67 @@ def empty_norm_workspace(T: int, C: int, device="cuda") -> torch.Tensor:
     return torch.empty((max(tern_norm_bwd_workspace_bytes(T, C), 16),), dtype=torch.uint8, device=device)
 
 
-def _matrix(fn, name, t, shape, dtypes) -> tuple:
-    """Address, row stride and type code of a matrix whose rows are contiguous."""
-    _shaped(fn, name, t, shape, dtypes)
-    # (the stride of rows without elements means nothing)
-    return t.data_ptr(), _row_stride(fn, name, t) if shape[1] else 0, TERN_BF16 if t.dtype is torch.bfloat16 else TERN_F32
+# As for the calls above: what is wrong is worded by the helpers, what is right takes
+# the fewest steps.  `dev` is the device of the call's first array.
+
+def _elsewhere(fn, t) -> None:
+    raise ValueError(f"{fn}: tensors on several devices (one on {t.device})")
 
 
-def _vector(fn, name, t, shape, dtypes=_F32):
-    """Address of a contiguous array (None: not given)."""
-    if t is None:
-        return None
-    _shaped(fn, name, t, shape, dtypes)
-    return _addr(t)
-
-
-def _rows_of(fn, name, t) -> tuple:
+def _first(fn, name, t) -> int:
+    """Device index of the call's first array, a matrix (-1: not on a GPU)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a tensor")
     if t.dim() != 2:
         raise ValueError(f"{fn}: {name} must have two dimensions")
-    return t.shape
+    return t.get_device()
+
+
+def _matrix(fn, name, t, shape, dtypes, dev) -> tuple:
+    """Address, row stride and type code of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a tensor")
+    dt = t.dtype
+    if dt not in dtypes or t.shape != shape:
+        _need(fn, name, t, shape, dtypes)
+    if t.get_device() != dev:
+        _elsewhere(fn, t)
+    ld, one = t.stride()
+    if one != 1 or shape[0] <= 1 or shape[1] == 0:
+        ld = _row_stride(fn, name, t) if shape[1] else 0   # (the stride of rows without elements means nothing)
+    return t.data_ptr(), ld, TERN_BF16 if dt is torch.bfloat16 else TERN_F32
+
+
+def _vector(fn, name, t, shape, dtypes, dev):
+    """Address of a contiguous array (None: not given)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype not in dtypes:
+        _need(fn, name, t, shape, dtypes)
+    if t.get_device() != dev:
+        _elsewhere(fn, t)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libtern must be contiguous")
+    return t.data_ptr()
+
+
+def _work(fn, t, dev) -> tuple:
+    """Address and bytes of a workspace (None: not given)."""
+    # (its contents mean nothing, so its type and shape do not either)
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: workspace must be a tensor or None")
+    if t.get_device() != dev:
+        _elsewhere(fn, t)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libtern must be contiguous")
+    return t.data_ptr(), t.nbytes
+
+
+def _on_gpu(fn, dev, t) -> None:
+    if dev < 0:
+        _need_device(fn, t)
 
 
 def tern_norm_fwd(X, Y, w=None, b=None, A=None, S=None, stats=None, eps: float = 1e-5, stream=None) -> None:
@@ -932,19 +972,21 @@ def tern_norm_fwd(X, Y, w=None, b=None, A=None, S=None, stats=None, eps: float =
     with A, receives the sum (it may be X: in place); stats [T, 2] the rows'
     mean and 1 / deviation for tern_norm_bwd."""
     fn = "tern_norm_fwd"
-    shape = T, C = _rows_of(fn, "X", X)
-    x, ldx, xd = _matrix(fn, "X", X, shape, _ACT)
-    y, ldy, yd = _matrix(fn, "Y", Y, shape, _ACT)
+    dev = _first(fn, "X", X)
+    shape = X.shape
+    T, C = shape
+    x, ldx, xd = _matrix(fn, "X", X, shape, _ACT, dev)
+    y, ldy, yd = _matrix(fn, "Y", Y, shape, _ACT, dev)
     a, lda, ad, s, lds = None, 0, 0, None, 0
     if A is not None or S is not None:
         if A is None or S is None:
             raise ValueError(f"{fn}: A and S are given together")
-        a, lda, ad = _matrix(fn, "A", A, shape, _ACT)
-        s, lds, _ = _matrix(fn, "S", S, shape, (X.dtype,))
-    wp, bp = _vector(fn, "w", w, (C,)), _vector(fn, "b", b, (C,))
-    st = _vector(fn, "stats", stats, (T, 2))
-    dev = _device_of(fn, X, Y, w, b, A, S, stats)
-    _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, float(eps), T, C, s, lds, y, ldy, yd, st)
+        a, lda, ad = _matrix(fn, "A", A, shape, _ACT, dev)
+        s, lds, _ = _matrix(fn, "S", S, shape, (X.dtype,), dev)
+    wp, bp = _vector(fn, "w", w, (C,), _F32, dev), _vector(fn, "b", b, (C,), _F32, dev)
+    st = _vector(fn, "stats", stats, (T, 2), _F32, dev)
+    _on_gpu(fn, dev, X)
+    _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, eps, T, C, s, lds, y, ldy, yd, st)
 
 
 def tern_norm_bwd(S, stats, dY, dX, workspace=None, w=None, dS=None, dw=None, db=None, stream=None) -> None:
@@ -952,18 +994,22 @@ def tern_norm_bwd(S, stats, dY, dX, workspace=None, w=None, dS=None, dw=None, db
     dS, the gradient that reaches S besides the norm (None: zeros; dX may be dS);
     dw and db [C] where given, which need the workspace (empty_norm_workspace)."""
     fn = "tern_norm_bwd"
-    shape = T, C = _rows_of(fn, "S", S)
-    s, lds, sd = _matrix(fn, "S", S, shape, _ACT)
-    dy, lddy, dyd = _matrix(fn, "dY", dY, shape, _ACT)
-    dx, lddx, dxd = _matrix(fn, "dX", dX, shape, (torch.float32, S.dtype))
+    dev = _first(fn, "S", S)
+    shape = S.shape
+    T, C = shape
+    s, lds, sd = _matrix(fn, "S", S, shape, _ACT, dev)
+    dy, lddy, dyd = _matrix(fn, "dY", dY, shape, _ACT, dev)
+    dx, lddx, dxd = _matrix(fn, "dX", dX, shape, (torch.float32, S.dtype), dev)
     ds, ldds = None, 0
     if dS is not None:
-        ds, ldds, _ = _matrix(fn, "dS", dS, shape, (dX.dtype,))
-    _shaped(fn, "stats", stats, (T, 2), _F32)
-    args = (s, lds, sd, _addr(stats), _vector(fn, "w", w, (C,)), dy, lddy, dyd, ds, ldds, T, C, dx, lddx, dxd,
-            _vector(fn, "dw", dw, (C,)), _vector(fn, "db", db, (C,)))
-    dev = _device_of(fn, S, stats, dY, dX, workspace, w, dS, dw, db)
-    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
+        ds, ldds, _ = _matrix(fn, "dS", dS, shape, (dX.dtype,), dev)
+    if stats is None:
+        _need(fn, "stats", stats, (T, 2), _F32)
+    st, wp = _vector(fn, "stats", stats, (T, 2), _F32, dev), _vector(fn, "w", w, (C,), _F32, dev)
+    dwp, dbp = _vector(fn, "dw", dw, (C,), _F32, dev), _vector(fn, "db", db, (C,), _F32, dev)
+    ws, n = _work(fn, workspace, dev)
+    _on_gpu(fn, dev, S)
+    _call(fn, dev, stream, s, lds, sd, st, wp, dy, lddy, dyd, ds, ldds, T, C, dx, lddx, dxd, dwp, dbp, ws, n)
 
 
 def tern_logprob_workspace_bytes(T: int, V: int, k: int = 0) -> int:
@@ -975,10 +1021,21 @@ def empty_logprob_workspace(T: int, V: int, k: int = 0, device="cuda") -> torch.
     return torch.empty((max(tern_logprob_workspace_bytes(T, V, k), 16),), dtype=torch.uint8, device=device)
 
 
-def _logits(fn, name, t, shape, dtypes) -> tuple:
-    """As _matrix, for rows of any length: what a single row's stride would be."""
-    p, ld, dt = _matrix(fn, name, t, shape, dtypes)
+def _logits(fn, name, t, shape, dtypes, dev) -> tuple:
+    """As _matrix, for rows of any length: a single row's stride is what it would be."""
+    p, ld, dt = _matrix(fn, name, t, shape, dtypes, dev)
     return p, (ld if shape[0] > 1 else -(-shape[1] // 8) * 8), dt
+
+
+def _pair(fn, ids_name, ids, lp_name, lp, T, dev) -> tuple:
+    """Number of entries a row and addresses of two [T, k] arrays that come together."""
+    if ids is None and lp is None:
+        return 0, None, None
+    if ids is None or lp is None:
+        raise ValueError(f"{fn}: {ids_name} and {lp_name} are given together")
+    _first(fn, ids_name, ids)
+    k = ids.shape[1]
+    return k, _vector(fn, ids_name, ids, (T, k), _I64, dev), _vector(fn, lp_name, lp, (T, k), _F32, dev)
 
 
 def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None,
@@ -989,18 +1046,16 @@ def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=No
     by rising index.  Rows start on 16 bytes: for a V that is no multiple of 8,
     Z is a column slice of a wider matrix."""
     fn = "tern_logprob"
-    shape = T, V = _rows_of(fn, "Z", Z)
-    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT)
-    k = 0
-    if top_ids is not None or top_logp is not None:
-        if top_ids is None or top_logp is None:
-            raise ValueError(f"{fn}: top_ids and top_logp are given together")
-        k = _rows_of(fn, "top_ids", top_ids)[1]
-    args = (z, ld, zd, float(scale), T, V, _vector(fn, "tokens", tokens, (T,), _I64), _vector(fn, "logp", logp, (T,)),
-            _vector(fn, "entropy", entropy, (T,)), _vector(fn, "lse", lse, (T,)), k,
-            _vector(fn, "top_ids", top_ids, (T, k), _I64), _vector(fn, "top_logp", top_logp, (T, k)))
-    dev = _device_of(fn, Z, workspace, tokens, logp, entropy, lse, top_ids, top_logp)
-    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
+    dev = _first(fn, "Z", Z)
+    shape = Z.shape
+    T, V = shape
+    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT, dev)
+    k, ids, lp = _pair(fn, "top_ids", top_ids, "top_logp", top_logp, T, dev)
+    tok, lt = _vector(fn, "tokens", tokens, (T,), _I64, dev), _vector(fn, "logp", logp, (T,), _F32, dev)
+    en, ls = _vector(fn, "entropy", entropy, (T,), _F32, dev), _vector(fn, "lse", lse, (T,), _F32, dev)
+    ws, n = _work(fn, workspace, dev)
+    _on_gpu(fn, dev, Z)
+    _call(fn, dev, stream, z, ld, zd, scale, T, V, tok, lt, en, ls, k, ids, lp, ws, n)
 
 
 def tern_distill_workspace_bytes(T: int, V: int) -> int:
@@ -1020,21 +1075,19 @@ def tern_distill(Z, workspace=None, targets=None, teacher_ids=None, teacher_logp
     teacher_logp [T, K] are what tern_logprob with scale = 1 / tau writes; their
     probabilities are made to sum to one."""
     fn = "tern_distill"
-    shape = T, V = _rows_of(fn, "Z", Z)
-    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT)
+    dev = _first(fn, "Z", Z)
+    shape = Z.shape
+    T, V = shape
+    z, ld, zd = _logits(fn, "Z", Z, shape, _ACT, dev)
     dz, lddz = None, 0
     if dZ is not None:
-        dz, lddz, _ = _logits(fn, "dZ", dZ, shape, (Z.dtype,))
-    K = 0
-    if teacher_ids is not None or teacher_logp is not None:
-        if teacher_ids is None or teacher_logp is None:
-            raise ValueError(f"{fn}: teacher_ids and teacher_logp are given together")
-        K = _rows_of(fn, "teacher_ids", teacher_ids)[1]
-    args = (z, ld, zd, T, V, _vector(fn, "targets", targets, (T,), _I64), K,
-            _vector(fn, "teacher_ids", teacher_ids, (T, K), _I64), _vector(fn, "teacher_logp", teacher_logp, (T, K)),
-            float(alpha), float(tau), _vector(fn, "dloss", dloss, (T,)), _vector(fn, "loss", loss, (T,)), dz, lddz)
-    dev = _device_of(fn, Z, workspace, targets, teacher_ids, teacher_logp, loss, dloss, dZ)
-    _call(fn, dev, stream, *args, _addr(workspace), _bytes_of(workspace))
+        dz, lddz, _ = _logits(fn, "dZ", dZ, shape, (Z.dtype,), dev)
+    K, ids, lp = _pair(fn, "teacher_ids", teacher_ids, "teacher_logp", teacher_logp, T, dev)
+    y, dl = _vector(fn, "targets", targets, (T,), _I64, dev), _vector(fn, "dloss", dloss, (T,), _F32, dev)
+    lo = _vector(fn, "loss", loss, (T,), _F32, dev)
+    ws, n = _work(fn, workspace, dev)
+    _on_gpu(fn, dev, Z)
+    _call(fn, dev, stream, z, ld, zd, T, V, y, K, ids, lp, alpha, tau, dl, lo, dz, lddz, ws, n)
 
 
 def tern_graph_begin(stream) -> None:

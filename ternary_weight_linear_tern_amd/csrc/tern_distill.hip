@@ -11,9 +11,10 @@
 // (tau = 1, or only one part) each element takes one exponential a pass; where tau is
 // 2, exp(Z - m) is the square of the other; else two.
 //
-// Rows that are cut (few rows, or longer than a workgroup's registers) take two
-// launches: the segments' sums, and the logits of the named tokens, which dZ may
-// overwrite; then the gradient, which reads the segments again.
+// Without dZ a row is taken in segments, one after the other, as tern_logprob takes
+// it.  Rows that are cut (few rows, or with dZ longer than a workgroup's registers)
+// take two launches: the parts' sums, and the logits of the named tokens, which dZ
+// may overwrite; then the loss and the gradient, which reads the parts again.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -32,7 +33,7 @@ struct DistillArgs {
     const void *Z;
     int64_t ld, lddz, T;
     int V, K, S;
-    int seg;
+    int part, seg;            // elements of a workgroup's part of a row, of a segment of it
     const int64_t *targets, *ids;
     const float *lp, *dloss;
     float alpha, tau;
@@ -40,7 +41,7 @@ struct DistillArgs {
     bool ce, kl;              // which parts the call has
     float *loss;
     void *dZ;
-    float4 *part;             // [T][S]: largest logit, s1, st of a segment
+    float4 *sums;             // [T][S]: largest logit, s1, st of a part
     float *named;             // [T][65]: logits of the teacher's tokens and of the target
 };
 
@@ -236,8 +237,23 @@ __device__ inline void write_grad(const DistillArgs &a, int64_t t, const char *z
     }
 }
 
-// PHASE 0: whole rows.  1: a segment's sums and the named logits.  2: the row's sums from
-// its segments', loss and gradient.
+// The row's sums from its parts', by a wave.
+__device__ inline Sums join_sums(const DistillArgs &a, int64_t t, float c, Kind kind, int lane) {
+    const float4 r = lane < a.S ? a.sums[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
+    const float m = wave_all<Max>(r.x);
+    Sums q;
+    q.m0 = m == -kInf ? 0.0f : m;
+    q.st = wave_all<Add>(r.z * exp2_((r.x - q.m0) * c));
+    q.s1 = kind == kOne ? q.st : wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1));
+    return q;
+}
+
+__device__ inline Kind kind_of(const DistillArgs &a) {
+    return !(a.ce && a.kl) || a.tau == 1.0f ? kOne : a.tau == 2.0f ? kSquare : kTwo;
+}
+
+// PHASE 0: whole rows with dZ, a segment each.  1: a part's sums and the named logits.
+// 2: the row's sums from its parts', loss and gradient.  3: whole rows without dZ.
 template <int DT, int W, int NV, int PHASE>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(DistillArgs a) {
     constexpr int R = W == 1 ? 4 : 1;   // rows of a workgroup
@@ -245,48 +261,83 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
     __shared__ float sh[3][W];
     const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x, lane = tid & 63;
     Names &e = names[slot];
-    const Kind kind = !(a.ce && a.kl) || a.tau == 1.0f ? kOne : a.tau == 2.0f ? kSquare : kTwo;
+    const Kind kind = kind_of(a);
     const float c = a.kl ? a.ct : a.c1;
     const int64_t items = a.T * a.S;
     for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
-        const int64_t t = PHASE == 0 ? item : item / a.S;
-        const int s = PHASE == 0 ? 0 : (int)(item - t * a.S), first = s * a.seg, n = min(a.seg, a.V - first);
+        const bool whole = PHASE == 0 || PHASE == 3;
+        const int64_t t = whole ? item : item / a.S;
+        const int begin = whole ? 0 : (int)(item - t * a.S) * a.part, end = min(begin + a.part, a.V);
         const char *row = (const char *)a.Z + t * a.ld * esize<DT>();
-        const char *z = row + (int64_t)first * esize<DT>();
         Raw8<DT> x[NV];
-        load_row<DT, W, NV>(z, n, tid, x);
-        if (PHASE == 1) {
-            // logits of the named tokens of this segment
-            if (tid < 64) {
-                const int64_t id = a.kl && lane < a.K ? a.ids[t * a.K + lane] : -1;
-                if (id >= first && id < first + n) a.named[t * kEntries + lane] = at<DT>(row, id);
-                const int64_t y = a.ce && lane == 0 ? a.targets[t] : -1;
-                if (y >= first && y < first + n) a.named[t * kEntries + kEntries - 1] = at<DT>(row, y);
-            }
-        } else if (tid < 64) {
-            read_names<DT>(a, t, row, e, lane, PHASE == 2);
-        }
         Sums q;
-        if (PHASE != 2) {
-            const float m = row_all<Max, W>(lane_max<DT, W, NV>(x, n), sh[0], tid);
+        auto largest_and_sums = [&](const char *z, int n, float &m, float &s1, float &st) {
+            m = row_all<Max, W>(lane_max<DT, W, NV>(x, n), sh[0], tid);
+            const float m0 = m == -kInf ? 0.0f : m;
+            sums_of<DT, W, NV>(z, x, n, Exponents(m0, c, a.c1, kind), kind, tid, s1, st);
+            row_sums<W>(s1, st, &sh[1], tid);
+        };
+        if (PHASE == 2) {
+            load_row<DT, W, NV>(row + (int64_t)begin * esize<DT>(), end - begin, tid, x);
+            if (tid < 64) read_names<DT>(a, t, row, e, lane, true);
+            q = join_sums(a, t, c, kind, lane);
+        } else if (PHASE == 0) {
+            load_row<DT, W, NV>(row, a.V, tid, x);
+            if (tid < 64) read_names<DT>(a, t, row, e, lane, false);
+            float m;
+            largest_and_sums(row, a.V, m, q.s1, q.st);
             q.m0 = m == -kInf ? 0.0f : m;
-            sums_of<DT, W, NV>(z, x, n, Exponents(q.m0, c, a.c1, kind), kind, tid, q.s1, q.st);
-            row_sums<W>(q.s1, q.st, &sh[1], tid);
-            if (PHASE == 1 && tid == 0) a.part[item] = float4{m, q.s1, q.st, 0.0f};
+            if (kind == kOne) q.s1 = q.st;
         } else {
-            const float4 r = lane < a.S ? a.part[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
-            const float m = wave_all<Max>(r.x);
-            q.m0 = m == -kInf ? 0.0f : m;
-            q.s1 = kind != kOne ? wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)) : 0.0f;
-            q.st = wave_all<Add>(r.z * exp2_((r.x - q.m0) * c));
+            float M = -kInf, s1 = 0.0f, st = 0.0f;   // of the segments so far
+            for (int first = begin; first < end; first += a.seg) {
+                const int n = min(a.seg, end - first);
+                const char *z = row + (int64_t)first * esize<DT>();
+                load_row<DT, W, NV>(z, n, tid, x);
+                if (first == begin && tid < 64) {
+                    if (PHASE == 3) {
+                        read_names<DT>(a, t, row, e, lane, false);
+                    } else {   // the logits of the tokens that are named of this part
+                        const int64_t id = a.kl && lane < a.K ? a.ids[t * a.K + lane] : -1;
+                        if (id >= begin && id < end) a.named[t * kEntries + lane] = at<DT>(row, id);
+                        const int64_t y = a.ce && lane == 0 ? a.targets[t] : -1;
+                        if (y >= begin && y < end) a.named[t * kEntries + kEntries - 1] = at<DT>(row, y);
+                    }
+                }
+                float m, p1, pt;
+                largest_and_sums(z, n, m, p1, pt);
+                // to the larger of the two largest
+                const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both, d0 = M - b0, d1 = m - b0;
+                st = fmaf(exp2_(d0 * c), st, exp2_(d1 * c) * pt);
+                if (kind != kOne) s1 = fmaf(exp2_(d0 * a.c1), s1, exp2_(d1 * a.c1) * p1);
+                M = both;
+                meet<W>();
+            }
+            q = Sums{M == -kInf ? 0.0f : M, kind == kOne ? st : s1, st};
+            if (PHASE == 1 && tid == 0) a.sums[item] = float4{M, s1, st, 0.0f};
         }
-        if (kind == kOne) q.s1 = q.st;
         if (PHASE != 1) {
             meet<W>();   // the names are there
-            if (a.loss && s == 0 && tid < 64) write_loss(a, t, e, q, lane);
-            if (a.dZ) write_grad<DT, W, NV>(a, t, z, x, first, n, e, q, c, kind, tid);
+            if (a.loss && begin == 0 && tid < 64) write_loss(a, t, e, q, lane);
+            if (PHASE != 3)
+                write_grad<DT, W, NV>(a, t, row + (int64_t)begin * esize<DT>(), x, begin, end - begin, e, q, c, kind,
+                                      tid);
+            meet<W>();
         }
-        meet<W>();
+    }
+}
+
+// The loss alone of rows that were cut: a wave each.
+template <int DT>
+__global__ __launch_bounds__(64) void distill_loss_kernel(DistillArgs a) {
+    __shared__ Names e;
+    const int lane = threadIdx.x;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        read_names<DT>(a, t, nullptr, e, lane, true);
+        const Sums q = join_sums(a, t, a.kl ? a.ct : a.c1, kind_of(a), lane);
+        meet<1>();
+        write_loss(a, t, e, q, lane);
+        meet<1>();
     }
 }
 
@@ -297,6 +348,12 @@ namespace {
 using kdev::DistillArgs;
 
 int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP; }
+
+// With dZ a part has to fit a workgroup's registers: up to 16 waves.  Without, four
+// waves take segments in turn.
+RowPlan plan_call(int32_t dt, int64_t T, int64_t V, bool grad) {
+    return plan_rows(dt, T, V, grad ? 16 : 4, !grad);
+}
 
 size_t workspace_of(const RowPlan &p, int64_t T) {
     return p.S == 1 ? 0 : (size_t)T * ((size_t)p.S * 16 + kdev::kEntries * 4);
@@ -317,11 +374,15 @@ struct Launch {
 template <int32_t DT>
 void run(const DistillArgs &a, const RowPlan &p, hipStream_t st) {
     if (a.S == 1) {
-        with_plan<DT>(p, Launch<DT, 0>{a, st});
-    } else {
-        with_plan<DT>(p, Launch<DT, 1>{a, st});
-        with_plan<DT>(p, Launch<DT, 2>{a, st});
+        if (a.dZ) with_plan<DT>(p, Launch<DT, 0>{a, st});
+        else with_plan<DT>(p, Launch<DT, 3>{a, st});
+        return;
     }
+    with_plan<DT>(p, Launch<DT, 1>{a, st});
+    if (a.dZ) with_plan<DT>(p, Launch<DT, 2>{a, st});
+    else
+        hipLaunchKernelGGL(kdev::distill_loss_kernel<DT>, dim3((unsigned)std::min<int64_t>(a.T, 1 << 21)), dim3(64), 0,
+                           st, a);
 }
 
 }  // namespace
@@ -333,7 +394,10 @@ extern "C" {
 
 size_t tern_distill_workspace_bytes(int64_t T, int64_t V) {
     if (!row_sizes_ok(T, V)) return 0;
-    return std::max(workspace_of(plan_rows(TERN_F32, T, V, 16, false), T), workspace_of(plan_rows(TERN_BF16, T, V, 16, false), T));
+    size_t most = 0;
+    for (int32_t dt : {TERN_F32, TERN_BF16})
+        for (bool grad : {false, true}) most = std::max(most, workspace_of(plan_call(dt, T, V, grad), T));
+    return most;
 }
 
 int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t V, const int64_t *targets, int32_t K,
@@ -346,7 +410,7 @@ int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t 
         return TERN_ERR_VALUE;
     if (T == 0 || (!loss && !dZ)) return TERN_OK;
     if (!Z || (K > 0 && (!teacher_ids || !teacher_logp))) return TERN_ERR_NULL;
-    const RowPlan p = plan_rows(z_dtype, T, V, 16, false);
+    const RowPlan p = plan_call(z_dtype, T, V, dZ != nullptr);
     const size_t wsb = workspace_of(p, T);
     if (wsb && (!workspace || workspace_bytes < wsb)) return TERN_ERR_WORKSPACE;
     if (off_by(Z, 16) || off_by(dZ, 16) || off_by(targets, 8) || off_by(teacher_ids, 8) || off_by(teacher_logp, 4) ||
@@ -359,10 +423,10 @@ int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t 
     const Mat ins[] = {vec(targets, T, 8), vec(teacher_ids, T * K, 8), vec(teacher_logp, T * K, 4), vec(dloss, T, 4),
                        {in_place ? nullptr : Z, T, V, ld, es}};
     if (any_overlap(outs, 3, ins, 5)) return TERN_ERR_ALIAS;
-    DistillArgs a{Z, ld, lddz, T, (int)V, K, p.S, (int)p.seg, targets, teacher_ids, teacher_logp, dloss, alpha, tau,
+    DistillArgs a{Z, ld, lddz, T, (int)V, K, p.S, (int)p.part, (int)p.seg, targets, teacher_ids, teacher_logp, dloss, alpha, tau,
                   (float)rows::kLog2e, (float)(rows::kLog2e / tau), alpha > 0.0f && targets, alpha < 1.0f && K > 0, loss,
                   dZ, (float4 *)workspace, nullptr};
-    if (p.S > 1) a.named = (float *)(a.part + T * p.S);
+    if (p.S > 1) a.named = (float *)(a.sums + T * p.S);
     hipStream_t st = (hipStream_t)stream;
     if (z_dtype == TERN_BF16) run<TERN_BF16>(a, p, st);
     else run<TERN_F32>(a, p, st);

@@ -219,23 +219,26 @@ inline int64_t cdiv_(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whole rows where there are enough of them; few long rows are cut, so that some
 // 512 workgroups share them.  `most`: waves of a workgroup; in_turn: a part may take
-// several segments, else it is one.
+// several segments, else it is one (and a gradient reads cut rows again, so that
+// they are cut only where the rows are fewer: 200 rows of 131072, 20 alternatives,
+// 36 us whole and 28 cut; 300 rows of 50021 with gradient, 25 us whole and 27 cut).
 inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V, int most, bool in_turn) {
     const int nv = held(dt);
     RowPlan p{};
     const int64_t fits = (int64_t)most * 512 * nv;
     int64_t S = in_turn ? 1 : cdiv_(V, fits);
-    if (T < 128) S = std::max(S, std::min(cdiv_(512, std::max<int64_t>(T, 1)), cdiv_(V, 4096)));
+    if (T < (in_turn ? 512 : 128)) S = std::max(S, std::min(cdiv_(512, std::max<int64_t>(T, 1)), cdiv_(V, 4096)));
     S = std::min<int64_t>(S, kMaxSegments);
     p.part = cdiv_(cdiv_(V, S), 8) * 8;
     p.S = (int)cdiv_(V, p.part);
     p.seg = cdiv_(cdiv_(p.part, cdiv_(p.part, fits)), 8) * 8;
-    // waves: what the registers take, and more where the rows leave the chip empty
+    // waves: what the registers take, and four where single ones leave the chip empty
+    // (16 waves where 4 do cost more than they give: 300 rows of 50021, 20 alternatives,
+    // 29 us with 16 and 20 with 4)
     p.W = 1;
     for (int w : {4, 8, 16})
         if ((int64_t)p.W * 512 * nv < p.seg) p.W = w;
-    for (int w : {4, 16})
-        if (w > p.W && T * p.S * p.W < 2048 && (int64_t)p.W * 512 < p.seg) p.W = w;
+    if (p.W == 1 && T * p.S < 2048 && p.seg > 512) p.W = 4;
     p.NV = nv;
     for (int v : {4, 1})
         if ((int64_t)p.W * 512 * v >= p.seg) p.NV = v;
@@ -261,8 +264,7 @@ void with_plan(const RowPlan &p, F f) {
         f.template operator()<8, H>();
         break;
     default:
-        if (big) f.template operator()<16, H>();
-        else f.template operator()<16, 4>();
+        f.template operator()<16, H>();
     }
 }
 

@@ -45,7 +45,8 @@ def check(Z, targets=None, ids=None, lp=None, alpha=0.0, tau=1.0, dloss=None, ta
     ref.assert_within(loss, L, le, tag + " loss")
     ref.assert_within(dZ, G, ge + ref.half_step(Z.dtype) * (G.abs() + ge), tag + " dZ")
     alone, _ = run(Z, targets, ids, lp, alpha, tau, dloss, grad=False)
-    assert torch.equal(torch.nan_to_num(alone), torch.nan_to_num(loss)), tag
+    # (the loss alone may cut rows otherwise: the same sums in another order, within the same bound)
+    ref.assert_within(alone, L, le, tag + " loss alone")
     return loss, dZ
 
 

@@ -153,7 +153,6 @@ def _check(fn: str, rc: int):
 
 _F32 = (torch.float32,)
 _ACT = (torch.bfloat16, torch.float32)
-_I64 = (torch.int64,)
 
 
 def _need(fn: str, name: str, t, shape, dtypes) -> None:
@@ -920,32 +919,38 @@ def _first(fn, name, t) -> int:
     return t.get_device()
 
 
+def _bad(fn, name, t, shape, dtypes, dev):
+    """Words what is wrong with an array that is not [shape], of these dtypes, on dev."""
+    _need(fn, name, t, shape, dtypes)
+    _elsewhere(fn, t)
+
+
 def _matrix(fn, name, t, shape, dtypes, dev) -> tuple:
     """Address, row stride and type code of a matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{fn}: {name} must be a tensor")
-    dt = t.dtype
-    if dt not in dtypes or t.shape != shape:
-        _need(fn, name, t, shape, dtypes)
-    if t.get_device() != dev:
-        _elsewhere(fn, t)
-    ld, one = t.stride()
+    try:
+        dt = t.dtype
+        if dt not in dtypes or t.shape != shape or t.get_device() != dev:
+            _bad(fn, name, t, shape, dtypes, dev)
+        ld, one = t.stride()
+    except AttributeError:
+        raise TypeError(f"{fn}: {name} must be a tensor") from None
     if one != 1 or shape[0] <= 1 or shape[1] == 0:
         ld = _row_stride(fn, name, t) if shape[1] else 0   # (the stride of rows without elements means nothing)
     return t.data_ptr(), ld, TERN_BF16 if dt is torch.bfloat16 else TERN_F32
 
 
-def _vector(fn, name, t, shape, dtypes, dev):
+def _vector(fn, name, t, shape, dtype, dev):
     """Address of a contiguous array (None: not given)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype not in dtypes:
-        _need(fn, name, t, shape, dtypes)
-    if t.get_device() != dev:
-        _elsewhere(fn, t)
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libtern must be contiguous")
-    return t.data_ptr()
+    try:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+            _bad(fn, name, t, shape, (dtype,), dev)
+        if t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{fn}: {name} must be a tensor") from None
+    raise ValueError("tensors passed to libtern must be contiguous")
 
 
 def _work(fn, t, dev) -> tuple:
@@ -983,8 +988,8 @@ def tern_norm_fwd(X, Y, w=None, b=None, A=None, S=None, stats=None, eps: float =
             raise ValueError(f"{fn}: A and S are given together")
         a, lda, ad = _matrix(fn, "A", A, shape, _ACT, dev)
         s, lds, _ = _matrix(fn, "S", S, shape, (X.dtype,), dev)
-    wp, bp = _vector(fn, "w", w, (C,), _F32, dev), _vector(fn, "b", b, (C,), _F32, dev)
-    st = _vector(fn, "stats", stats, (T, 2), _F32, dev)
+    wp, bp = _vector(fn, "w", w, (C,), torch.float32, dev), _vector(fn, "b", b, (C,), torch.float32, dev)
+    st = _vector(fn, "stats", stats, (T, 2), torch.float32, dev)
     _on_gpu(fn, dev, X)
     _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, eps, T, C, s, lds, y, ldy, yd, st)
 
@@ -1004,9 +1009,9 @@ def tern_norm_bwd(S, stats, dY, dX, workspace=None, w=None, dS=None, dw=None, db
     if dS is not None:
         ds, ldds, _ = _matrix(fn, "dS", dS, shape, (dX.dtype,), dev)
     if stats is None:
-        _need(fn, "stats", stats, (T, 2), _F32)
-    st, wp = _vector(fn, "stats", stats, (T, 2), _F32, dev), _vector(fn, "w", w, (C,), _F32, dev)
-    dwp, dbp = _vector(fn, "dw", dw, (C,), _F32, dev), _vector(fn, "db", db, (C,), _F32, dev)
+        raise TypeError(f"{fn}: stats must be a tensor")
+    st, wp = _vector(fn, "stats", stats, (T, 2), torch.float32, dev), _vector(fn, "w", w, (C,), torch.float32, dev)
+    dwp, dbp = _vector(fn, "dw", dw, (C,), torch.float32, dev), _vector(fn, "db", db, (C,), torch.float32, dev)
     ws, n = _work(fn, workspace, dev)
     _on_gpu(fn, dev, S)
     _call(fn, dev, stream, s, lds, sd, st, wp, dy, lddy, dyd, ds, ldds, T, C, dx, lddx, dxd, dwp, dbp, ws, n)
@@ -1035,7 +1040,7 @@ def _pair(fn, ids_name, ids, lp_name, lp, T, dev) -> tuple:
         raise ValueError(f"{fn}: {ids_name} and {lp_name} are given together")
     _first(fn, ids_name, ids)
     k = ids.shape[1]
-    return k, _vector(fn, ids_name, ids, (T, k), _I64, dev), _vector(fn, lp_name, lp, (T, k), _F32, dev)
+    return k, _vector(fn, ids_name, ids, (T, k), torch.int64, dev), _vector(fn, lp_name, lp, (T, k), torch.float32, dev)
 
 
 def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None,
@@ -1051,8 +1056,8 @@ def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=No
     T, V = shape
     z, ld, zd = _logits(fn, "Z", Z, shape, _ACT, dev)
     k, ids, lp = _pair(fn, "top_ids", top_ids, "top_logp", top_logp, T, dev)
-    tok, lt = _vector(fn, "tokens", tokens, (T,), _I64, dev), _vector(fn, "logp", logp, (T,), _F32, dev)
-    en, ls = _vector(fn, "entropy", entropy, (T,), _F32, dev), _vector(fn, "lse", lse, (T,), _F32, dev)
+    tok, lt = _vector(fn, "tokens", tokens, (T,), torch.int64, dev), _vector(fn, "logp", logp, (T,), torch.float32, dev)
+    en, ls = _vector(fn, "entropy", entropy, (T,), torch.float32, dev), _vector(fn, "lse", lse, (T,), torch.float32, dev)
     ws, n = _work(fn, workspace, dev)
     _on_gpu(fn, dev, Z)
     _call(fn, dev, stream, z, ld, zd, scale, T, V, tok, lt, en, ls, k, ids, lp, ws, n)
@@ -1083,8 +1088,8 @@ def tern_distill(Z, workspace=None, targets=None, teacher_ids=None, teacher_logp
     if dZ is not None:
         dz, lddz, _ = _logits(fn, "dZ", dZ, shape, (Z.dtype,), dev)
     K, ids, lp = _pair(fn, "teacher_ids", teacher_ids, "teacher_logp", teacher_logp, T, dev)
-    y, dl = _vector(fn, "targets", targets, (T,), _I64, dev), _vector(fn, "dloss", dloss, (T,), _F32, dev)
-    lo = _vector(fn, "loss", loss, (T,), _F32, dev)
+    y, dl = _vector(fn, "targets", targets, (T,), torch.int64, dev), _vector(fn, "dloss", dloss, (T,), torch.float32, dev)
+    lo = _vector(fn, "loss", loss, (T,), torch.float32, dev)
     ws, n = _work(fn, workspace, dev)
     _on_gpu(fn, dev, Z)
     _call(fn, dev, stream, z, ld, zd, T, V, y, K, ids, lp, alpha, tau, dl, lo, dz, lddz, ws, n)

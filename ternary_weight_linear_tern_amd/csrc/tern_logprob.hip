@@ -364,7 +364,7 @@ struct Launch {
 
 template <int32_t DT>
 void run(const LogprobArgs &a, const RowPlan &p, hipStream_t st) {
-    with_plan<DT>(p, Launch<DT>{a, st});
+    with_plan<DT, 1, 4>(p, Launch<DT>{a, st});
     if (a.S > 1)
         hipLaunchKernelGGL(hdev::logprob_join_kernel<DT>, dim3((unsigned)std::min<int64_t>(a.T, 1 << 21)), dim3(256), 0,
                            st, a);

@@ -245,26 +245,25 @@ inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V, int most, bool in_tur
     return p;
 }
 
-// f<W, NV>() of the kernel that a plan asks for.
-template <int32_t DT, class F>
+// f<W, NV>() of the kernel that a plan of LEAST to MOST waves asks for.
+template <int32_t DT, int LEAST, int MOST, class F>
 void with_plan(const RowPlan &p, F f) {
     constexpr int H = held(DT);
     const bool big = p.NV > 4;
-    switch (p.W) {
-    case 1:
-        if (big) f.template operator()<1, H>();
-        else if (p.NV > 1) f.template operator()<1, 4>();
-        else f.template operator()<1, 1>();
-        break;
-    case 4:
+    if constexpr (LEAST <= 1) {
+        if (p.W == 1) {
+            if (big) f.template operator()<1, H>();
+            else if (p.NV > 1) f.template operator()<1, 4>();
+            else f.template operator()<1, 1>();
+        }
+    }
+    if (p.W == 4) {
         if (big) f.template operator()<4, H>();
         else f.template operator()<4, 4>();
-        break;
-    case 8:
-        f.template operator()<8, H>();
-        break;
-    default:
-        f.template operator()<16, H>();
+    }
+    if constexpr (MOST >= 16) {
+        if (p.W == 8) f.template operator()<8, H>();
+        if (p.W == 16) f.template operator()<16, H>();
     }
 }
 

@@ -378,9 +378,9 @@ void run(const DistillArgs &a, const RowPlan &p, hipStream_t st) {
         else with_plan<DT, 1, 4>(p, Launch<DT, 3>{a, st});
         return;
     }
-    // (parts are longer than one wave's)
-    with_plan<DT, 4, 16>(p, Launch<DT, 1>{a, st});
-    if (a.dZ) with_plan<DT, 4, 16>(p, Launch<DT, 2>{a, st});
+    // (parts are longer than one wave takes, and take eight at most)
+    with_plan<DT, 4, 8>(p, Launch<DT, 1>{a, st});
+    if (a.dZ) with_plan<DT, 4, 8>(p, Launch<DT, 2>{a, st});
     else
         hipLaunchKernelGGL(kdev::distill_loss_kernel<DT>, dim3((unsigned)std::min<int64_t>(a.T, 1 << 21)), dim3(64), 0,
                            st, a);

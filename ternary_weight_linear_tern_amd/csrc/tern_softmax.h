@@ -227,7 +227,13 @@ inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V, int most, bool in_tur
     RowPlan p{};
     const int64_t fits = (int64_t)most * 512 * nv;
     int64_t S = in_turn ? 1 : cdiv_(V, fits);
-    if (T < (in_turn ? 512 : 128)) S = std::max(S, std::min(cdiv_(512, std::max<int64_t>(T, 1)), cdiv_(V, 4096)));
+    if (S > 1) S = cdiv_(V, fits / 2);   // cut anyway: halves, two of which share a compute unit
+    if (T < (in_turn ? 512 : 128)) {
+        // (rounded down while that leaves four parts: a second turn of few workgroups costs
+        // more than it gives; 127 rows of 131072 fp32 with gradient 47 us in 5 parts, 40 in 4)
+        const int64_t want = T < 128 ? 512 / std::max<int64_t>(T, 1) : cdiv_(512, T);
+        S = std::max(S, std::min(want, cdiv_(V, 4096)));
+    }
     S = std::min<int64_t>(S, kMaxSegments);
     p.part = cdiv_(cdiv_(V, S), 8) * 8;
     p.S = (int)cdiv_(V, p.part);
@@ -261,10 +267,10 @@ void with_plan(const RowPlan &p, F f) {
         if (big) f.template operator()<4, H>();
         else f.template operator()<4, 4>();
     }
-    if constexpr (MOST >= 16) {
+    if constexpr (MOST >= 8)
         if (p.W == 8) f.template operator()<8, H>();
+    if constexpr (MOST >= 16)
         if (p.W == 16) f.template operator()<16, H>();
-    }
 }
 
 inline bool row_sizes_ok(int64_t T, int64_t V) { return T >= 0 && T <= kMaxT && V >= 1 && V <= kMaxInOut; }

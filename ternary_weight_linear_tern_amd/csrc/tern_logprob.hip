@@ -10,8 +10,10 @@
 // elements reach, and hardly more do; a bisection over its bits by one wave finds
 // it.  The eights that hold an element which reaches it go to a list in shared
 // memory, their elements that do to another, and each one's place is the
-// number of greater keys there.  Rows whose lists would overflow (ties, rows in
-// which fewer than k tokens are allowed) are taken one alternative after the other.
+// number of greater keys there.  Where a list would overflow (ties, rows in which
+// fewer than k tokens are allowed) the k-th largest value is found itself, by the same
+// bisection over all elements unless the bound is it, and then the elements above it
+// and the first of those equal to it, by their index.
 //
 // A row longer than a workgroup's registers is taken in segments, one after the
 // other (the sums rescaled, the alternatives so far a bound for the next); where
@@ -47,8 +49,10 @@ struct Pick {
     uint64_t key[kKeys];
     Raw8<DT> eight[kEights];
     int from[kEights];             // index of an eight's first element in its segment
-    uint64_t round[2][W];
+    uint64_t mask[64];             // lanes with an element equal to the k-th largest, stride by stride and wave by wave
+    int before[64];                // how many such lanes stand before a mask's
     uint32_t group[kGroups];
+    float sum[2][W];
     uint32_t bound;
     int keys, eights;
 };
@@ -65,15 +69,6 @@ __device__ inline uint32_t wave_all_u(uint32_t x) {
     for (int d = 1; d < 64; d *= 2) x = Op::of(x, (uint32_t)__shfl_xor((int)x, d));
     return x;
 }
-__device__ inline uint64_t wave_max64(uint64_t x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t y = __shfl_xor((unsigned long long)x, d);
-        x = y > x ? y : x;
-    }
-    return x;
-}
-
 // A bound that at least k of the groups' largest reach (0 where there are not k
 // groups), by one wave.
 template <int G>
@@ -109,9 +104,112 @@ __device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
     return lo;
 }
 
+// The elements that the listed eights hold, as keys: those that `take` says.
+template <int DT, int W, class F>
+__device__ inline void keys_of_eights(Pick<DT, W> &p, int eights, int n, uint32_t first, int tid, F take) {
+    for (int q = tid; q < eights * 8; q += W * 64) {
+        const int v = p.from[q >> 3] + (q & 7);
+        const float f = at<DT>((const char *)&p.eight[q >> 3], q & 7);
+        if (v < n && take(f)) {
+            const int at = atomicAdd(&p.keys, 1);
+            if (at < Pick<DT, W>::kKeys) p.key[at] = key_of(f, first + v);
+        }
+    }
+}
+
+// The `want` largest of a segment as keys behind the `had` in p.key, whatever it holds
+// (of NaNs, as of infinities, any).  `bound` is reached by that many at least.
+template <int DT, int W, int NV>
+__device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first, int want, int had, uint32_t bound,
+                                  Pick<DT, W> &p, int tid) {
+    constexpr int ST = W * 512, kTies = TERN_TOP_MAX;   // ties stand behind 64 other eights
+    tid = fresh(tid);
+    const int lane = tid & 63, wave = tid >> 6;
+    auto number = [](float f) { return f != f ? kInf : f; };
+    int turn = 0;
+    auto above = [&](uint32_t t) {
+        const float v = from_ordered(t);
+        float c = 0.0f;
+        each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) c += number(f[j]) > v && i * ST + tid * 8 + j < n ? 1.0f : 0.0f;
+        });
+        turn ^= 1;
+        return (int)row_all<Add, W>(c, p.sum[turn], tid);
+    };
+    const uint32_t least = ordered(-kInf), most = ordered(kInf);
+    uint32_t value = min(max(bound, least), most);
+    int more = above(value);
+    if (more >= want) {   // fewer than want are above hi, more are above lo
+        uint32_t lo = value, hi = most;
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (above(mid) < want) hi = mid;
+            else lo = mid;
+        }
+        value = hi;
+        more = above(value);
+    }
+    const float v = from_ordered(value);
+    meet<W>();
+    if (tid == 0) p.keys = had, p.eights = 0;
+    if (tid < 64) p.mask[tid] = 0;
+    meet<W>();
+    each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+        bool over = false, equal = false;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const bool in = i * ST + tid * 8 + j < n;
+            over = over || (in && number(f[j]) > v);
+            equal = equal || (in && number(f[j]) == v);
+        }
+        const uint64_t m = __ballot(equal);
+        if (lane == 0) p.mask[i * W + wave] = m;
+        if (over) {
+            const int at = atomicAdd(&p.eights, 1);   // fewer than want
+            p.eight[at] = x[i], p.from[at] = i * ST + tid * 8;
+        }
+    });
+    meet<W>();
+    keys_of_eights<DT, W>(p, p.eights, n, first, tid, [&](float f) { return number(f) > v; });
+    if (tid < 64) {
+        const int mine = __builtin_popcountll(p.mask[tid]);
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        p.before[tid] = sum - mine;
+    }
+    meet<W>();
+    const int ties = want - more;
+    each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+        const uint64_t m = p.mask[i * W + wave];
+        const int rank = p.before[i * W + wave] + __builtin_popcountll(m & ((1ull << lane) - 1));
+        if ((m >> lane & 1) && rank < ties)
+            p.eight[kTies + rank] = x[i], p.from[kTies + rank] = i * ST + tid * 8;
+    });
+    meet<W>();
+    if (tid < 64) {   // the listed eights in order, 64 elements at a time
+        const int eights = min(ties, p.before[63] + __builtin_popcountll(p.mask[63]));
+        int taken = 0;
+        for (int q = tid; q < (eights * 8 + 63) / 64 * 64; q += 64) {
+            const int at8 = kTies + min(q >> 3, eights - 1), i = p.from[at8] + (q & 7);
+            const float f = at<DT>((const char *)&p.eight[at8], q & 7);
+            const bool tie = q < eights * 8 && i < n && number(f) == v;
+            const uint64_t m = __ballot(tie);
+            const int rank = taken + __builtin_popcountll(m & ((1ull << lane) - 1));
+            if (tie && rank < ties) p.key[atomicAdd(&p.keys, 1)] = key_of(f, first + i);
+            taken += __builtin_popcountll(m);
+        }
+    }
+    meet<W>();
+}
+
 // The k largest (fewer where there are not so many) of the segment in x, n elements
 // of which `first` is the first's index, and of the `had` that p.top holds already:
-// to p.top.  Says how many there are, or -1 where a list would overflow.
+// to p.top.  Returns how many there are.
 template <int DT, int W, int NV>
 __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t first, int k, int had, float mine,
                                      Pick<DT, W> &p, int tid) {
@@ -126,33 +224,31 @@ __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t fi
     for (int i = tid; i < had; i += W * 64) p.key[i] = p.top[i];
     meet<W>();
     if (tid < 64) {
-        uint32_t b = bound_of<G>(p.group, k, tid);
-        if (had == k) b = max(b, (uint32_t)(p.top[k - 1] >> 32));
+        const uint32_t b = bound_of<G>(p.group, k, tid);
         if (tid == 0) p.bound = b;
     }
     meet<W>();
-    const float bound = from_ordered(p.bound);   // of 0: NaN, below which nothing is
-    if (__ballot(!(mine < bound))) {
+    const uint32_t reached = p.bound;
+    // the last of the k so far is a bound as well
+    const float bound = from_ordered(had == k ? max(reached, (uint32_t)(p.top[k - 1] >> 32)) : reached);
+    if (__ballot(!(mine < bound)))
         each8<DT, W, NV>(x, n, [&](int i, const float *f) {
             if (max8(f) < bound) return;
             const int at = atomicAdd(&p.eights, 1);
             if (at < P::kEights) p.eight[at] = x[i], p.from[at] = i * ST + tid * 8;
         });
-    }
     meet<W>();
     const int eights = p.eights;
-    if (eights > P::kEights) return -1;
-    for (int q = tid; q < eights * 8; q += W * 64) {
-        const int v = p.from[q >> 3] + (q & 7);
-        const float f = at<DT>((const char *)&p.eight[q >> 3], q & 7);
-        if (!(f < bound) && v < n) {
-            const int at = atomicAdd(&p.keys, 1);
-            if (at < P::kKeys) p.key[at] = key_of(f, first + v);
-        }
-    }
+    if (eights <= P::kEights)
+        keys_of_eights<DT, W>(p, eights, n, first, tid, [&](float f) { return !(f < bound); });
     meet<W>();
-    const int keys = p.keys, want = min(k, had + n);
-    if (keys > P::kKeys || keys < want) return -1;
+    const int want = min(k, had + n);
+    int keys = p.keys;
+    if (eights > P::kEights || keys > P::kKeys || keys < want) {
+        meet<W>();
+        exact_keys<DT, W, NV>(x, n, first, min(k, n), had, reached, p, tid);
+        keys = p.keys;
+    }
     for (int q = tid; q < keys; q += W * 64) {
         const uint64_t key = p.key[q];
         int place = 0;
@@ -162,32 +258,6 @@ __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t fi
     }
     meet<W>();
     return want;
-}
-
-// The same of n elements in memory, one after the other: each lane keeps its largest
-// below the last one taken.
-template <int DT, int W>
-__device__ inline void top_by_turns(const char *z, int n, uint32_t first, int k, Pick<DT, W> &p, int tid) {
-    tid = fresh(tid);
-    uint64_t last = ~(uint64_t)0, best = 0;
-    for (int r = 0; r < k; r++) {
-        if (best == last || r == 0) {
-            best = 0;
-            for (int v = tid; v < n; v += W * 64) {
-                const uint64_t key = key_of(at<DT>(z, v), first + v);
-                if (key < last && key > best) best = key;
-            }
-        }
-        uint64_t top = wave_max64(best);
-        if constexpr (W > 1) {
-            if ((tid & 63) == 0) p.round[r & 1][tid >> 6] = top;
-            __syncthreads();
-            for (int i = 0; i < W; i++) top = max(top, p.round[r & 1][i]);
-        }
-        last = top;
-        if (tid == 0) p.top[r] = top;
-    }
-    meet<W>();
 }
 
 // what a row's sums say
@@ -267,12 +337,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
             u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
             s = f0 * s + f1 * s1;
             M = both;
-            if (a.k && had >= 0) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);
+            if (a.k) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);
             meet<W>();
-        }
-        if (had < 0) {
-            top_by_turns<DT, W>(row + (int64_t)begin * esize<DT>(), end - begin, begin, min(a.k, end - begin), pick, tid);
-            had = min(a.k, end - begin);
         }
         const int l = fresh(tid);
         if (a.S == 1) {
@@ -290,9 +356,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
     }
 }
 
-// Rows that were cut: the parts' sums meet, and their alternatives.  Each
-// part's keys fall, so that with r = ceil(k / S) the smallest of their r-th is
-// reached by k at least.
+// Rows that were cut: the parts' sums meet, and their alternatives.  Each part's keys
+// fall, so that k at least reach the k-th of any part, and, with r = ceil(k / S), the
+// smallest of the parts' r-th: the larger of the two bounds leaves few to compare.
 template <int DT>
 __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     __shared__ uint64_t list[kMaxSegments * TERN_TOP_MAX];
@@ -308,9 +374,14 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
         if (!a.k) continue;
         const uint64_t *keys = a.keys + t * a.S * a.k;
         const int rank = (a.k + a.S - 1) / a.S - 1;
-        uint64_t bound = lane < a.S ? keys[lane * a.k + rank] : ~(uint64_t)0;
+        uint64_t low = lane < a.S ? keys[lane * a.k + rank] : ~(uint64_t)0;
+        uint64_t high = lane < a.S ? keys[lane * a.k + a.k - 1] : 0;
 #pragma unroll
-        for (int i = 1; i < 64; i *= 2) bound = min(bound, (uint64_t)__shfl_xor((unsigned long long)bound, i));
+        for (int i = 1; i < 64; i *= 2) {
+            low = min(low, (uint64_t)__shfl_xor((unsigned long long)low, i));
+            high = max(high, (uint64_t)__shfl_xor((unsigned long long)high, i));
+        }
+        const uint64_t bound = max(low, high);
         if (tid == 0) count = 0;
         __syncthreads();
         for (int i = tid; i < a.S * a.k; i += 256) {

@@ -217,23 +217,23 @@ struct RowPlan {
 
 inline int64_t cdiv_(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Whole rows where there are enough of them; few long rows are cut, so that some
-// 512 workgroups share them.  `most`: waves of a workgroup; in_turn: a part may take
-// several segments, else it is one (and a gradient reads cut rows again, so that
-// they are cut only where the rows are fewer: 200 rows of 131072, 20 alternatives,
-// 36 us whole and 28 cut; 300 rows of 50021 with gradient, 25 us whole and 27 cut).
+// Whole rows where there are enough of them; few long rows are cut, so that up to 512
+// workgroups share them.  `most`: waves of a workgroup; in_turn: a part may take
+// several segments, else it is one.  Rounded down, since a second turn of few
+// workgroups costs more than it gives (127 rows of 131072 fp32 with gradient: 47 us
+// in 5 parts, 40 in 4).  A gradient reads cut rows again, so that more rows than that
+// stay whole (300 rows of 50021: 25 us whole, 27 cut); in turn, they are cut while
+// the 1024 workgroups that run at once get 24576 elements each (20 alternatives, 200
+// rows: of 131072 36 us whole, 28 in 3 parts, 24 in 5; of 32768 11 us whole, 15 in 3).
 inline RowPlan plan_rows(int32_t dt, int64_t T, int64_t V, int most, bool in_turn) {
     const int nv = held(dt);
     RowPlan p{};
     const int64_t fits = (int64_t)most * 512 * nv;
     int64_t S = in_turn ? 1 : cdiv_(V, fits);
     if (S > 1) S = cdiv_(V, fits / 2);   // cut anyway: halves, two of which share a compute unit
-    if (T < (in_turn ? 512 : 128)) {
-        // (rounded down while that leaves four parts: a second turn of few workgroups costs
-        // more than it gives; 127 rows of 131072 fp32 with gradient 47 us in 5 parts, 40 in 4)
-        const int64_t want = T < 128 ? 512 / std::max<int64_t>(T, 1) : cdiv_(512, T);
-        S = std::max(S, std::min(want, cdiv_(V, 4096)));
-    }
+    const int64_t rows = std::max<int64_t>(T, 1);
+    if (T < 128) S = std::max(S, std::min(512 / rows, cdiv_(V, 4096)));
+    if (in_turn && T < 512) S = std::max(S, std::min(1024 / rows, V / 24576));
     S = std::min<int64_t>(S, kMaxSegments);
     p.part = cdiv_(cdiv_(V, S), 8) * 8;
     p.S = (int)cdiv_(V, p.part);

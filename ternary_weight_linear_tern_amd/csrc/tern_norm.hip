@@ -28,7 +28,7 @@ struct FwdArgs {
     void *S, *Y;
     float *stats;
     int64_t ldx, lda, lds, ldy, T;
-    int C, W, a_dtype;
+    int C, W, P, a_dtype;
     float eps;
 };
 
@@ -40,7 +40,7 @@ struct BwdArgs {
     float *part;             // [groups][2][C]: dw and db of the groups' rows
     int64_t lds, lddy, ldds, lddx, T;
     int64_t groups;          // row groups, a workgroup each
-    int C, W;
+    int C, W, P;
 };
 
 template <int DT>
@@ -77,17 +77,27 @@ struct RawA {
 };
 
 // How a workgroup takes rows of up to 16 * 512 * CV columns: W waves a row, eight
-// neighbours a lane, CV times; R rows at once.
+// neighbours a lane, CV times; rows of 256 columns and fewer take P = 8, 16 or 32
+// lanes of one wave (65536 rows of 64 forward: 27.7 us with a wave
+// each, 7.5 with 8 lanes).  R rows at once.
+// (P is a variable in kernels of their own: that costs the others some per cent.)
+template <bool NARROW>
 struct Lanes {
-    int W, R, slot, tid, wave;   // this lane's row among the R, its number and its wave in the row
-    __device__ explicit Lanes(int waves) : W(waves) {
-        const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        R = (int)blockDim.x / (64 * W);
-        slot = w / W;
-        wave = w - slot * W;
-        tid = wave * 64 + (int)(threadIdx.x & 63);
+    int W, P, R, slot, tid, wave;   // this lane's row among the R, its number and its wave in the row
+    __device__ Lanes(int waves, int lanes) : W(NARROW ? 1 : waves), P(NARROW ? lanes : 64) {
+        R = (int)blockDim.x / (P * W);
+        if (!NARROW) {
+            const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+            slot = w / W;
+            wave = w - slot * W;
+            tid = wave * 64 + (int)(threadIdx.x & 63);
+        } else {
+            slot = (int)threadIdx.x / P;
+            wave = 0;
+            tid = (int)threadIdx.x & (P - 1);
+        }
     }
-    __device__ int col(int v) const { return (v * W * 64 + tid) * 8; }
+    __device__ int col(int v) const { return (v * W * P + tid) * 8; }
     // columns of wave w of a row
     template <int CV>
     __device__ float columns(int w, int C) const {
@@ -104,10 +114,10 @@ constexpr int kTogether = 8;   // waves of a backward workgroup that has several
 // registers and, where they leave room (CV 1), the next rows' loads under way.  Each
 // wave takes the mean of its columns and the squares around that; the waves'
 // meet by n_i (mu_i - mu)^2: one barrier for R rows.
-template <int XD, int YD, int CV>
+template <int XD, int YD, int CV, bool NARROW>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a) {
     __shared__ float2 sh[2][kMaxWaves];
-    const Lanes l(a.W);
+    const Lanes<NARROW> l(a.W, a.P);
     float w[CV][8], b[CV][8];
 #pragma unroll
     for (int v = 0; v < CV; v++)
@@ -127,7 +137,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a
             }
     };
     const int64_t step = (int64_t)gridDim.x * l.R;
-    const float n = l.columns<CV>(l.wave, a.C);
+    const float n = l.template columns<CV>(l.wave, a.C);
     if (CV == 1) fetch((int64_t)blockIdx.x * l.R + l.slot);
     int turn = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * l.R; t0 < a.T; t0 += step, turn ^= 1) {
@@ -149,24 +159,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a
                 for (int j = 0; j < 8; j++) sum += x[v][j];
             }
         if (CV == 1) fetch(t + step);
-        float mu = wave_all<Add>(sum) / fmaxf(n, 1.0f);
+        float mu = lanes_all<Add>(sum, l.P) / fmaxf(n, 1.0f);
 #pragma unroll
         for (int v = 0; v < CV; v++)
             if (here && l.col(v) < a.C)
 #pragma unroll
                 for (int j = 0; j < 8; j++) sq = fmaf(x[v][j] - mu, x[v][j] - mu, sq);
-        sq = wave_all<Add>(sq);
-        if (l.W > 1) {
+        sq = lanes_all<Add>(sq, l.P);
+        if (!NARROW && l.W > 1) {
             const float2 *of = &sh[turn][l.slot * l.W];
             if ((threadIdx.x & 63) == 0) sh[turn][l.slot * l.W + l.wave] = float2{mu, sq};
             __syncthreads();
             float m = 0.0f;
-            for (int i = 0; i < l.W; i++) m = fmaf(l.columns<CV>(i, a.C), of[i].x, m);
+            for (int i = 0; i < l.W; i++) m = fmaf(l.template columns<CV>(i, a.C), of[i].x, m);
             mu = m / (float)a.C;
             sq = 0.0f;
             for (int i = 0; i < l.W; i++) {
                 const float d = of[i].x - mu;
-                sq += fmaf(l.columns<CV>(i, a.C) * d, d, of[i].y);
+                sq += fmaf(l.template columns<CV>(i, a.C) * d, d, of[i].y);
             }
         }
         const float r = 1.0f / sqrtf(sq / (float)a.C + a.eps);
@@ -227,11 +237,11 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(FwdArgs a) {
 // The backward of rows in registers, as the forward's: S and dY are read once, for
 // dX and for the sums of dw and db, which a lane keeps for its columns over all
 // rows of its workgroup.
-template <int SD, int DY, int DX, int CV>
+template <int SD, int DY, int DX, int CV, bool NARROW>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a) {
     __shared__ float2 sh[2][kMaxWaves];
     __shared__ float4 meet[kTogether * 128];   // [R][C / 4] where there are several rows
-    const Lanes l(a.W);
+    const Lanes<NARROW> l(a.W, a.P);
     float w[CV][8], dw[CV][8] = {}, db[CV][8] = {};
 #pragma unroll
     for (int v = 0; v < CV; v++)
@@ -278,9 +288,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a
                 }
             }
         if (CV == 1) fetch(t + step);
-        s1 = wave_all<Add>(s1);
-        s2 = wave_all<Add>(s2);
-        if (l.W > 1) {
+        s1 = lanes_all<Add>(s1, l.P);
+        s2 = lanes_all<Add>(s2, l.P);
+        if (!NARROW && l.W > 1) {
             const float2 *of = &sh[turn][l.slot * l.W];
             if ((threadIdx.x & 63) == 0) sh[turn][l.slot * l.W + l.wave] = float2{s1, s2};
             __syncthreads();
@@ -421,18 +431,20 @@ int launched() { return hipGetLastError() == hipSuccess ? TERN_OK : TERN_ERR_HIP
 bool sizes_ok(int64_t T, int64_t C) { return T >= 0 && T <= kMaxT && C >= 0 && C <= kMaxInOut && C % 8 == 0; }
 bool stride_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0 && ld <= kMaxInOut * 8; }
 
-// Waves of a row and eights of a lane; waves 0: rows too long for registers.
+// Waves of a row, eights of a lane and lanes of a wave; waves 0: rows too long for
+// registers.
 struct RowShape {
-    int W, CV;
+    int W, CV, P;
 };
 RowShape shape_of(int64_t C) {
     const int64_t most = ndev::kMaxWaves * 512;
-    if (C <= most) return {(int)cdiv(C, 512), 1};
-    if (C <= 2 * most) return {(int)cdiv(C, 1024), 2};
-    return {0, 0};
+    if (C <= 512) return {1, 1, C <= 64 ? 8 : C <= 128 ? 16 : C <= 256 ? 32 : 64};
+    if (C <= most) return {(int)cdiv(C, 512), 1, 64};
+    if (C <= 2 * most) return {(int)cdiv(C, 1024), 2, 64};
+    return {0, 0, 64};
 }
 // rows of a workgroup of about `waves` waves
-int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std::max(s.W, 1)); }
+int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std::max(s.W, 1)) * (64 / s.P); }
 
 // Row groups of the backward, a workgroup each.
 int64_t groups_of(int64_t T, int64_t C) {
@@ -478,7 +490,7 @@ int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, in
                        {in_place ? nullptr : X, T, C, ldx, xs}};
     if (any_overlap(outs, 3, ins, 4)) return TERN_ERR_ALIAS;
     const RowShape shape = shape_of(C);
-    FwdArgs a{X, A, w, b, S, Y, stats, ldx, lda, lds, ldy, T, (int)C, shape.W, a_dtype, eps};
+    FwdArgs a{X, A, w, b, S, Y, stats, ldx, lda, lds, ldy, T, (int)C, shape.W, shape.P, a_dtype, eps};
     hipStream_t st = (hipStream_t)stream;
     with_type(x_dtype, [&](auto xd) {
         with_type(y_dtype, [&](auto yd) {
@@ -489,9 +501,10 @@ int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, in
                 return;
             }
             const int R = rows_at_once(shape, 4);
-            const dim3 g((unsigned)std::min<int64_t>(cdiv(T, R), 2048)), bl(64 * shape.W * R);
-            if (shape.CV == 1) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1>), g, bl, 0, st, a);
-            else hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 2>), g, bl, 0, st, a);
+            const dim3 g((unsigned)std::min<int64_t>(cdiv(T, R), 2048)), bl(shape.P * shape.W * R);
+            if (shape.P < 64) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1, true>), g, bl, 0, st, a);
+            else if (shape.CV == 1) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1, false>), g, bl, 0, st, a);
+            else hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 2, false>), g, bl, 0, st, a);
         });
     });
     return launched();
@@ -526,7 +539,7 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
     if (T == 0 && !weights) return TERN_OK;
     const RowShape shape = shape_of(C);
     BwdArgs a{S, dY, dS, stats, w, dX, dw, db, weights ? (float *)workspace : nullptr, lds, lddy, ldds, lddx, T, groups,
-              (int)C, shape.W};
+              (int)C, shape.W, shape.P};
     hipStream_t st = (hipStream_t)stream;
     const unsigned cols = (unsigned)cdiv(C, 64);
     if (T > 0) {
@@ -541,10 +554,12 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
                                                dim3((unsigned)std::min<int64_t>(T, 65536)), dim3(256), 0, st, a);
                             return;
                         }
-                        const dim3 g((unsigned)groups), bl(64 * shape.W * rows_at_once(shape, ndev::kTogether));
-                        if (shape.CV == 1)
-                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1>), g, bl, 0, st, a);
-                        else hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 2>), g, bl, 0, st, a);
+                        const dim3 g((unsigned)groups), bl(shape.P * shape.W * rows_at_once(shape, ndev::kTogether));
+                        if (shape.P < 64)
+                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1, true>), g, bl, 0, st, a);
+                        else if (shape.CV == 1)
+                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1, false>), g, bl, 0, st, a);
+                        else hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 2, false>), g, bl, 0, st, a);
                     }
                 });
                 if (weights && shape.W == 0)

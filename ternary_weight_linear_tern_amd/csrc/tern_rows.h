@@ -93,16 +93,26 @@ template <int CTRL>
 __device__ inline float dpp(float x) {
     return as_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_u(x), CTRL, 0xF, 0xF, false));
 }
+// over groups of P = 8, 16, 32 or 64 neighbouring lanes
 template <class Op>
-__device__ inline float wave_all(float x) {
+__device__ inline float lanes_all(float x, int P) {
     x = Op::of(x, dpp<0xB1>(x));    // lane ^ 1
     x = Op::of(x, dpp<0x4E>(x));    // lane ^ 2
     x = Op::of(x, dpp<0x141>(x));   // mirrored in 8
-    x = Op::of(x, dpp<0x140>(x));   // mirrored in 16
-    const auto a = __builtin_amdgcn_permlane16_swap(as_u(x), as_u(x), false, false);
-    x = Op::of(as_f(a[0]), as_f(a[1]));
-    const auto b = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(x), false, false);
-    return Op::of(as_f(b[0]), as_f(b[1]));
+    if (P > 8) x = Op::of(x, dpp<0x140>(x));   // mirrored in 16
+    if (P > 16) {
+        const auto a = __builtin_amdgcn_permlane16_swap(as_u(x), as_u(x), false, false);
+        x = Op::of(as_f(a[0]), as_f(a[1]));
+    }
+    if (P > 32) {
+        const auto b = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(x), false, false);
+        x = Op::of(as_f(b[0]), as_f(b[1]));
+    }
+    return x;
+}
+template <class Op>
+__device__ inline float wave_all(float x) {
+    return lanes_all<Op>(x, 64);
 }
 
 // Over the W waves of a workgroup; `sh` holds W floats and is free again after

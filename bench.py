@@ -73,8 +73,9 @@ def parse():
                          "HBM traffic counters)")
     ap.add_argument("--extras", action="store_true",
                     help="instead of the step: per-call times of the accumulating backward, the q/k/v "
-                         "group, the health panel, the scale step, the recurrence, the 4-bit products and "
-                         "the orthogonalisation on the workload's shapes (eager, one JSON line)")
+                         "group, the health panel, the scale step, the recurrence, the 4-bit products, "
+                         "the orthogonalisation, the layer norm, the log probabilities and the distillation "
+                         "loss on the workload's shapes (eager, one JSON line)")
     return ap.parse_args()
 
 
@@ -216,8 +217,10 @@ def layer_operators(w, projs, timed):
     """The operators around a layer's projections on the workload's sizes: the
     gated linear recurrence (over sequences of 1024 tokens; 256 in the small
     workload), one token of 32 sequences through it, one token through every
-    projection as a 4-bit product, and the layer's weight gradients
-    orthogonalised."""
+    projection as a 4-bit product, the layer's weight gradients
+    orthogonalised, the layer norm in front of the projections (an fp32 stream,
+    bf16 into the projections), and behind a head of 32768 tokens the teacher's
+    32 alternatives and the distillation loss with its gradient."""
     import torch
 
     import ternary_weight_linear_tern_amd as tl
@@ -267,6 +270,29 @@ def layer_operators(w, projs, timed):
     flops = sum(5.0 * min(s) ** 2 * (3 * max(s) + min(s)) for s in shapes)
     out["orthogonalize"] = {"ms": round(ms, 4), "steps": 5, "tflops": round(flops / ms / 1e9, 1),
                             "mfma_frac": round(flops / ms / 1e9 / PEAK_TFLOPS["bf16"], 4)}
+    del buf, grad, states, mats, q4
+
+    X, A, wgt, bias = N(T, d), N(T, d), N(d), N(d)
+    S, stats = torch.empty_like(X), tl.empty_norm_stats(T)
+    ms = timed(lambda: tl.tern_norm_fwd(X, Y, w=wgt, b=bias, A=A, S=S, stats=stats))
+    out["norm_fwd"] = {"ms": round(ms, 4), **hbm(ms, 14 * T * d)}
+    dX, dw, db, ws = torch.empty_like(X), torch.empty_like(wgt), torch.empty_like(bias), tl.empty_norm_workspace(T, d)
+    ms = timed(lambda: tl.tern_norm_bwd(S, stats, dY, dX, ws, w=wgt, dS=A, dw=dw, db=db))
+    out["norm_bwd"] = {"ms": round(ms, 4), **hbm(ms, 16 * T * d)}
+    V, K = 32768, 32
+    Z = torch.empty((T, V), **bf)
+    for t in range(0, T, 2048):
+        Z[t:t + 2048] = N(min(2048, T - t), V)
+    ids, lp = torch.empty((T, K), dtype=torch.int64, device="cuda"), torch.empty((T, K), device="cuda")
+    loss, dZ = torch.empty(T, device="cuda"), torch.empty_like(Z)
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    ws = tl.empty_logprob_workspace(T, V, K)
+    ms = timed(lambda: tl.tern_logprob(Z, ws, top_ids=ids, top_logp=lp, scale=0.5))
+    out["logprob_top"] = {"ms": round(ms, 4), "vocabulary": V, "k": K, **hbm(ms, 2 * T * V)}
+    ws = tl.empty_distill_workspace(T, V)
+    ms = timed(lambda: tl.tern_distill(Z, ws, targets=y, teacher_ids=ids, teacher_logp=lp, alpha=0.1, tau=2.0,
+                                       loss=loss, dZ=dZ))
+    out["distill"] = {"ms": round(ms, 4), "vocabulary": V, **hbm(ms, 4 * T * V)}
     return out
 
 

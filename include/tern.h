@@ -674,7 +674,7 @@ int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_
  *   K, teacher_ids, teacher_logp   0 to 64 entries (TERN_ERR_VALUE) a row: int64 and fp32
  *            [T, K], as tern_logprob with scale = 1 / tau writes them.  Entries with an
  *            id outside [0, V) or a logp of -inf are none; a token that is named twice
- *            has the sum of both.  A row without entries has no KL.
+ *            is two entries (and its dZ loses both p).  A row without entries has no KL.
  *   alpha    0 to 1 (a part whose factor is 0 is left out, whatever it would be);
  *   tau      above 0 and finite (TERN_ERR_VALUE).
  *   loss     fp32 [T], or NULL.

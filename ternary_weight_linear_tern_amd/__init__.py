@@ -991,7 +991,7 @@ def tern_norm_fwd(X, Y, w=None, b=None, A=None, S=None, stats=None, eps: float =
     wp, bp = _vector(fn, "w", w, (C,), torch.float32, dev), _vector(fn, "b", b, (C,), torch.float32, dev)
     st = _vector(fn, "stats", stats, (T, 2), torch.float32, dev)
     _on_gpu(fn, dev, X)
-    _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, eps, T, C, s, lds, y, ldy, yd, st)
+    _call(fn, dev, stream, x, ldx, xd, a, lda, ad, wp, bp, float(eps), T, C, s, lds, y, ldy, yd, st)
 
 
 def tern_norm_bwd(S, stats, dY, dX, workspace=None, w=None, dS=None, dw=None, db=None, stream=None) -> None:
@@ -1060,7 +1060,7 @@ def tern_logprob(Z, workspace=None, tokens=None, logp=None, entropy=None, lse=No
     en, ls = _vector(fn, "entropy", entropy, (T,), torch.float32, dev), _vector(fn, "lse", lse, (T,), torch.float32, dev)
     ws, n = _work(fn, workspace, dev)
     _on_gpu(fn, dev, Z)
-    _call(fn, dev, stream, z, ld, zd, scale, T, V, tok, lt, en, ls, k, ids, lp, ws, n)
+    _call(fn, dev, stream, z, ld, zd, float(scale), T, V, tok, lt, en, ls, k, ids, lp, ws, n)
 
 
 def tern_distill_workspace_bytes(T: int, V: int) -> int:
@@ -1092,7 +1092,7 @@ def tern_distill(Z, workspace=None, targets=None, teacher_ids=None, teacher_logp
     lo = _vector(fn, "loss", loss, (T,), torch.float32, dev)
     ws, n = _work(fn, workspace, dev)
     _on_gpu(fn, dev, Z)
-    _call(fn, dev, stream, z, ld, zd, T, V, y, K, ids, lp, alpha, tau, dl, lo, dz, lddz, ws, n)
+    _call(fn, dev, stream, z, ld, zd, T, V, y, K, ids, lp, float(alpha), float(tau), dl, lo, dz, lddz, ws, n)
 
 
 def tern_graph_begin(stream) -> None:

@@ -243,8 +243,8 @@ __device__ inline Sums join_sums(const DistillArgs &a, int64_t t, float c, Kind 
     const float m = wave_all<Max>(r.x);
     Sums q;
     q.m0 = m == -kInf ? 0.0f : m;
-    q.st = wave_all<Add>(r.z * exp2_((r.x - q.m0) * c));
-    q.s1 = kind == kOne ? q.st : wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1));
+    q.st = at_least_one(wave_all<Add>(r.z * exp2_((r.x - q.m0) * c)));
+    q.s1 = kind == kOne ? q.st : at_least_one(wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)));
     return q;
 }
 
@@ -287,7 +287,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
             float m;
             largest_and_sums(row, a.V, m, q.s1, q.st);
             q.m0 = m == -kInf ? 0.0f : m;
-            if (kind == kOne) q.s1 = q.st;
+            q.st = at_least_one(q.st);
+            q.s1 = kind == kOne ? q.st : at_least_one(q.s1);
         } else {
             float M = -kInf, s1 = 0.0f, st = 0.0f;   // of the segments so far
             for (int first = begin; first < end; first += a.seg) {
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
                 M = both;
                 meet<W>();
             }
-            q = Sums{M == -kInf ? 0.0f : M, kind == kOne ? st : s1, st};
+            q = Sums{M == -kInf ? 0.0f : M, at_least_one(kind == kOne ? st : s1), at_least_one(st)};
             if (PHASE == 1 && tid == 0) a.sums[item] = float4{M, s1, st, 0.0f};
         }
         if (PHASE != 1) {

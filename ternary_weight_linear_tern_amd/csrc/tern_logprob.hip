@@ -266,10 +266,14 @@ struct RowEnd {
     __device__ float log_p(float z) const { return s == 0.0f ? -kInf : (z - m0) * scale - logs; }
 };
 __device__ inline RowEnd finish_row(const LogprobArgs &a, int64_t t, float m0, float s, float u, int tid) {
+    s = at_least_one(s);
     RowEnd r{m0, s, logf(s), a.scale};
     if (tid == 0) {
         if (a.lse) a.lse[t] = fmaf(m0, a.scale, r.logs);
-        if (a.entropy) a.entropy[t] = s == 0.0f ? 0.0f : r.logs - u / s * kLn2;
+        if (a.entropy) {
+            const float h = r.logs - u / s * kLn2;
+            a.entropy[t] = s == 0.0f || h < 0.0f ? 0.0f : h;
+        }
     }
     return r;
 }

@@ -18,7 +18,7 @@
 #include "tern_rows.h"
 
 namespace tern {
-namespace ndev {
+namespace ldev {
 
 using namespace rows;
 
@@ -415,12 +415,12 @@ __global__ __launch_bounds__(32 * kStrands) void norm_dw_sum_kernel(const float 
     if (out) out[c < C ? c : c - C] = (float)s;
 }
 
-}  // namespace ndev
+}  // namespace ldev
 
 namespace {
 
-using ndev::BwdArgs;
-using ndev::FwdArgs;
+using ldev::BwdArgs;
+using ldev::FwdArgs;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool misaligned(const void *p) { return ((uintptr_t)p & 15u) != 0; }
@@ -437,7 +437,7 @@ struct RowShape {
     int W, CV, P;
 };
 RowShape shape_of(int64_t C) {
-    const int64_t most = ndev::kMaxWaves * 512;
+    const int64_t most = ldev::kMaxWaves * 512;
     if (C <= 512) return {1, 1, C <= 64 ? 8 : C <= 128 ? 16 : C <= 256 ? 32 : 64};
     if (C <= most) return {(int)cdiv(C, 512), 1, 64};
     if (C <= 2 * most) return {(int)cdiv(C, 1024), 2, 64};
@@ -449,7 +449,7 @@ int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std:
 // Row groups of the backward, a workgroup each.
 int64_t groups_of(int64_t T, int64_t C) {
     const RowShape s = shape_of(C);
-    return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(T, rows_at_once(s, ndev::kTogether))));
+    return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(T, rows_at_once(s, ldev::kTogether))));
 }
 
 // f with a type code as a compile-time constant
@@ -496,15 +496,15 @@ int tern_norm_fwd(const void *X, int64_t ldx, int32_t x_dtype, const void *A, in
         with_type(y_dtype, [&](auto yd) {
             constexpr int XD = decltype(xd)::value, YD = decltype(yd)::value;
             if (shape.W == 0) {
-                hipLaunchKernelGGL((ndev::norm_fwd_kernel<XD, YD>), dim3((unsigned)std::min<int64_t>(T, 65536)),
+                hipLaunchKernelGGL((ldev::norm_fwd_kernel<XD, YD>), dim3((unsigned)std::min<int64_t>(T, 65536)),
                                    dim3(256), 0, st, a);
                 return;
             }
             const int R = rows_at_once(shape, 4);
             const dim3 g((unsigned)std::min<int64_t>(cdiv(T, R), 2048)), bl(shape.P * shape.W * R);
-            if (shape.P < 64) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1, true>), g, bl, 0, st, a);
-            else if (shape.CV == 1) hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 1, false>), g, bl, 0, st, a);
-            else hipLaunchKernelGGL((ndev::norm_fwd_rows_kernel<XD, YD, 2, false>), g, bl, 0, st, a);
+            if (shape.P < 64) hipLaunchKernelGGL((ldev::norm_fwd_rows_kernel<XD, YD, 1, true>), g, bl, 0, st, a);
+            else if (shape.CV == 1) hipLaunchKernelGGL((ldev::norm_fwd_rows_kernel<XD, YD, 1, false>), g, bl, 0, st, a);
+            else hipLaunchKernelGGL((ldev::norm_fwd_rows_kernel<XD, YD, 2, false>), g, bl, 0, st, a);
         });
     });
     return launched();
@@ -550,26 +550,26 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
                     constexpr int DX = decltype(xd)::value;
                     if constexpr (DX == TERN_F32 || SD == TERN_BF16) {
                         if (shape.W == 0) {
-                            hipLaunchKernelGGL((ndev::norm_dx_kernel<SD, DY, DX>),
+                            hipLaunchKernelGGL((ldev::norm_dx_kernel<SD, DY, DX>),
                                                dim3((unsigned)std::min<int64_t>(T, 65536)), dim3(256), 0, st, a);
                             return;
                         }
-                        const dim3 g((unsigned)groups), bl(shape.P * shape.W * rows_at_once(shape, ndev::kTogether));
+                        const dim3 g((unsigned)groups), bl(shape.P * shape.W * rows_at_once(shape, ldev::kTogether));
                         if (shape.P < 64)
-                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1, true>), g, bl, 0, st, a);
+                            hipLaunchKernelGGL((ldev::norm_bwd_rows_kernel<SD, DY, DX, 1, true>), g, bl, 0, st, a);
                         else if (shape.CV == 1)
-                            hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 1, false>), g, bl, 0, st, a);
-                        else hipLaunchKernelGGL((ndev::norm_bwd_rows_kernel<SD, DY, DX, 2, false>), g, bl, 0, st, a);
+                            hipLaunchKernelGGL((ldev::norm_bwd_rows_kernel<SD, DY, DX, 1, false>), g, bl, 0, st, a);
+                        else hipLaunchKernelGGL((ldev::norm_bwd_rows_kernel<SD, DY, DX, 2, false>), g, bl, 0, st, a);
                     }
                 });
                 if (weights && shape.W == 0)
-                    hipLaunchKernelGGL((ndev::norm_dw_kernel<SD, DY>), dim3(cols, (unsigned)groups), dim3(64), 0, st, a);
+                    hipLaunchKernelGGL((ldev::norm_dw_kernel<SD, DY>), dim3(cols, (unsigned)groups), dim3(64), 0, st, a);
             });
         });
     }
     if (weights)
-        hipLaunchKernelGGL(ndev::norm_dw_sum_kernel, dim3((unsigned)cdiv(2 * C, 32)),
-                           dim3(32 * ndev::kStrands), 0, st, a.part,
+        hipLaunchKernelGGL(ldev::norm_dw_sum_kernel, dim3((unsigned)cdiv(2 * C, 32)),
+                           dim3(32 * ldev::kStrands), 0, st, a.part,
                            T > 0 ? (int)groups : 0, a.C, dw, db);
     return launched();
 }

@@ -197,6 +197,10 @@ struct Exponent {
     __device__ float of(float z) const { return fmaf(z, c, -mc); }
 };
 
+// A row's sum of exponentials, to which its largest element gives 1 (nothing allowed:
+// 0): a rounding below that would make a probability above 1.
+__device__ inline float at_least_one(float s) { return s > 0.0f && s < 1.0f ? 1.0f : s; }
+
 template <int DT>
 __device__ inline float at(const char *z, int64_t v) { return load1<DT>(z + v * esize<DT>()); }
 

@@ -104,6 +104,38 @@ def test_hard_rows(V, dt):
     check(hard_rows(V, dt, 40), k=20, tag=f"{V} {dt} many")
 
 
+@pytest.mark.parametrize("V", [2000, 30000, 131072, 500000])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_alternatives_close_together(V, dt):
+    """The large values stand in few places of every stride of 2048 (or 512), where the
+    lanes' largest elements say little of the others'; values that repeat; a few
+    tokens allowed among them."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    i = torch.arange(V, device="cuda")
+    R = lambda: torch.randn(V, generator=g, device="cuda")
+    rows = [torch.where(i % 2048 < 512, R(), R() - 20), torch.where(i % 512 < 64, R(), R() - 20),
+            torch.where(i % 2048 < 8, R(), -INF), torch.where(i % 2048 < 512, torch.round(R() * 2), -3.0),
+            torch.where(i // 8 % 256 < 66, i / V, -1.0), torch.where(i % 3 == 0, torch.round(R()), -INF)]
+    ld = (V + 7) // 8 * 8
+    buf = torch.zeros(len(rows), ld, dtype=dt, device="cuda")
+    for t, r in enumerate(rows):
+        buf[t, :V] = r.to(dt)
+    for k in (1, 2, 33, 64):
+        check(buf[:, :V], k=k, tag=f"{V} {dt} top {k}")
+        check(buf.repeat(100, 1)[:, :V], k=k, tag=f"{V} {dt} top {k}, many")
+
+
+@pytest.mark.parametrize("V", [256, 50021, 200000])
+def test_certain_rows(V):
+    """One token has next to all probability: no log probability above 0, no entropy below."""
+    for gap in (5.0, 15.0, 30.0, 100.0):
+        Z = logits(5, V, 3, size=1e-3)
+        Z += 37.123
+        Z[:, V // 2] += gap
+        o = check(Z, k=3, tokens=torch.full((5,), V // 2, device="cuda"), tag=f"{V} {gap}")
+        assert bool((o["logp"] <= 0).all()) and bool((o["top_logp"] <= 0).all()) and bool((o["entropy"] >= 0).all())
+
+
 @pytest.mark.parametrize("V", [100, 3000, 131072])
 def test_non_finite_rows_stay_alone(V):
     Z = logits(7, V, 4)

@@ -207,6 +207,35 @@ def test_backward_against_differences():
         assert abs(float(q) - float(db[c])) < 1e-7 + 64 * ref.U * 30
 
 
+@pytest.mark.parametrize("T,C", [(1, 64), (63, 64), (64, 64), (65, 8), (1000, 128), (777, 136), (300, 256), (40, 264)])
+def test_narrow_rows(T, C):
+    """Rows that take part of a wave: next to each other, and less than a workgroup has."""
+    w, b = rand((C,), 1, shift=1.0), rand((C,), 2)
+    check_fwd(rand((T, C), 3, F32, 2.0, 0.5), BF, w, b, A=rand((T, C), 4, BF), tag=f"{T} x {C}")
+    check_bwd(rand((T, C), 5, BF, 2.0, 0.5), BF, F32, w, ds=True, tag=f"{T} x {C}")
+
+
+def test_far_rows():
+    """Offsets past 2^31 elements: the last rows of a matrix of 2.3e9."""
+    T, C = 140000, 16384
+    tail, w = rand((3, C), 1, BF), rand((C,), 2)
+    X = torch.zeros(T, C, dtype=BF, device="cuda")
+    X[-3:] = tail
+    st = tl.empty_norm_stats(T)
+    Y = torch.full((T, C), 9.0, dtype=BF, device="cuda")
+    tl.tern_norm_fwd(X, Y, w=w, stats=st)
+    want, _, wst = fwd(tail, BF, w)
+    assert torch.equal(Y[-3:], want) and torch.equal(st[-3:], wst) and not bool(Y[:4].any())
+    dw, db = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    dY = X                                            # zero but for the last rows
+    tl.tern_norm_bwd(X, st, dY, Y, tl.empty_norm_workspace(T, C), w=w, dw=dw, db=db)
+    dX, gw, gb, e, ew, eb = ref.norm_bwd(tail, wst, w, tail, None)
+    ref.assert_within(Y[-3:], dX, e + ref.half_step(BF) * (dX.abs() + e), "dX")
+    ref.assert_within(dw, gw, ew, "dw")
+    ref.assert_within(db, gb, eb, "db")
+    assert not bool(Y[:4].any())
+
+
 def test_repeats_bitwise():
     S, w = rand((3000, 1032), 1, BF), rand((1032,), 2)
     first = check_bwd(S, BF, BF, w)

@@ -6,10 +6,10 @@
 //   xh = (S - mu) r,  g = dY w:
 //   dX = dS + r (g - mean g - xh mean (g xh)),  dw = sum_t dY xh,  db = sum_t dY
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/tern.h"
@@ -394,8 +394,8 @@ __global__ __launch_bounds__(64) void norm_dw_kernel(BwdArgs a) {
 }
 
 // The groups' sums: 32 columns a workgroup, of [2][C]; 32 strands of groups, each in
-// order, then the strands.  (512 groups of 1032
-// columns: 3.0 us, with 8 strands 4.8.)
+// order, then the strands.  (512 groups of 1032 columns: 3.0 us, with 8 strands 4.8;
+// a number of strands chosen by the groups costs 0.4 us in every call.)
 constexpr int kStrands = 32;
 __global__ __launch_bounds__(32 * kStrands) void norm_dw_sum_kernel(const float *part, int groups, int C, float *dw,
                                                                     float *db) {
@@ -446,10 +446,15 @@ RowShape shape_of(int64_t C) {
 // rows of a workgroup of about `waves` waves
 int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std::max(s.W, 1)) * (64 / s.P); }
 
-// Row groups of the backward, a workgroup each.
+// Row groups of the backward, a workgroup each: at most 512, which fill the chip.
+// With few long rows the groups' sums are as large as the rows: a group that takes
+// `turns` times its rows costs about 2 us a turn and saves 16 C bytes of sums, written and
+// read, so that their total is least at turns^2 = 16 C T / (R 4.9 TB/s 2 us).  (bf16, 300
+// rows of 16384: 32 us with a group each, 26 with this; 1000 rows 57 and 49.)
 int64_t groups_of(int64_t T, int64_t C) {
-    const RowShape s = shape_of(C);
-    return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(T, rows_at_once(s, ldev::kTogether))));
+    const int64_t R = rows_at_once(shape_of(C), ldev::kTogether);
+    const int64_t turns = std::max<int64_t>(1, (int64_t)std::sqrt(1.6e-6 * (double)T * (double)C / (double)R));
+    return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(T, R * turns)));
 }
 
 // f with a type code as a compile-time constant

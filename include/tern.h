@@ -610,7 +610,8 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
  *            asked for.  Calls that may run at the same time need one each.
  * Statistics and sums are fp32 (mu first, then the squares of the differences);
  * the order of every sum is fixed: repeated calls are bitwise identical.  A row
- * with a non-finite value spoils its own rows of the outputs, and its columns of dw, db.
+ * with a non-finite value spoils its own row of S, Y, stats and dX, and what sums over
+ * rows: dw, and db where it is dY's.
  * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
  */
 size_t tern_norm_bwd_workspace_bytes(int64_t T, int64_t C);

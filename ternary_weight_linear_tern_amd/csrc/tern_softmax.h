@@ -213,6 +213,8 @@ __device__ inline float at(const char *z, int64_t v) { return load1<DT>(z + v * 
 // Eights a lane holds at most: 64 registers.
 constexpr int held(int32_t dt) { return dt == TERN_BF16 ? 16 : 8; }
 constexpr int kMaxSegments = 64;
+// workgroups of a launch; they go on to further rows
+constexpr int64_t kMaxGroups = 1 << 16;
 
 struct RowPlan {
     int S, W, NV;        // parts of a row, a workgroup (or wave) each; its waves, and eights of a lane

@@ -207,6 +207,28 @@ def test_far_rows():
     assert bool((loss[:-3] == 0).all()) and not bool(Z[:4].any())
 
 
+@pytest.mark.parametrize("T,V", [(300000, 64), (70000, 5003), (66000, 8200), (65600, 33000), (65600, 65608)])
+def test_more_rows_than_workgroups(T, V):
+    """Workgroups go on to further rows: equal rows but for the last ones, in place."""
+    ld = (V + 7) // 8 * 8
+    tail = logits(5, V, 2, BF)
+    Z = torch.zeros(T, ld, dtype=BF, device="cuda")[:, :V]
+    Z[-5:] = tail
+    i5, l5 = teacher(5, V, 7, 1)
+    ids, lp = i5[:1].repeat(T, 1), l5[:1].repeat(T, 1)
+    ids[-5:], lp[-5:] = i5, l5
+    y = torch.full((T,), 5, device="cuda")
+    y[-5:] = targets_of(5, V)
+    w = torch.full((T,), 0.5, device="cuda")
+    loss, dZ = run(Z, y, ids, lp, 0.3, 1.5, w, in_place=True)
+    L, le, G, ge = ref.distill(tail, y[-5:], i5, l5, 0.3, 1.5, w[-5:])
+    ref.assert_within(loss[-5:], L, le, "loss")
+    ref.assert_within(dZ[-5:], G, ge + ref.half_step(BF) * (G.abs() + ge), "dZ")
+    assert bool((loss[:-5] == loss[0]).all())
+    for t in range(0, T - 5, 8192):
+        assert bool((dZ[t:min(t + 8192, T - 5)] == dZ[:1]).all())
+
+
 @pytest.mark.parametrize("T,V", [(3, 131072), (700, 50024), (4000, 256)])
 def test_repeats_bitwise(T, V):
     Z, y = logits(T, V, 1, BF), targets_of(T, V)

@@ -182,6 +182,22 @@ def test_far_rows():
     assert torch.equal(a["top_ids"][0], torch.tensor([0, 1], device="cuda"))
 
 
+@pytest.mark.parametrize("T,V", [(300000, 64), (70000, 5003), (66000, 8200), (65600, 40000)])
+def test_more_rows_than_workgroups(T, V):
+    """Workgroups go on to further rows: equal rows but for the last ones."""
+    ld = (V + 7) // 8 * 8
+    tail = logits(5, V, 2, BF)
+    Z = logits(1, V, 3, BF).repeat(T, 1) if V % 8 == 0 else torch.zeros(T, ld, dtype=BF, device="cuda")[:, :V]
+    Z[-5:] = tail
+    a, b = run(Z, k=3), run(tail, k=3)
+    want = ref.logprob(tail, 1.0, None, 3)
+    assert torch.equal(a["top_ids"][-5:], want["top_ids"])
+    for name in ("lse", "entropy", "top_logp"):
+        ref.assert_within(a[name][-5:], *want[name], tag=name)
+        assert bool((a[name][:-5] == a[name][:1]).all())
+    assert bool((a["top_ids"][:-5] == a["top_ids"][:1]).all())
+
+
 @pytest.mark.parametrize("T,V", [(3, 131072), (700, 50024), (4000, 256)])
 def test_repeats_bitwise(T, V):
     Z = logits(T, V, 1, BF)

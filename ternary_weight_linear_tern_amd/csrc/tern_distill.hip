@@ -57,6 +57,7 @@ struct Names {
     float z[kEntries];        // their logits
     float less[kEntries];     // what the gradient loses there, before dloss
     float p[kEntries], logp[kEntries];   // the teacher's
+    uint8_t place[1024];      // which entry wrote here last, by its token's last ten bits
     bool kl, ce;
 };
 
@@ -86,14 +87,21 @@ __device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z
     float p = id < 0 ? 0.0f : exp2_((lp - lm) * a.c1);
     const float ps = wave_all<Add>(p);
     p = id < 0 ? 0.0f : p / ps;
-    // a token that is named twice loses the sum, wherever it stands; the order of the sum is the entries'
     const int me = (int)id, target = (int)y;
-    float mine = 0.0f, its = 0.0f;
-    for (int j = 0; j < a.K; j++) {
-        const int o = __builtin_amdgcn_readlane(me, j);
-        const float q = as_f(__builtin_amdgcn_readlane(as_u(p), j));
-        mine += o == me ? q : 0.0f;
-        its += o == target ? q : 0.0f;
+    if (me >= 0) e.place[me & 1023] = (uint8_t)lane;
+    meet<1>();
+    float mine = p, its = 0.0f;
+    if (__ballot(me >= 0 && e.place[me & 1023] != lane)) {
+        // a token that is named twice (or two that share a place) loses the sum, in the order of the entries
+        mine = 0.0f;
+        for (int j = 0; j < a.K; j++) {
+            const int o = __builtin_amdgcn_readlane(me, j);
+            const float q = as_f(__builtin_amdgcn_readlane(as_u(p), j));
+            mine += o == me ? q : 0.0f;
+            its += o == target ? q : 0.0f;
+        }
+    } else {
+        its = wave_all<Add>(me == target ? p : 0.0f);   // one entry at most
     }
     const float f = (1.0f - a.alpha) * a.tau;
     e.id[lane] = me;

@@ -61,33 +61,42 @@ struct Names {
     bool kl, ce;
 };
 
-// By the first wave of a row.  `z` is the row (its logits are read where `cut` is not
-// set: in a row that is cut they come from the workspace).
-template <int DT>
-__device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z, Names &e, int lane, bool cut) {
-    int64_t id = -1;
+// An entry of a row as the caller gives it (-1 and -inf: none), and the row's target.
+struct Given {
+    int id, target;
+    float lp;
+};
+__device__ inline Given given(const DistillArgs &a, int64_t t, int lane) {
+    int64_t id = -1, y = a.ce ? a.targets[t] : -1;
     float lp = -kInf;
     if (a.kl && lane < a.K) {
         id = a.ids[t * a.K + lane];
         lp = a.lp[t * a.K + lane];
-        if (id < 0 || id >= a.V || lp == -kInf) id = -1, lp = -kInf;
     }
-    int64_t y = a.ce ? a.targets[t] : -1;
-    if (y < 0 || y >= a.V) y = -1;
+    if (id < 0 || id >= a.V || lp == -kInf) id = -1, lp = -kInf;
+    return Given{(int)id, y >= 0 && y < a.V ? (int)y : -1, lp};
+}
+
+// By the first wave of a row.  `z` is the row (its logits are read where `cut` is not
+// set: in a row that is cut they come from the workspace).
+template <int DT>
+__device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z, const Given &in, Names &e, int lane,
+                                  bool cut) {
+    const int me = in.id, target = in.target;
+    const float lp = in.lp;
     float zid = 0.0f, zy = 0.0f;
     if (cut) {
-        if (id >= 0) zid = a.named[t * kEntries + lane];
-        if (y >= 0) zy = a.named[t * kEntries + kEntries - 1];
+        if (me >= 0) zid = a.named[t * kEntries + lane];
+        if (target >= 0) zy = a.named[t * kEntries + kEntries - 1];
     } else {
-        if (id >= 0) zid = at<DT>(z, id);
-        if (y >= 0) zy = at<DT>(z, y);
+        if (me >= 0) zid = at<DT>(z, me);
+        if (target >= 0) zy = at<DT>(z, target);
     }
-    const bool kl = __ballot(id >= 0) != 0;
+    const bool kl = __ballot(me >= 0) != 0;
     const float lm = wave_all<Max>(lp);
-    float p = id < 0 ? 0.0f : exp2_((lp - lm) * a.c1);
+    float p = me < 0 ? 0.0f : exp2_((lp - lm) * a.c1);
     const float ps = wave_all<Add>(p);
-    p = id < 0 ? 0.0f : p / ps;
-    const int me = (int)id, target = (int)y;
+    p = me < 0 ? 0.0f : p / ps;
     if (me >= 0) e.place[me & 1023] = (uint8_t)lane;
     meet<1>();
     float mine = p, its = 0.0f;
@@ -107,7 +116,7 @@ __device__ inline void read_names(const DistillArgs &a, int64_t t, const char *z
     e.id[lane] = me;
     e.z[lane] = zid;
     e.p[lane] = p;
-    e.logp[lane] = id < 0 ? 0.0f : lp - lm - logf(ps);
+    e.logp[lane] = me < 0 ? 0.0f : lp - lm - logf(ps);
     e.less[lane] = kl ? fmaf(f, mine, me == target ? a.alpha : 0.0f) : 0.0f;
     if (lane == 0) {
         e.id[kEntries - 1] = target;
@@ -291,13 +300,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
             sums_of<DT, W, NV>(z, x, n, Exponents(m0, c, a.c1, kind), kind, tid, s1, st);
             row_sums<W>(s1, st, &sh[1], tid);
         };
+        // the row's names before the row: loads come back in order, and the first wave needs them for
+        // further ones (which the others wait for)
+        Given names_in{};
+        if (tid < 64) names_in = given(a, t, lane);
+        __builtin_amdgcn_sched_barrier(0);
         if (PHASE == 2) {
             load_row<DT, W, NV>(row + (int64_t)begin * esize<DT>(), end - begin, tid, x);
-            if (tid < 64) read_names<DT>(a, t, row, e, lane, true);
+            if (tid < 64) read_names<DT>(a, t, row, names_in, e, lane, true);
             q = join_sums(a, t, c, kind, lane);
         } else if (PHASE == 0) {
             load_row<DT, W, NV>(row, a.V, tid, x);
-            if (tid < 64) read_names<DT>(a, t, row, e, lane, false);
+            if (tid < 64) read_names<DT>(a, t, row, names_in, e, lane, false);
             float m;
             largest_and_sums(row, a.V, m, q.s1, q.st);
             q.m0 = m == -kInf ? 0.0f : m;
@@ -311,12 +325,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
                 load_row<DT, W, NV>(z, n, tid, x);
                 if (first == begin && tid < 64) {
                     if (PHASE == 3) {
-                        read_names<DT>(a, t, row, e, lane, false);
+                        read_names<DT>(a, t, row, names_in, e, lane, false);
                     } else {   // the logits of the tokens that are named of this part
-                        const int64_t id = a.kl && lane < a.K ? a.ids[t * a.K + lane] : -1;
-                        if (id >= begin && id < end) a.named[t * kEntries + lane] = at<DT>(row, id);
-                        const int64_t y = a.ce && lane == 0 ? a.targets[t] : -1;
-                        if (y >= begin && y < end) a.named[t * kEntries + kEntries - 1] = at<DT>(row, y);
+                        const int v = names_in.id, y = names_in.target;
+                        if (v >= begin && v < end) a.named[t * kEntries + lane] = at<DT>(row, v);
+                        if (lane == 0 && y >= begin && y < end)
+                            a.named[t * kEntries + kEntries - 1] = at<DT>(row, y);
                     }
                 }
                 float m, p1, pt;
@@ -348,7 +362,7 @@ __global__ __launch_bounds__(64) void distill_loss_kernel(DistillArgs a) {
     __shared__ Names e;
     const int lane = threadIdx.x;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        read_names<DT>(a, t, nullptr, e, lane, true);
+        read_names<DT>(a, t, nullptr, given(a, t, lane), e, lane, true);
         const Sums q = join_sums(a, t, a.kl ? a.ct : a.c1, kind_of(a), lane);
         meet<1>();
         write_loss(a, t, e, q, lane);

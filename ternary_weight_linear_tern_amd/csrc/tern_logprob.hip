@@ -284,11 +284,22 @@ __device__ inline RowEnd finish_row(const LogprobArgs &a, int64_t t, float m0, f
     return r;
 }
 
+// The row's token (-1: none to tell of) and its logit.  (Fetched ahead of a whole row it
+// costs registers and 1 to 8 per cent; where parts are joined it comes first.)
+struct Token {
+    int64_t id;
+    float z;
+};
 template <int DT>
-__device__ inline void token_of(const LogprobArgs &a, int64_t t, const RowEnd &r, int tid) {
-    if (!a.tokens || tid != 0) return;
-    const int64_t y = a.tokens[t];
-    a.logp[t] = y >= 0 && y < a.V ? r.log_p(at<DT>((const char *)a.Z + t * a.ld * esize<DT>(), y)) : 0.0f;
+__device__ inline Token token_of(const LogprobArgs &a, int64_t t, int tid) {
+    Token y{-1, 0.0f};
+    if (a.tokens && tid == 0) y.id = a.tokens[t];
+    if (y.id >= a.V) y.id = -1;
+    if (y.id >= 0) y.z = at<DT>((const char *)a.Z + t * a.ld * esize<DT>(), y.id);
+    return y;
+}
+__device__ inline void tell_token(const LogprobArgs &a, int64_t t, const RowEnd &r, const Token &y, int tid) {
+    if (a.tokens && tid == 0) a.logp[t] = y.id >= 0 ? r.log_p(y.z) : 0.0f;
 }
 
 // s = sum e, u = sum e d over a lane's elements, m0 the segment's largest
@@ -353,7 +364,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
         const int l = fresh(tid);
         if (a.S == 1) {
             const RowEnd r = finish_row(a, t, M == -kInf ? 0.0f : M, s, u, l);
-            token_of<DT>(a, t, r, l);
+            tell_token(a, t, r, token_of<DT>(a, t, l), l);
             if (l < a.k) {
                 a.top_ids[t * a.k + l] = index_of(pick.top[l]);
                 a.top_logp[t * a.k + l] = r.log_p(value_of(pick.top[l]));
@@ -375,12 +386,13 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const Token y = token_of<DT>(a, t, tid);
         float4 q = lane < a.S ? a.sums[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
         const float m = wave_all<Max>(q.x), m0 = m == -kInf ? 0.0f : m;
         const float d = (q.x - m0) * a.c, f = exp2_(d);
         const float s = wave_all<Add>(f * q.y), u = wave_all<Add>(f * fmaf(q.y, fmaxf(d, -200.0f), q.z));
         const RowEnd r = finish_row(a, t, m0, s, u, tid);
-        token_of<DT>(a, t, r, tid);
+        tell_token(a, t, r, y, tid);
         if (!a.k) continue;
         const uint64_t *keys = a.keys + t * a.S * a.k;
         const int rank = (a.k + a.S - 1) / a.S - 1;

@@ -10,7 +10,8 @@
 // elements reach, and hardly more do; a bisection over its bits by one wave finds
 // it.  The eights that hold an element which reaches it go to a list in shared
 // memory, their elements that do to another, and each one's place is the
-// number of greater keys there.  Where a list would overflow (ties, rows in which
+// number of greater keys there.  One alternative is the first element that equals the
+// row's largest, without lists.  Where a list would overflow (ties, rows in which
 // fewer than k tokens are allowed) the k-th largest value is found itself, by the same
 // bisection over all elements unless the bound is it, and then the elements above it
 // and the first of those equal to it, by their index.
@@ -86,7 +87,6 @@ __device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
 #pragma unroll
     for (int i = 1; i < G / 64; i++) most = max(most, g[i]), least = min(least, g[i]);
     most = wave_all_u<MaxU>(most);
-    if (k == 1) return most;
     if (k > G) return 0;
     auto reach = [&](uint32_t t) {
         int c = 0;
@@ -211,6 +211,35 @@ __device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first
         }
     }
     meet<W>();
+}
+
+// The largest alone: the first of a segment's elements that equal its largest, m, and the
+// one that p.top holds where one is had.  (A row of nothing but NaN: its first.)
+template <int DT, int W, int NV>
+__device__ inline int first_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t first, int had, float mine, float m,
+                                       Pick<DT, W> &p, int tid) {
+    tid = fresh(tid);
+    if (tid == 0) p.bound = 0xFFFFFFFFu;
+    meet<W>();
+    if (__ballot(mine == m)) {
+        uint32_t at = 0xFFFFFFFFu;
+        each8<DT, W, NV>(x, n, [&](int i, const float *f) {
+            if (max8(f) < m) return;
+#pragma unroll
+            for (int j = 7; j >= 0; j--) {
+                const uint32_t v = i * W * 512 + tid * 8 + j;
+                if (f[j] == m && v < (uint32_t)n) at = min(at, v);
+            }
+        });
+        if (at != 0xFFFFFFFFu) atomicMin(&p.bound, at);
+    }
+    meet<W>();
+    if (tid == 0) {
+        const uint64_t key = key_of(m, first + (p.bound == 0xFFFFFFFFu ? 0 : p.bound));
+        p.top[0] = had ? max(p.top[0], key) : key;
+    }
+    meet<W>();
+    return 1;
 }
 
 // The k largest (fewer where there are not so many) of the segment in x, n elements
@@ -358,7 +387,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
             u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
             s = f0 * s + f1 * s1;
             M = both;
-            if (a.k) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);
+            if (a.k == 1) had = first_of_segment<DT, W, NV>(x, n, first, had, mine, m, pick, tid);
+            else if (a.k) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);
             meet<W>();
         }
         const int l = fresh(tid);

@@ -7,6 +7,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,23 +30,32 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def build(out: str = LIB, verbose: bool = False, save_temps_dir: str | None = None) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), *DEVICE_FLAGS, *srcs, "-o", out + ".tmp"]
-    if save_temps_dir:
-        cmd[1:1] = ["-save-temps=obj"]
-    env = dict(os.environ)
-    r = subprocess.run(cmd, capture_output=True, text=True, env=env,
-                       cwd=save_temps_dir or None)
+def _run(cmd: list, cwd: str | None = None) -> str:
+    """Run a compiler command; returns what it says on stderr, raises where it fails."""
+    r = subprocess.run(cmd, capture_output=True, text=True, cwd=cwd)
     # hipcc's host pass does not know the device-only feature flag; drop that note
     noise = "'-packed-fp32-ops' is not a recognized feature for this target (ignoring feature)"
     err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
     if r.returncode != 0:
         sys.stderr.write(err + "\n")
         raise RuntimeError(f"hipcc failed ({r.returncode}): {' '.join(cmd)}")
-    if verbose and err.strip():
-        sys.stderr.write(err + "\n")
+    return err
+
+
+def build(out: str = LIB, verbose: bool = False, save_temps_dir: str | None = None) -> str:
+    """Compile every source, several at a time, and link the library."""
+    common = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC"]
+    if save_temps_dir:
+        common += ["-save-temps=obj"]
+    jobs = max(1, min(int(os.environ.get("MAX_JOBS") or 8), os.cpu_count() or 1, len(SOURCES)))
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(jobs) as pool:
+        objs = [os.path.join(save_temps_dir or tmp, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        cmds = [[*common, "-I", os.path.join(ROOT, "include"), *DEVICE_FLAGS, "-c", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objs)]
+        errs = list(pool.map(lambda c: _run(c, save_temps_dir), cmds))
+        errs.append(_run([*common, "-shared", *objs, "-o", out + ".tmp"], save_temps_dir))
+    if verbose and "".join(errs).strip():
+        sys.stderr.write("\n".join(e for e in errs if e.strip()) + "\n")
     os.replace(out + ".tmp", out)
     return out
 

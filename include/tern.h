@@ -634,7 +634,8 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
  *
  *   Z        [T, V] of z_dtype (TERN_F32 or TERN_BF16), row stride ld (elements, a
  *            multiple of 8, >= V).  V from 1 to 2^20, any number.  T >= 0.
- *   scale    1 / temperature, above 0 and finite (TERN_ERR_VALUE).
+ *   scale    1 / temperature, above 0 and finite (TERN_ERR_VALUE).  An lse beyond fp32's
+ *            range is infinite.
  *   tokens   int64 [T]; logp[t] is 0 for a token outside [0, V) (padding).  tokens
  *            and logp are both given or both NULL.
  *   entropy, lse   fp32 [T], or NULL.

@@ -207,4 +207,5 @@ def distill(Z, targets, ids, lp, alpha, tau, dloss):
     loss = torch.where(ce | kl, loss, zero)
     dZ = torch.where(gone[:, None], torch.zeros_like(G), G * w[:, None])
     # below 2^-126 a probability may be flushed to zero
-    return loss, le + U * torch.nan_to_num(loss, posinf=0.0).abs(), dZ, GE * w.abs()[:, None] + 2.0 ** -120
+    GE = torch.where(gone[:, None], torch.zeros_like(GE), GE * w.abs()[:, None])
+    return loss, torch.where(ce | kl, le + U * torch.nan_to_num(loss, posinf=0.0).abs(), zero), dZ, GE + 2.0 ** -120

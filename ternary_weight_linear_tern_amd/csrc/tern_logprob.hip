@@ -5,8 +5,8 @@
 //   s = sum e^d,  u = sum e^d d:  logp = d[token] - log s,  entropy = log s - u / s.
 // The exponentials are powers of two (d is carried in units of log 2).
 //
-// The k largest: 256 groups of lanes (64 where one wave has the row) know their
-// own largest element.  The k-th largest of those is a bound that at least k
+// The k largest: 256 groups of elements (64, a lane's each, where one wave has the row
+// and few are asked for) know their own largest element.  The k-th largest of those is a bound that at least k
 // elements reach, and hardly more do; a bisection over its bits by one wave finds
 // it.  The eights that hold an element which reaches it go to a list in shared
 // memory, their elements that do to another, and each one's place is the
@@ -49,16 +49,18 @@ struct LogprobArgs {
     uint64_t *keys;            // [T][S][k]: its alternatives, 0 behind the last
 };
 
-template <int DT, int W>
+// (Rows of one stride and wave have 64 eights, all of which their list holds.)
+template <int DT, int W, int NV>
 struct Pick {
-    static constexpr int kGroups = W >= 4 ? 256 : 64, kKeys = W >= 4 ? 1024 : 256, kEights = W >= 4 ? 512 : 128;
+    static constexpr int kKeys = W >= 4 ? 1024 : 256;
+    static constexpr int kEights = W >= 4 ? 512 : NV > 1 ? 128 : 64, kMasks = NV * W;
     uint64_t top[TERN_TOP_MAX];    // the largest so far, falling
     uint64_t key[kKeys];
     Raw8<DT> eight[kEights];
     int from[kEights];             // index of an eight's first element in its segment
-    uint64_t mask[64];             // lanes with an element equal to the k-th largest, stride by stride and wave by wave
-    int before[64];                // how many such lanes stand before a mask's
-    uint32_t group[kGroups];
+    uint64_t mask[kMasks];         // lanes with an element equal to the k-th largest, stride by stride and wave by wave
+    int before[kMasks];            // how many such lanes stand before a mask's
+    uint32_t group[W >= 4 ? W * 64 : 1];
     float sum[2][W];
     uint32_t bound;
     int keys, eights;
@@ -76,22 +78,18 @@ __device__ inline uint32_t wave_all_u(uint32_t x) {
     for (int d = 1; d < 64; d *= 2) x = Op::of(x, (uint32_t)__shfl_xor((int)x, d));
     return x;
 }
-// A bound that at least k of the groups' largest reach (0 where there are not k
-// groups), by one wave.
+// A bound that at least k of the groups' largest reach, by one wave, of whose lanes
+// each knows G of them (k <= 64 G).
 template <int G>
-__device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
-    uint32_t g[G / 64];
-#pragma unroll
-    for (int i = 0; i < G / 64; i++) g[i] = group[i * 64 + lane];
+__device__ inline uint32_t bound_of(const uint32_t (&g)[G], int k) {
     uint32_t most = g[0], least = g[0];
 #pragma unroll
-    for (int i = 1; i < G / 64; i++) most = max(most, g[i]), least = min(least, g[i]);
+    for (int i = 1; i < G; i++) most = max(most, g[i]), least = min(least, g[i]);
     most = wave_all_u<MaxU>(most);
-    if (k > G) return 0;
     auto reach = [&](uint32_t t) {
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < G / 64; i++) c += __builtin_popcountll(__ballot(g[i] >= t));
+        for (int i = 0; i < G; i++) c += __builtin_popcountll(__ballot(g[i] >= t));
         return c;
     };
     if (reach(most) >= k) return most;
@@ -111,14 +109,14 @@ __device__ inline uint32_t bound_of(const uint32_t *group, int k, int lane) {
 }
 
 // The elements that the listed eights hold, as keys: those that `take` says.
-template <int DT, int W, class F>
-__device__ inline void keys_of_eights(Pick<DT, W> &p, int eights, int n, uint32_t first, int tid, F take) {
+template <int DT, int W, int NV, class F>
+__device__ inline void keys_of_eights(Pick<DT, W, NV> &p, int eights, int n, uint32_t first, int tid, F take) {
     for (int q = tid; q < eights * 8; q += W * 64) {
         const int v = p.from[q >> 3] + (q & 7);
         const float f = at<DT>((const char *)&p.eight[q >> 3], q & 7);
         if (v < n && take(f)) {
             const int at = atomicAdd(&p.keys, 1);
-            if (at < Pick<DT, W>::kKeys) p.key[at] = key_of(f, first + v);
+            if (at < Pick<DT, W, NV>::kKeys) p.key[at] = key_of(f, first + v);
         }
     }
 }
@@ -127,8 +125,8 @@ __device__ inline void keys_of_eights(Pick<DT, W> &p, int eights, int n, uint32_
 // (of NaNs, as of infinities, any).  `bound` is reached by that many at least.
 template <int DT, int W, int NV>
 __device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first, int want, int had, uint32_t bound,
-                                  Pick<DT, W> &p, int tid) {
-    constexpr int ST = W * 512, kTies = TERN_TOP_MAX;   // ties stand behind 64 other eights
+                                  Pick<DT, W, NV> &p, int tid) {
+    constexpr int ST = W * 512, M = Pick<DT, W, NV>::kMasks;
     tid = fresh(tid);
     const int lane = tid & 63, wave = tid >> 6;
     auto number = [](float f) { return f != f ? kInf : f; };
@@ -159,7 +157,7 @@ __device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first
     const float v = from_ordered(value);
     meet<W>();
     if (tid == 0) p.keys = had, p.eights = 0;
-    if (tid < 64) p.mask[tid] = 0;
+    if (tid < M) p.mask[tid] = 0;
     meet<W>();
     each8<DT, W, NV>(x, n, [&](int i, const float *f) {
         bool over = false, equal = false;
@@ -177,31 +175,31 @@ __device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first
         }
     });
     meet<W>();
-    keys_of_eights<DT, W>(p, p.eights, n, first, tid, [&](float f) { return number(f) > v; });
+    keys_of_eights<DT, W, NV>(p, p.eights, n, first, tid, [&](float f) { return number(f) > v; });
     if (tid < 64) {
-        const int mine = __builtin_popcountll(p.mask[tid]);
+        const int mine = lane < M ? __builtin_popcountll(p.mask[lane]) : 0;
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int o = __shfl_up(sum, d);
             if (lane >= d) sum += o;
         }
-        p.before[tid] = sum - mine;
+        if (lane < M) p.before[lane] = sum - mine;
     }
     meet<W>();
     const int ties = want - more;
     each8<DT, W, NV>(x, n, [&](int i, const float *f) {
         const uint64_t m = p.mask[i * W + wave];
         const int rank = p.before[i * W + wave] + __builtin_popcountll(m & ((1ull << lane) - 1));
-        if ((m >> lane & 1) && rank < ties)
-            p.eight[kTies + rank] = x[i], p.from[kTies + rank] = i * ST + tid * 8;
+        if ((m >> lane & 1) && rank < ties)   // the list's other eights have been taken
+            p.eight[rank] = x[i], p.from[rank] = i * ST + tid * 8;
     });
     meet<W>();
     if (tid < 64) {   // the listed eights in order, 64 elements at a time
-        const int eights = min(ties, p.before[63] + __builtin_popcountll(p.mask[63]));
+        const int eights = min(ties, p.before[M - 1] + __builtin_popcountll(p.mask[M - 1]));
         int taken = 0;
         for (int q = tid; q < (eights * 8 + 63) / 64 * 64; q += 64) {
-            const int at8 = kTies + min(q >> 3, eights - 1), i = p.from[at8] + (q & 7);
+            const int at8 = min(q >> 3, eights - 1), i = p.from[at8] + (q & 7);
             const float f = at<DT>((const char *)&p.eight[at8], q & 7);
             const bool tie = q < eights * 8 && i < n && number(f) == v;
             const uint64_t m = __ballot(tie);
@@ -217,7 +215,7 @@ __device__ inline void exact_keys(const Raw8<DT> (&x)[NV], int n, uint32_t first
 // one that p.top holds where one is had.  (A row of nothing but NaN: its first.)
 template <int DT, int W, int NV>
 __device__ inline int first_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t first, int had, float mine, float m,
-                                       Pick<DT, W> &p, int tid) {
+                                       Pick<DT, W, NV> &p, int tid) {
     tid = fresh(tid);
     if (tid == 0) p.bound = 0xFFFFFFFFu;
     meet<W>();
@@ -247,23 +245,44 @@ __device__ inline int first_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t 
 // to p.top.  Returns how many there are.
 template <int DT, int W, int NV>
 __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t first, int k, int had, float mine,
-                                     Pick<DT, W> &p, int tid) {
-    using P = Pick<DT, W>;
-    constexpr int G = P::kGroups, PER = W * 64 / G, ST = W * 512;
+                                     Pick<DT, W, NV> &p, int tid) {
+    using P = Pick<DT, W, NV>;
+    constexpr int ST = W * 512;
     tid = fresh(tid);
-    float m = mine;
-    if constexpr (PER >= 2) m = fmaxf(m, dpp<0xB1>(m));
-    if constexpr (PER >= 4) m = fmaxf(m, dpp<0x4E>(m));
-    if (tid % PER == 0) p.group[tid / PER] = ordered(m);
     if (tid == 0) p.keys = had, p.eights = 0;
     for (int i = tid; i < had; i += W * 64) p.key[i] = p.top[i];
-    meet<W>();
-    if (tid < 64) {
-        const uint32_t b = bound_of<G>(p.group, k, tid);
-        if (tid == 0) p.bound = b;
+    uint32_t reached;
+    if constexpr (W == 1) {
+        // Groups of two where 64 would not do.  16384 rows of bf16, 64 groups and 256: of 512, 28
+        // alternatives 22.9 us and 24.5, 32: 26.3 and 25.1; of 256, 16: 21.0 and 22.8, 24: 47 and 24;
+        // of 4000, 64: 547 (the lists overflow) and 73.
+        if (n < 2 * k) {   // most are asked for, and all are compared: of 64, 64: 40 us with a search, 24 without
+            reached = ordered(-kInf);
+        } else if (2 * k < min(64, (n + 7) / 8)) {
+            const uint32_t g[1] = {ordered(mine)};
+            reached = bound_of(g, k);
+        } else {
+            float m[4] = {-kInf, -kInf, -kInf, -kInf};
+            each8<DT, W, NV>(x, n, [&](int, const float *f) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) m[j] = max3(m[j], f[2 * j], f[2 * j + 1]);
+            });
+            const uint32_t g[4] = {ordered(m[0]), ordered(m[1]), ordered(m[2]), ordered(m[3])};
+            reached = bound_of(g, k);
+        }
+        meet<W>();
+    } else {
+        static_assert(W == 4, "a group for each lane");
+        p.group[tid] = ordered(mine);
+        meet<W>();
+        if (tid < 64) {
+            const uint32_t g[4] = {p.group[tid], p.group[tid + 64], p.group[tid + 128], p.group[tid + 192]};
+            const uint32_t b = bound_of(g, k);
+            if (tid == 0) p.bound = b;
+        }
+        meet<W>();
+        reached = p.bound;
     }
-    meet<W>();
-    const uint32_t reached = p.bound;
     // the last of the k so far is a bound as well
     const float bound = from_ordered(had == k ? max(reached, (uint32_t)(p.top[k - 1] >> 32)) : reached);
     if (__ballot(!(mine < bound)))
@@ -275,7 +294,7 @@ __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t fi
     meet<W>();
     const int eights = p.eights;
     if (eights <= P::kEights)
-        keys_of_eights<DT, W>(p, eights, n, first, tid, [&](float f) { return !(f < bound); });
+        keys_of_eights<DT, W, NV>(p, eights, n, first, tid, [&](float f) { return !(f < bound); });
     meet<W>();
     const int want = min(k, had + n);
     int keys = p.keys;
@@ -354,10 +373,10 @@ __device__ inline void lane_sums(const char *z, const Raw8<DT> (&x)[NV], int n, 
 template <int DT, int W, int NV>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(LogprobArgs a) {
     constexpr int R = W == 1 ? 4 : 1;   // rows of a workgroup
-    __shared__ Pick<DT, W> picks[R];
+    __shared__ Pick<DT, W, NV> picks[R];
     __shared__ float sh[3][W];
     const int slot = R > 1 ? threadIdx.x >> 6 : 0, tid = R > 1 ? threadIdx.x & 63 : threadIdx.x;
-    Pick<DT, W> &pick = picks[slot];
+    Pick<DT, W, NV> &pick = picks[slot];
     const int64_t items = a.T * a.S;
     for (int64_t item = (int64_t)blockIdx.x * R + slot; item < items; item += (int64_t)gridDim.x * R) {
         const int64_t t = a.S == 1 ? item : item / a.S;

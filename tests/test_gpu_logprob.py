@@ -67,6 +67,19 @@ def test_many_rows(T, V, k):
     check(logits(T, V, k, BF), k=k, scale=0.5, tag=f"{T} x {V} k {k}")
 
 
+@pytest.mark.parametrize("V", [8, 64, 100, 127, 128, 250, 256, 512, 1000, 2000, 4000])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_alternatives_of_short_rows(V, dt):
+    """Rows of one wave (2100 of them): from few of its lanes' elements to most of the row."""
+    Z = logits(2100, V, V, dt)
+    Z[::5] = torch.round(Z[::5])                       # ties
+    Z[1::5, V // 3:] = -INF                            # a third is allowed
+    Z[2::5, 1:] = -INF
+    for k in sorted({min(V, k) for k in (2, 4, 15, 16, 17, 31, 32, 33, 50, 63, 64)}):
+        check(Z, k=k, tag=f"{V} {dt} top {k}")
+    check(hard_rows(V, dt, 150), k=min(V, 64), tag=f"{V} {dt} hard")
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.125, 1.7, 30.0])
 def test_scales(scale):
     check(logits(7, 5000, 1), k=9, scale=scale, tag=str(scale))

@@ -608,7 +608,8 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
  *   dw, db   fp32 [C], each may be NULL.
  *   workspace  at least tern_norm_bwd_workspace_bytes(T, C) bytes where dw or db is
  *            asked for.  Calls that may run at the same time need one each.
- * Statistics and sums are fp32 (mu first, then the squares of the differences);
+ * Statistics and sums are fp32 (mu first, then the squares of the differences, in
+ * other units where those pass fp32's range: rows may hold any finite numbers);
  * the order of every sum is fixed: repeated calls are bitwise identical.  A row
  * with a non-finite value spoils its own row of S, Y, stats and dX, and what sums over
  * rows: dw, and db where it is dY's.

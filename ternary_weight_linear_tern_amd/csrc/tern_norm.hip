@@ -116,8 +116,79 @@ struct Lanes {
         return (float)n;
     }
 };
+// Rows whose squares pass fp32's range (differences above about 1e19), told by sums that do, take
+// them of their values times 2^-80: squares of any differences, and sums of 2^20 of those, fit.
+constexpr float kFar = 0x1p-80f;
+constexpr float kFarSquares = 0x1p-33f, kFarSum = 0x1p47f;   // of those values: half of what passes the range
+constexpr float kInf = __builtin_inff();
+
+// xh = (x k - mu) r: a row's mean and 1 / deviation in units of 1 / k, in which the difference of any two
+// numbers and 1 / deviation fit: k is 1, or 1/16 for a far row (sq: of its values times 2^-80).
+struct RowStats {
+    float k, mu, r;
+    __device__ RowStats(float mean, float sq, float C, float eps, bool far) : k(1.0f), mu(mean) {
+        if (far) {
+            k = 0.0625f, mu = mean * 0x1p76f;
+            // deviation and sqrt(eps) times 2^-68 (equal values leave no deviation, and no eps that has a square)
+            const float e = fmaxf(sqrtf(eps) * 0x1p-68f, 0x1p-126f), q = fmaf(sq / C, 0x1p24f, e * e);
+            r = 0x1p-64f / (q == 0.0f ? e : sqrtf(q));
+        } else {
+            r = 1.0f / sqrtf(sq / C + eps);
+        }
+    }
+    __device__ float of(float x) const { return fmaf(x, k, -mu) * r; }
+    __device__ float2 as_stored() const { return float2{mu / k, r * k}; }
+};
+// xh in the backward, by halves: the difference of any two numbers fits
+struct Hat {
+    float mu, r;   // -mu / 2, 2 r
+    __device__ Hat(float2 stats) : mu(-0.5f * stats.x), r(2.0f * stats.y) {}
+    __device__ float of(float x) const { return fmaf(x, 0.5f, mu) * r; }
+};
+
 constexpr int kMaxWaves = 16;
 constexpr int kTogether = 8;   // waves of a backward workgroup that has several rows
+
+// The far rows of a wave, after the others: once more, from what is stored of them (a row's S by all its
+// waves, before they met).  Each wave takes the sums over all columns, and writes its own columns again.
+template <int XD, int YD, int CV, bool NARROW>
+__device__ void norm_far_rows(const FwdArgs &a, const Lanes<NARROW> &l) {
+    const void *src = a.A ? a.S : a.X;
+    const int64_t ld = a.A ? a.lds : a.ldx, step = (int64_t)gridDim.x * l.R;
+    const int lane = l.tid & (l.P - 1);
+    for (int64_t t0 = (int64_t)blockIdx.x * l.R; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + l.slot;
+        const bool here = t < a.T;
+        auto sum = [&](auto of) {
+            float s = 0.0f;
+            for (int c = lane * 8; here && c < a.C; c += l.P * 8) {
+                float x[8];
+                get8<XD>(src, t, ld, c, x);
+#pragma unroll
+                for (int j = 0; j < 8; j++) s += of(x[j] * kFar);
+            }
+            return lanes_all<Add>(s, l.P);
+        };
+        const float all = sum([](float x) { return x; }), mu = all / (float)a.C;
+        const float sq = sum([&](float x) { return (x - mu) * (x - mu); });
+        if (!here || (sq < kFarSquares && fabsf(all) < kFarSum)) continue;
+        const RowStats st(mu, sq, (float)a.C, a.eps, true);
+#pragma unroll 1
+        for (int v = 0; v < CV; v++) {
+            int c = l.col(v);
+            asm volatile("" : "+v"(c));   // (w and b are loaded again, not kept from the rows before)
+            if (c >= a.C) continue;
+            float x[8], w[8], b[8];
+            get8<XD>(src, t, ld, c, x);
+            coef8(a.w, c, 1.0f, w);
+            coef8(a.b, c, 0.0f, b);
+#pragma unroll
+            for (int j = 0; j < 8; j++) x[j] = fmaf(st.of(x[j]), w[j], b[j]);
+            put8<YD>(a.Y, t, a.ldy, c, x);
+        }
+        if (a.stats && l.tid == 0) *(float2 *)(a.stats + 2 * t) = st.as_stored();
+    }
+}
 
 // Rows in registers.  A workgroup goes on to further rows, with w and b in
 // registers and, where they leave room (CV 1), the next rows' loads under way.  Each
@@ -149,6 +220,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a
     const float n = l.template columns<CV>(l.wave, a.C);
     if (CV == 1) fetch((int64_t)blockIdx.x * l.R + l.slot);
     int turn = 0;
+    uint64_t far = 0;   // (told, not taken here: a branch in this loop costs 2 to 6 per cent)
     for (int64_t t0 = (int64_t)blockIdx.x * l.R; t0 < a.T; t0 += step, turn ^= 1) {
         const int64_t t = t0 + l.slot;
         const bool here = t < a.T;
@@ -188,6 +260,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a
                 sq += fmaf(l.template columns<CV>(i, a.C) * d, d, of[i].y);
             }
         }
+        far |= __ballot(!(sq < kInf));
         const float r = 1.0f / sqrtf(sq / (float)a.C + a.eps);
 #pragma unroll
         for (int v = 0; v < CV; v++)
@@ -198,6 +271,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_rows_kernel(FwdArgs a
             }
         if (a.stats && here && l.tid == 0) *(float2 *)(a.stats + 2 * t) = float2{mu, r};
     }
+    if (far) norm_far_rows<XD, YD, CV, NARROW>(a, l);
 }
 
 // Rows of any length: a workgroup a row, which it reads three times.
@@ -205,7 +279,7 @@ template <int XD, int YD>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(FwdArgs a) {
     __shared__ float sh[2][4];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float sum = 0.0f, sq = 0.0f;
+        float sum = 0.0f;
         for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
             float x[8];
             get8<XD>(a.X, t, a.ldx, c, x);
@@ -221,24 +295,44 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(FwdArgs a) {
         }
         const void *src = a.A ? a.S : a.X;   // each lane reads what it wrote
         const int64_t ld = a.A ? a.lds : a.ldx;
-        const float mu = group_all<Add, 4>(sum, sh[0]) / (float)a.C;
-        for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
-            float x[8];
-            get8<XD>(src, t, ld, c, x);
+        float mu = group_all<Add, 4>(sum, sh[0]) / (float)a.C;
+        auto squares = [&](float k) {   // of the values times k
+            float s = 0.0f;
+            for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
+                float x[8];
+                get8<XD>(src, t, ld, c, x);
 #pragma unroll
-            for (int j = 0; j < 8; j++) sq = fmaf(x[j] - mu, x[j] - mu, sq);
+                for (int j = 0; j < 8; j++) {
+                    const float d = fmaf(x[j], k, -mu);
+                    s = fmaf(d, d, s);
+                }
+            }
+            return group_all<Add, 4>(s, sh[1]);
+        };
+        float sq = squares(1.0f);
+        const bool far = !(sq < kInf);   // (the same in all lanes)
+        if (far) {
+            sum = 0.0f;
+            for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
+                float x[8];
+                get8<XD>(src, t, ld, c, x);
+#pragma unroll
+                for (int j = 0; j < 8; j++) sum = fmaf(x[j], kFar, sum);
+            }
+            mu = group_all<Add, 4>(sum, sh[0]) / (float)a.C;
+            sq = squares(kFar);
         }
-        const float r = 1.0f / sqrtf(group_all<Add, 4>(sq, sh[1]) / (float)a.C + a.eps);
+        const RowStats st(mu, sq, (float)a.C, a.eps, far);
         for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
             float x[8], w[8], b[8];
             get8<XD>(src, t, ld, c, x);
             coef8(a.w, c, 1.0f, w);
             coef8(a.b, c, 0.0f, b);
 #pragma unroll
-            for (int j = 0; j < 8; j++) x[j] = fmaf((x[j] - mu) * r, w[j], b[j]);
+            for (int j = 0; j < 8; j++) x[j] = fmaf(st.of(x[j]), w[j], b[j]);
             put8<YD>(a.Y, t, a.ldy, c, x);
         }
-        if (a.stats && threadIdx.x == 0) *(float2 *)(a.stats + 2 * t) = float2{mu, r};
+        if (a.stats && threadIdx.x == 0) *(float2 *)(a.stats + 2 * t) = st.as_stored();
         __syncthreads();
     }
 }
@@ -278,7 +372,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a
         const bool here = t < a.T;
         if (CV > 1) fetch(t);
         float xh[CV][8], g[CV][8], s1 = 0.0f, s2 = 0.0f;
-        const float mu = ns.x, r = ns.y;
+        const Hat hat(ns);
         Raw8<DX> d[CV];
 #pragma unroll
         for (int v = 0; v < CV; v++)
@@ -288,7 +382,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a
                 d[v] = nd[v];
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    xh[v][j] = (xh[v][j] - mu) * r;
+                    xh[v][j] = hat.of(xh[v][j]);
                     dw[v][j] = fmaf(g[v][j], xh[v][j], dw[v][j]);
                     db[v][j] += g[v][j];
                     g[v][j] *= w[v][j];
@@ -296,7 +390,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a
                     s2 = fmaf(g[v][j], xh[v][j], s2);
                 }
             }
-        if (CV == 1) fetch(t + step);
+        if (CV == 1) {
+            fetch(t + step);
+        } else {   // nothing is kept for a turn without a row: up to 34 registers (4096 x 16384 bf16 177 us, 136 without)
+            ns = float2{};
+#pragma unroll
+            for (int v = 0; v < CV; v++) nx[v] = Raw8<SD>{}, ny[v] = Raw8<DY>{};
+        }
         s1 = lanes_all<Add>(s1, l.P);
         s2 = lanes_all<Add>(s2, l.P);
         if (!NARROW && l.W > 1) {
@@ -306,14 +406,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_rows_kernel(BwdArgs a
             s1 = s2 = 0.0f;
             for (int i = 0; i < l.W; i++) s1 += of[i].x, s2 += of[i].y;
         }
-        const float m1 = s1 / (float)a.C, m2 = s2 / (float)a.C;
+        const float m1 = 0.5f * (s1 / (float)a.C), m2 = 0.5f * (s2 / (float)a.C);   // (halves, for 2 r)
 #pragma unroll
         for (int v = 0; v < CV; v++)
             if (here && l.col(v) < a.C) {
                 float o[8] = {};
                 if (a.dS) unpack8<DX>(d[v], o);
 #pragma unroll
-                for (int j = 0; j < 8; j++) o[j] = fmaf(r, fmaf(-xh[v][j], m2, g[v][j] - m1), o[j]);
+                for (int j = 0; j < 8; j++)
+                    o[j] = fmaf(hat.r, fmaf(-xh[v][j], m2, fmaf(g[v][j], 0.5f, -m1)), o[j]);
                 store8<DX>((char *)a.dX + (t * a.lddx + l.col(v)) * esize<DX>(), pack8<DX>(o));
             }
     }
@@ -353,6 +454,7 @@ __global__ __launch_bounds__(256) void norm_dx_kernel(BwdArgs a) {
     __shared__ float sh[2][4];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const float2 st = *(const float2 *)(a.stats + 2 * t);
+        const Hat hat(st);
         float s1 = 0.0f, s2 = 0.0f;
         for (int c = threadIdx.x * 8; c < a.C; c += 2048) {
             float x[8], g[8], w[8];
@@ -362,7 +464,7 @@ __global__ __launch_bounds__(256) void norm_dx_kernel(BwdArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 s1 = fmaf(g[j], w[j], s1);
-                s2 = fmaf(g[j] * w[j], (x[j] - st.x) * st.y, s2);
+                s2 = fmaf(g[j] * w[j], hat.of(x[j]), s2);
             }
         }
         const float m1 = group_all<Add, 4>(s1, sh[0]) / (float)a.C, m2 = group_all<Add, 4>(s2, sh[1]) / (float)a.C;
@@ -374,7 +476,7 @@ __global__ __launch_bounds__(256) void norm_dx_kernel(BwdArgs a) {
             if (a.dS) get8<DX>(a.dS, t, a.ldds, c, d);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const float xh = (x[j] - st.x) * st.y;
+                const float xh = hat.of(x[j]);
                 d[j] = fmaf(st.y, fmaf(g[j], w[j], -m1) - xh * m2, d[j]);
             }
             put8<DX>(a.dX, t, a.lddx, c, d);
@@ -391,10 +493,10 @@ __global__ __launch_bounds__(64) void norm_dw_kernel(BwdArgs a) {
     for (int64_t g = blockIdx.y; g < a.groups; g += gridDim.y) {
         float dw = 0.0f, db = 0.0f;
         for (int64_t t = g; t < a.T; t += a.groups) {
-            const float2 st = *(const float2 *)(a.stats + 2 * t);
+            const Hat hat(*(const float2 *)(a.stats + 2 * t));
             const float x = load1<SD>((const char *)a.S + (t * a.lds + c) * esize<SD>());
             const float d = load1<DY>((const char *)a.dY + (t * a.lddy + c) * esize<DY>());
-            dw = fmaf(d, (x - st.x) * st.y, dw);
+            dw = fmaf(d, hat.of(x), dw);
             db += d;
         }
         a.part[(g * 2) * a.C + c] = dw;

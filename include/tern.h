@@ -648,6 +648,7 @@ int tern_norm_bwd(const void *S, int64_t lds, int32_t s_dtype, const float *stat
  * Int64 arrays are 8-byte aligned, fp32 arrays of this call and of tern_distill 4-byte.
  * A logit of -inf is a token that is not allowed: p = 0, log p = -inf.  In a row
  * where nothing is allowed lse and every log probability are -inf, the entropy 0.
+ * Other logits may be any finite numbers, their differences beyond fp32's range too.
  * A row that holds a NaN or +inf gets NaN, and top_ids in [0, V); other rows are
  * not touched by it.  Sums are fp32 in a fixed order: repeated calls are bitwise identical.
  * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.
@@ -688,7 +689,8 @@ int tern_logprob(const void *Z, int64_t ld, int32_t z_dtype, float scale, int64_
  *   workspace  at least tern_distill_workspace_bytes(T, V) bytes (NULL when that is 0).
  *            Calls that may run at the same time need one each.
  * A logit of -inf has q = 0; a teacher's token with q = 0 makes the loss +inf.  A row
- * of nothing but -inf has q = 0 everywhere.  A row that holds a NaN or +inf gets NaN.
+ * of nothing but -inf has q = 0 everywhere.  A loss beyond fp32's range is infinite,
+ * whatever is beyond it on the way there is not.  A row that holds a NaN or +inf gets NaN.
  * Sums are fp32 in a fixed order: repeated calls are bitwise identical (a call
  * without dZ may sum in another order than one with).
  * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, ALIAS, HIP.

@@ -44,6 +44,7 @@ struct DistillArgs {
     const float *lp, *dloss;
     float alpha, tau;
     float c1, ct;             // log2 e, log2 e / tau
+    float unit, rest;         // tau = 2 unit rest: unit a power of two, rest from 1 to 2
     bool ce, kl;              // which parts the call has
     float *loss;
     void *dZ;
@@ -164,9 +165,9 @@ __device__ inline void sums_of(const char *z, const Raw8<DT> (&x)[NV], int n, co
         st *= exp2_(-e.t.off);
     } else {
         for (int v = fresh(tid); v < n; v += W * 64) {
-            const float d = at<DT>(z, v) - e.m0;
-            st += exp2_(d * e.t.c);
-            s1 += exp2_(d * e.one.c);
+            const float f = at<DT>(z, v);
+            st += exp2_(apart(f, e.m0, e.t.c));
+            s1 += exp2_(apart(f, e.m0, e.one.c));
         }
     }
 }
@@ -175,17 +176,19 @@ struct Sums {
     float m0, s1, st;
 };
 
-// the loss of a row, by its first wave
+// The loss of a row, by its first wave.  The KL is summed in units of 1 / unit, about tau / 2: neither it nor
+// tau^2 alone has to fit fp32, but tau times a difference of logits.
 __device__ inline void write_loss(const DistillArgs &a, int64_t t, const Names &e, const Sums &s, int lane) {
     float k = 0.0f;
     const float p = e.p[lane];
     if (e.id[lane] >= 0 && p != 0.0f)
-        k = s.st == 0.0f ? kInf : p * (e.logp[lane] - (e.z[lane] - s.m0) / a.tau + logf(s.st));
+        k = s.st == 0.0f ? kInf : p * fmaf(logf(s.st), a.unit, fmaf(e.logp[lane], a.unit, -half_apart(e.z[lane], s.m0) / a.rest));
     k = wave_all<Add>(k);
     if (lane != 0) return;
     float loss = 0.0f;
-    if (e.ce) loss += a.alpha * (s.s1 == 0.0f ? kInf : logf(s.s1) - (e.z[kEntries - 1] - s.m0));
-    if (e.kl) loss += (1.0f - a.alpha) * a.tau * a.tau * k;
+    if (e.ce)
+        loss = s.s1 == 0.0f ? kInf : 2.0f * (a.alpha * fmaf(logf(s.s1), 0.5f, -half_apart(e.z[kEntries - 1], s.m0)));
+    if (e.kl) loss = fmaf((1.0f - a.alpha) * a.tau * (2.0f * a.rest), k, loss);
     a.loss[t] = loss;
 }
 
@@ -208,9 +211,9 @@ __device__ inline void write_grad(const DistillArgs &a, int64_t t, const char *z
             for (int v = v0; v < min(v0 + 8, n); v++) {
                 float g = 0.0f;
                 if (!zero) {
-                    const float d = at<DT>(z, v) - s.m0;
-                    g = ft * exp2_(d * c);
-                    if (kind != kOne) g = fmaf(f1, exp2_(d * a.c1), g);
+                    const float f = at<DT>(z, v);
+                    g = ft * exp2_(apart(f, s.m0, c));
+                    if (kind != kOne) g = fmaf(f1, exp2_(apart(f, s.m0, a.c1)), g);
                 }
                 store1<DT>(dz + (int64_t)v * ES, g);
             }
@@ -253,9 +256,8 @@ __device__ inline void write_grad(const DistillArgs &a, int64_t t, const char *z
         const int j = r == 0 ? lane : kEntries - 1;
         const int v = e.id[j] - first;
         if ((r == 1 && lane != 0) || e.id[j] < 0 || v < 0 || v >= n || (v / 512) % W != wave) continue;
-        const float d = e.z[j] - s.m0;
-        float g = ft * exp2_(d * c);
-        if (kind != kOne) g = fmaf(f1, exp2_(d * a.c1), g);
+        float g = ft * exp2_(apart(e.z[j], s.m0, c));
+        if (kind != kOne) g = fmaf(f1, exp2_(apart(e.z[j], s.m0, a.c1)), g);
         store1<DT>(dz + (int64_t)v * ES, fmaf(-w, e.less[j], g));
     }
 }
@@ -266,8 +268,8 @@ __device__ inline Sums join_sums(const DistillArgs &a, int64_t t, float c, Kind 
     const float m = wave_all<Max>(r.x);
     Sums q;
     q.m0 = m == -kInf ? 0.0f : m;
-    q.st = at_least_one(wave_all<Add>(r.z * exp2_((r.x - q.m0) * c)));
-    q.s1 = kind == kOne ? q.st : at_least_one(wave_all<Add>(r.y * exp2_((r.x - q.m0) * a.c1)));
+    q.st = at_least_one(wave_all<Add>(r.z * exp2_(apart(r.x, q.m0, c))));
+    q.s1 = kind == kOne ? q.st : at_least_one(wave_all<Add>(r.y * exp2_(apart(r.x, q.m0, a.c1))));
     return q;
 }
 
@@ -336,9 +338,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void distill_kernel(Disti
                 float m, p1, pt;
                 largest_and_sums(z, n, m, p1, pt);
                 // to the larger of the two largest
-                const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both, d0 = M - b0, d1 = m - b0;
-                st = fmaf(exp2_(d0 * c), st, exp2_(d1 * c) * pt);
-                if (kind != kOne) s1 = fmaf(exp2_(d0 * a.c1), s1, exp2_(d1 * a.c1) * p1);
+                const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both;
+                st = fmaf(exp2_(apart(M, b0, c)), st, exp2_(apart(m, b0, c)) * pt);
+                if (kind != kOne) s1 = fmaf(exp2_(apart(M, b0, a.c1)), s1, exp2_(apart(m, b0, a.c1)) * p1);
                 M = both;
                 meet<W>();
             }
@@ -453,8 +455,10 @@ int tern_distill(const void *Z, int64_t ld, int32_t z_dtype, int64_t T, int64_t 
     const Mat ins[] = {vec(targets, T, 8), vec(teacher_ids, T * K, 8), vec(teacher_logp, T * K, 4), vec(dloss, T, 4),
                        {in_place ? nullptr : Z, T, V, ld, es}};
     if (any_overlap(outs, 3, ins, 5)) return TERN_ERR_ALIAS;
+    int exponent;
+    const float rest = 2.0f * std::frexp(tau, &exponent);
     DistillArgs a{Z, ld, lddz, T, (int)V, K, p.S, (int)p.part, (int)p.seg, targets, teacher_ids, teacher_logp, dloss, alpha, tau,
-                  (float)rows::kLog2e, (float)(rows::kLog2e / tau), alpha > 0.0f && targets, alpha < 1.0f && K > 0, loss,
+                  (float)rows::kLog2e, (float)(rows::kLog2e / tau), std::ldexp(1.0f, exponent - 2), rest, alpha > 0.0f && targets, alpha < 1.0f && K > 0, loss,
                   dZ, (float4 *)workspace, nullptr};
     if (p.S > 1) a.named = (float *)(a.sums + T * p.S);
     hipStream_t st = (hipStream_t)stream;

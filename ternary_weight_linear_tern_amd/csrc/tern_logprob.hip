@@ -317,7 +317,7 @@ __device__ inline int top_of_segment(const Raw8<DT> (&x)[NV], int n, uint32_t fi
 // what a row's sums say
 struct RowEnd {
     float m0, s, logs, scale;
-    __device__ float log_p(float z) const { return s == 0.0f ? -kInf : (z - m0) * scale - logs; }
+    __device__ float log_p(float z) const { return s == 0.0f ? -kInf : 2.0f * fmaf(half_apart(z, m0), scale, -0.5f * logs); }
 };
 __device__ inline RowEnd finish_row(const LogprobArgs &a, int64_t t, float m0, float s, float u, int tid) {
     s = at_least_one(s);
@@ -366,7 +366,7 @@ __device__ inline void lane_sums(const char *z, const Raw8<DT> (&x)[NV], int n, 
             for (int j = 0; j < 8; j++) add(e.of(f[j]));
         });
     } else {
-        for (int v = fresh(tid); v < n; v += W * 64) add((at<DT>(z, v) - m0) * e.c);
+        for (int v = fresh(tid); v < n; v += W * 64) add(apart(at<DT>(z, v), m0, e.c));
     }
 }
 
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
             }
             // to the larger of the two largest
             const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both;
-            const float d0 = (M - b0) * a.c, d1 = (m - b0) * a.c, f0 = exp2_(d0), f1 = exp2_(d1);
+            const float d0 = apart(M, b0, a.c), d1 = apart(m, b0, a.c), f0 = exp2_(d0), f1 = exp2_(d1);
             u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
             s = f0 * s + f1 * s1;
             M = both;
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
         const Token y = token_of<DT>(a, t, tid);
         float4 q = lane < a.S ? a.sums[t * a.S + lane] : float4{-kInf, 0.0f, 0.0f, 0.0f};
         const float m = wave_all<Max>(q.x), m0 = m == -kInf ? 0.0f : m;
-        const float d = (q.x - m0) * a.c, f = exp2_(d);
+        const float d = apart(q.x, m0, a.c), f = exp2_(d);
         const float s = wave_all<Add>(f * q.y), u = wave_all<Add>(f * fmaf(q.y, fmaxf(d, -200.0f), q.z));
         const RowEnd r = finish_row(a, t, m0, s, u, tid);
         tell_token(a, t, r, y, tid);

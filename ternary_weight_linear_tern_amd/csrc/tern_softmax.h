@@ -197,6 +197,10 @@ struct Exponent {
     __device__ float of(float z) const { return fmaf(z, c, -mc); }
 };
 
+// z - m by halves (half of it), and its product with a factor: the difference of any two numbers fits.
+__device__ inline float half_apart(float z, float m) { return fmaf(z, 0.5f, -0.5f * m); }
+__device__ inline float apart(float z, float m, float f) { return 2.0f * (half_apart(z, m) * f); }
+
 // A row's sum of exponentials, to which its largest element gives 1 (nothing allowed:
 // 0): a rounding below that would make a probability above 1.
 __device__ inline float at_least_one(float s) { return s > 0.0f && s < 1.0f ? 1.0f : s; }

@@ -206,17 +206,25 @@ __device__ inline void write_grad(const DistillArgs &a, int64_t t, const char *z
     const int full = n & ~7, l = fresh(tid);
     const Exponents x2(s.m0, c, a.c1, kind);
     if (zero || x2.far) {
-        // element by element, in the places of the pass below (a row of zeros takes nothing from Z)
-        for (int v0 = l * 8; v0 < n; v0 += ST)
-            for (int v = v0; v < min(v0 + 8, n); v++) {
-                float g = 0.0f;
-                if (!zero) {
-                    const float f = at<DT>(z, v);
-                    g = ft * exp2_(apart(f, s.m0, c));
-                    if (kind != kOne) g = fmaf(f1, exp2_(apart(f, s.m0, a.c1)), g);
-                }
-                store1<DT>(dz + (int64_t)v * ES, g);
+        // element by element, in the places of the pass below (a row of zeros takes nothing from Z), written in
+        // eights (no row of 8192 x 65536 bf16 with a weight: 405 us, element by element 738)
+        for (int v = l * 8; v < n; v += ST) {
+            float g[8] = {};
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if (zero || v + j >= n) continue;
+                const float f = at<DT>(z, v + j);
+                g[j] = ft * exp2_(apart(f, s.m0, c));
+                if (kind != kOne) g[j] = fmaf(f1, exp2_(apart(f, s.m0, a.c1)), g[j]);
             }
+            if (v < full) {
+                store8<DT>(dz + (int64_t)v * ES, pack8<DT>(g));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 7; j++)
+                    if (v + j < n) store1<DT>(dz + (int64_t)(v + j) * ES, g[j]);
+            }
+        }
         if (zero) return;
     } else {
         // the factors take off what the exponents are too large by

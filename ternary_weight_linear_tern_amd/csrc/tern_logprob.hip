@@ -400,11 +400,15 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, 4) void logprob_kernel(Logpr
                 u1 = fmaf(-e.off, s1, u1) * f;
                 s1 *= f;
             }
-            // to the larger of the two largest
-            const float both = fmaxf(M, m), b0 = both == -kInf ? 0.0f : both;
-            const float d0 = apart(M, b0, a.c), d1 = apart(m, b0, a.c), f0 = exp2_(d0), f1 = exp2_(d1);
-            u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
-            s = f0 * s + f1 * s1;
+            const float both = fmaxf(M, m);
+            if (first == begin) {
+                s = s1, u = u1;
+            } else {   // to the larger of the two largest
+                const float b0 = both == -kInf ? 0.0f : both;
+                const float d0 = apart(M, b0, a.c), d1 = apart(m, b0, a.c), f0 = exp2_(d0), f1 = exp2_(d1);
+                u = f0 * fmaf(s, fmaxf(d0, -200.0f), u) + f1 * fmaf(s1, fmaxf(d1, -200.0f), u1);
+                s = f0 * s + f1 * s1;
+            }
             M = both;
             if (a.k == 1) had = first_of_segment<DT, W, NV>(x, n, first, had, mine, m, pick, tid);
             else if (a.k) had = top_of_segment<DT, W, NV>(x, n, first, a.k, had, mine, pick, tid);

@@ -76,3 +76,22 @@ def test_backward(C, dt):
     ref.assert_within(dX, want, e + ref.half_step(F32) * (want.abs() + e), f"{C} {dt} dX")
     ref.assert_within(dw, gw, ew, f"{C} {dt} dw")
     ref.assert_within(db, gb, eb, f"{C} {dt} db")
+
+
+@pytest.mark.parametrize("T,C", [(70001, 64), (35001, 200), (9001, 512), (5003, 1024), (4500, 2048), (2100, 12000)])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_many_rows_in_place(T, C, dt):
+    """Far rows in any turn of a workgroup, the stream updated in place."""
+    X, A, w, b = rand((T, C), 1, dt, 2.0, 0.5), rand((T, C), 2, BF), rand((C,), 3, shift=1.0), rand((C,), 4)
+    far = far_rows(C, dt)
+    for i in range(far.shape[0]):
+        X[(i * 2741 + 5) % T] = far[i]
+    X[T - 1], X[T - 2] = far[1], far[4]
+    S = (X.float() + A.float()).to(dt)
+    Y, st = torch.empty(T, C, device="cuda"), tl.empty_norm_stats(T)
+    tl.tern_norm_fwd(X, Y, w=w, b=b, A=A, S=X, stats=st)
+    assert torch.equal(X, S)
+    want, mu, r, e, emu, er = ref.norm_fwd(S, w, b, 1e-5)
+    ref.assert_within(st[:, :1], mu, emu, f"{T} x {C} {dt} mu")
+    ref.assert_within(st[:, 1:], r, er + 2.0 ** -149, f"{T} x {C} {dt} r")
+    ref.assert_within(Y, want, e + ref.half_step(F32) * (want.abs() + e), f"{T} x {C} {dt} Y")

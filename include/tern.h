@@ -588,7 +588,8 @@ int tern_layer_orthogonalize(const tern_ortho_t *mats, int32_t n, int32_t g_dtyp
  *            the norm is that of S as stored, so that the backward, which reads S,
  *            sees the same numbers.  S may be X (the stream is then updated in
  *            place).  Both NULL: the norm of X.
- *   w, b     fp32 [C], or NULL (ones, zeros).
+ *   w, b     fp32 [C], or NULL (ones, zeros); the same for every row: a norm over heads
+ *            (a row each) has weights of its own for a head only in a call of its own.
  *   eps      above 0 and finite (TERN_ERR_VALUE).
  *   Y        [T, C] of y_dtype (either type), stride ldy, rounded once.
  *   stats    fp32 [T, 2], 8-byte aligned: mu and r of each row, which the backward

@@ -17,10 +17,10 @@
 // may overwrite; then the loss and the gradient, which reads the parts again.
 //
 // 8192 rows of 65536 bf16 logits, tau 2, loss and gradient: 413 to 440 us by the card, 4.9 to
-// 5.2 TB/s; at tau 1.5, with two exponentials, 488.  Two workgroups of eight waves share a
+// 5.2 TB/s; at tau 1.5, with two exponentials, 445 to 488.  Two workgroups of eight waves share a
 // compute unit and load and compute in turn; rows of 131072 fill it alone and are not
-// hidden (4096 of them 521 us, 4.1 TB/s).  fp32 rows of more than 65536 are read twice (2048
-// of 131072: 646 us where one pass would take 440).  The loss alone: 1021 rows of 50021 23 us.
+// hidden (4096 of them 505 us, 4.3 TB/s).  fp32 rows of more than 65536 are read twice (2048
+// of 131072: 590 to 646 us where one pass would take 440).  The loss alone: 1021 rows of 50021 23 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

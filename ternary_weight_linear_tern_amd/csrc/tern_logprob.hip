@@ -20,10 +20,10 @@
 // other (the sums rescaled, the alternatives so far a bound for the next); where
 // the rows are few, by workgroups that a second launch joins.
 //
-// 4096 rows of 131072 bf16 logits: 211 us without alternatives (5.1 TB/s: HBM bounds
-// it), 229 with 20, 237 to 258 with 64 (the search among the lanes' largest, and one
+// 4096 rows of 131072 bf16 logits: 196 us without alternatives (5.5 TB/s: HBM bounds
+// it), 221 with 20, 244 with 64 (the search among the lanes' largest, and one
 // more look at the registers, about as long as a third of the sums).  (Every alternative
-// by a maximum over the row: 43 ms.)  13 rows of 50021 in fp32, 20 alternatives: 11.8 us in
+// by a maximum over the row: 43 ms.)  13 rows of 50021 in fp32, 20 alternatives: 12.5 us in
 // two launches; 2048 rows of 256, the largest alone, 4.0.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -10,7 +10,7 @@
 // So rows of up to 16384 columns stay in registers between their sums and their
 // results, the backward sums dw and db from the same registers, and the next rows are
 // loaded meanwhile.  Forward, 16384 x 2048, fp32 + fp32 to fp32 and bf16: 91 us, 5.1 TB/s;
-// backward, 32768 x 4096, bf16 with fp32 dY, dS and dX: 357 us, 5.3 TB/s, of which 14 are the
+// backward, 32768 x 4096, bf16 with fp32 dY, dS and dX: 357 us, 5.3 TB/s, of which 5 are the
 // second launch, which adds up the groups' dw and db.  (Three passes over each row, and
 // dw and db from passes of their own: 109 and 721.)  Few rows are bound by the launches:
 // 32 x 2048 forward 3.4 us, 2048 x 512 backward 7.
@@ -87,8 +87,8 @@ struct RawA {
 
 // How a workgroup takes rows of up to 16 * 512 * CV columns: W waves a row, eight
 // neighbours a lane, CV times; rows of 256 columns and fewer take P = 8, 16 or 32
-// lanes of one wave (65536 rows of 64 forward: 27.7 us with a wave
-// each, 7.5 with 8 lanes).  R rows at once.
+// lanes of one wave (65536 rows of 64 in bf16: forward 30.6 us with a
+// wave each, 10.0 with 8 lanes; backward 30.7 and 16.0).  R rows at once.
 // (P is a variable in kernels of their own: that costs the others some per cent.)
 template <bool NARROW>
 struct Lanes {
@@ -561,7 +561,8 @@ int rows_at_once(const RowShape &s, int waves) { return std::max(1, waves / std:
 // With few long rows the groups' sums are as large as the rows: a group that takes
 // `turns` times its rows costs about 2 us a turn and saves 16 C bytes of sums, written and
 // read, so that their total is least at turns^2 = 16 C T / (R 4.9 TB/s 2 us).  (bf16, 300
-// rows of 16384: 32 us with a group each, 26 with this; 1000 rows 57 and 49.)
+// rows of 16384: 29 us with a group each, 23 with this; 1000 rows 44 and 36.  4096 rows are taken by 410
+// groups, of which a unit holds one: 136 us, and 131 with 512.)
 int64_t groups_of(int64_t T, int64_t C) {
     const int64_t R = rows_at_once(shape_of(C), ldev::kTogether);
     const int64_t turns = std::max<int64_t>(1, (int64_t)std::sqrt(1.6e-6 * (double)T * (double)C / (double)R));
